@@ -34,7 +34,11 @@ EXPORTS = ("lz_gla_fwd", "lz_gla_bwd", "lz_swa_meta_fwd", "lz_hybrid_fwd", "lz_s
            "lz_version", "lz_timing_enable", "lz_timing_only", "lz_timing_read",
            "lz_swa_meta_bwd_noalloc", "lz_device_check", "lz_prefer_tcgen05", "lz_decode_prefill",
            "lz_hybrid_fwd_mse", "lz_selftest_bounded_wait", "lz_cp_segment_decay", "lz_cp_fold",
-           "lz_cp_rows", "lz_tcgen05_all", "lz_qkg_projection", "lz_fused_gate_logits")
+           "lz_cp_rows", "lz_tcgen05_all", "lz_qkg_projection", "lz_fused_gate_logits",
+           "lz_conv_fwd", "lz_conv_bwd", "lz_conv_step", "lz_scan_fwd", "lz_scan_bwd",
+           "lz_scan_step", "lz_block_norm_fwd", "lz_block_norm_bwd", "lz_layer_workspace_bytes")
+
+LZ_WS_CONV_BWD, LZ_WS_SCAN_FWD, LZ_WS_SCAN_BWD, LZ_WS_SCAN_STATES, LZ_WS_NORM_BWD = range(16, 21)
 
 # size of the static scratch array behind lz_swa_meta_bwd_noalloc
 LZ_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -52,6 +56,31 @@ class LzDims(ctypes.Structure):
                 ("w", ctypes.c_int), ("M", ctypes.c_int), ("io", ctypes.c_int),
                 ("scale", ctypes.c_float), ("alpha", ctypes.c_float),
                 ("gate_logits", ctypes.c_int), ("gate_scale", ctypes.c_float)]
+
+
+class LzRows(ctypes.Structure):
+    """Strides of a strided input's rows in elements: token to token, sequence
+    to sequence (ld = 0: contiguous)."""
+    _fields_ = [("ld", ctypes.c_int64), ("bs", ctypes.c_int64)]
+
+
+class LzConvDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("K", ctypes.c_int), ("io", ctypes.c_int), ("silu", ctypes.c_int),
+                ("x", LzRows)]
+
+
+class LzScanDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("G", ctypes.c_int), ("N", ctypes.c_int), ("io", ctypes.c_int),
+                ("softplus", ctypes.c_int), ("u", LzRows), ("dt", LzRows), ("z", LzRows),
+                ("b", LzRows), ("c", LzRows)]
+
+
+class LzNormDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("G", ctypes.c_int), ("heads", ctypes.c_int), ("io", ctypes.c_int),
+                ("eps", ctypes.c_float), ("o", LzRows), ("z", LzRows), ("r", LzRows)]
 
 
 _lib = None
@@ -93,6 +122,17 @@ def load(path: str = LIB_PATH):
     lib.lz_cp_fold.argtypes = [ci] * 6 + [_P] * 4 + [_P]
     lib.lz_cp_rows.argtypes = ([ci] * 4 + [_P, ci, ci, ctypes.c_float, _P, ci, ci, _P, ci, ci] +
                                [_P])
+    CD, SD, ND = (ctypes.POINTER(x) for x in (LzConvDims, LzScanDims, LzNormDims))
+    lib.lz_conv_fwd.argtypes = [CD] + [_P] * 7 + [_P]
+    lib.lz_conv_bwd.argtypes = [CD] + [_P] * 11 + [_P, sz, _P]
+    lib.lz_conv_step.argtypes = [CD] + [_P] * 5 + [_P]
+    lib.lz_scan_fwd.argtypes = [SD] + [_P] * 13 + [_P, sz, _P]
+    lib.lz_scan_bwd.argtypes = [SD] + [_P] * 22 + [_P, sz, _P]
+    lib.lz_scan_step.argtypes = [SD] + [_P] * 10 + [_P]
+    lib.lz_block_norm_fwd.argtypes = [ND] + [_P] * 8 + [_P]
+    lib.lz_block_norm_bwd.argtypes = [ND] + [_P] * 14 + [_P, sz, _P]
+    lib.lz_layer_workspace_bytes.argtypes = [_P, ctypes.c_int]
+    lib.lz_layer_workspace_bytes.restype = sz
     lib.lz_timing_enable.argtypes = [ctypes.c_int]
     lib.lz_timing_only.argtypes = [ctypes.c_char_p]
     lib.lz_timing_read.argtypes = [ctypes.c_char_p, sz, ctypes.POINTER(ctypes.c_float),
@@ -101,7 +141,7 @@ def load(path: str = LIB_PATH):
         if name in ("lz_last_error", "lz_version"):
             getattr(lib, name).restype = ctypes.c_char_p
             getattr(lib, name).argtypes = []
-        elif name != "lz_workspace_bytes":
+        elif name not in ("lz_workspace_bytes", "lz_layer_workspace_bytes"):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -542,3 +582,328 @@ def qkg_projection(x, Wq=None, Wk=None, Wg=None, *, heads, gate_scale=1.0, strea
     lz_qkg_projection(B, T, Dm, heads, dk, x, Wq, Wk, Wg, gate_scale, q, k, g, stream)
     return q, k, g
 
+
+
+# ---- layer operators: short convolution, selective scan, block norms --------
+def lz_layer_workspace_bytes(dims, which: int) -> int:
+    return int(load().lz_layer_workspace_bytes(ctypes.byref(dims), which))
+
+
+def lz_conv_fwd(dims, x, w, bias, x0, lens, y, xT, stream=None):
+    _check(load().lz_conv_fwd(ctypes.byref(dims), _ptr(x), _ptr(w), _ptr(bias), _ptr(x0),
+                              _ptr(lens), _ptr(y), _ptr(xT), _stream(stream)))
+
+
+def lz_conv_bwd(dims, x, w, bias, x0, lens, dy, dxT, dx, dw, dbias, dx0, ws, ws_bytes,
+                stream=None):
+    _check(load().lz_conv_bwd(ctypes.byref(dims), _ptr(x), _ptr(w), _ptr(bias), _ptr(x0),
+                              _ptr(lens), _ptr(dy), _ptr(dxT), _ptr(dx), _ptr(dw), _ptr(dbias),
+                              _ptr(dx0), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def lz_conv_step(dims, hist, x, w, bias, y, stream=None):
+    _check(load().lz_conv_step(ctypes.byref(dims), _ptr(hist), _ptr(x), _ptr(w), _ptr(bias),
+                               _ptr(y), _stream(stream)))
+
+
+def lz_scan_fwd(dims, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, y, hT, states, ws, ws_bytes,
+                stream=None):
+    _check(load().lz_scan_fwd(ctypes.byref(dims), _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm),
+                              _ptr(Dskip), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens), _ptr(y),
+                              _ptr(hT), _ptr(states), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def lz_scan_bwd(dims, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT, states, du, ddt, dA,
+                dB, dC, dDskip, ddt_bias, dz, dh0, ws, ws_bytes, stream=None):
+    _check(load().lz_scan_bwd(ctypes.byref(dims), _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm),
+                              _ptr(Dskip), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens),
+                              _ptr(dy), _ptr(dhT), _ptr(states), _ptr(du), _ptr(ddt), _ptr(dA),
+                              _ptr(dB), _ptr(dC), _ptr(dDskip), _ptr(ddt_bias), _ptr(dz),
+                              _ptr(dh0), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def lz_scan_step(dims, state, u, dt, A, Bm, Cm, Dskip, z, dt_bias, y, stream=None):
+    _check(load().lz_scan_step(ctypes.byref(dims), _ptr(state), _ptr(u), _ptr(dt), _ptr(A),
+                               _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z), _ptr(dt_bias), _ptr(y),
+                               _stream(stream)))
+
+
+def lz_block_norm_fwd(dims, o, w, z, s, r, w2, out, n, stream=None):
+    _check(load().lz_block_norm_fwd(ctypes.byref(dims), _ptr(o), _ptr(w), _ptr(z), _ptr(s),
+                                    _ptr(r), _ptr(w2), _ptr(out), _ptr(n), _stream(stream)))
+
+
+def lz_block_norm_bwd(dims, o, w, z, s, w2, out, dout, dn, dOo, dz, dr, dw, ds, dw2, ws, ws_bytes,
+                      stream=None):
+    _check(load().lz_block_norm_bwd(ctypes.byref(dims), _ptr(o), _ptr(w), _ptr(z), _ptr(s),
+                                    _ptr(w2), _ptr(out), _ptr(dout), _ptr(dn), _ptr(dOo),
+                                    _ptr(dz), _ptr(dr), _ptr(dw), _ptr(ds), _ptr(dw2), _ptr(ws),
+                                    ws_bytes, _stream(stream)))
+
+
+def _need(ok, fn, what):
+    if not ok:
+        raise ValueError(f"{fn}: {what}")
+
+
+def _whole(fn, shape, dtype, dev, **tensors):
+    """Contiguous tensors (or None) of one shape, dtype and device."""
+    for name, t in tensors.items():
+        if t is not None and not (t.shape == shape and t.dtype == dtype and t.device == dev
+                                  and t.is_contiguous()):
+            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape "
+                             f"{tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                             f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _rows(fn, name, t, shape, dtype, dev):
+    """Row strides of a strided input of `shape` ([B, T, ...] for prompts): the
+    axes behind the tokens must be contiguous."""
+    if t is None:
+        return LzRows(0, 0)
+    if not (t.shape == shape and t.dtype == dtype and t.device == dev):
+        raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return LzRows(0, 0)
+    width = 1
+    for n, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        if n > 1 and st != width:
+            raise ValueError(f"{fn}: {name}: only the batch and token axes may be strided")
+        width *= n
+    B, T = t.shape[:2]
+    ld = t.stride(1) if T > 1 else max(width, 1)
+    if ld < 1:
+        raise ValueError(f"{fn}: {name}: one token's row shared by all tokens is not supported")
+    return LzRows(ld, t.stride(0) if B > 1 else 0)
+
+
+def _step_rows(fn, name, t, shape, dtype, dev):
+    """The same for single tokens: [B, ...]."""
+    if t is None or (t.is_contiguous() and t.shape == shape and t.dtype == dtype
+                     and t.device == dev):
+        return LzRows(0, 0)
+    return _rows(fn, name, t.unsqueeze(1), (shape[0], 1) + tuple(shape[1:]), dtype, dev)
+
+
+def _on(dev, stream):
+    """The device guard and stream of a layer call: work goes to the tensors'
+    device, on its current stream unless one is given."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {dev}")
+    return torch.cuda.device(dev)
+
+
+def conv_fwd(x, w, bias=None, x0=None, *, silu=True, lens=None, want_xT=False, stream=None):
+    """Short causal convolution (see lz_conv_fwd): x [B, T, D] (rows may be
+    strided), w [D, K] and bias [D] fp32, x0 [B, K-1, D] the history in front,
+    lens an int64 tensor [B] of the sequences' lengths in a right-padded batch.
+    Returns (y, xT); xT (None unless wanted) is the history after the last
+    token, which conv_step or the next conv_fwd continues."""
+    fn, dev = "conv_fwd", x.device
+    _need(x.dim() == 3 and w.dim() == 2, fn, "x must be [B, T, D] and w [D, K]")
+    (B, T, D), K = x.shape, w.shape[1]
+    d = LzConvDims(B, T, D, K, io_of(x.dtype), int(bool(silu)),
+                   _rows(fn, "x", x, x.shape, x.dtype, dev))
+    _whole(fn, (D, K), torch.float32, dev, w=w)
+    _whole(fn, (D,), torch.float32, dev, bias=bias)
+    _whole(fn, (B, K - 1, D), x.dtype, dev, x0=x0)
+    _whole(fn, (B,), torch.int64, dev, lens=lens)
+    with _on(dev, stream):
+        y = torch.empty(B, T, D, dtype=x.dtype, device=dev)
+        xT = torch.empty(B, K - 1, D, dtype=x.dtype, device=dev) if want_xT else None
+        lz_conv_fwd(d, x, w, bias, x0, lens, y, xT, stream)
+    return y, xT
+
+
+def conv_bwd(x, w, dy, bias=None, x0=None, dxT=None, *, silu=True, lens=None, want_dx0=False,
+             stream=None):
+    """Gradients of conv_fwd: a dict of dx, dw, dbias (None without bias) and
+    dx0 (None unless wanted)."""
+    fn, dev = "conv_bwd", x.device
+    _need(x.dim() == 3 and w.dim() == 2, fn, "x must be [B, T, D] and w [D, K]")
+    (B, T, D), K = x.shape, w.shape[1]
+    d = LzConvDims(B, T, D, K, io_of(x.dtype), int(bool(silu)),
+                   _rows(fn, "x", x, x.shape, x.dtype, dev))
+    _whole(fn, (D, K), torch.float32, dev, w=w)
+    _whole(fn, (D,), torch.float32, dev, bias=bias)
+    _whole(fn, (B, T, D), x.dtype, dev, dy=dy)
+    _whole(fn, (B, K - 1, D), x.dtype, dev, x0=x0, dxT=dxT)
+    _whole(fn, (B,), torch.int64, dev, lens=lens)
+    with _on(dev, stream):
+        dx = torch.empty(B, T, D, dtype=x.dtype, device=dev)
+        dw = torch.empty(D, K, dtype=torch.float32, device=dev)
+        db = torch.empty(D, dtype=torch.float32, device=dev) if bias is not None else None
+        dx0 = torch.empty(B, K - 1, D, dtype=x.dtype, device=dev) if want_dx0 else None
+        n = lz_layer_workspace_bytes(d, LZ_WS_CONV_BWD)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        lz_conv_bwd(d, x, w, bias, x0, lens, dy, dxT, dx, dw, db, dx0, ws, n, stream)
+    return {"dx": dx, "dw": dw, "dbias": db, "dx0": dx0}
+
+
+def conv_step(hist, x, w, bias=None, *, silu=True, y=None, stream=None):
+    """One generation step: x [B, D], hist [B, K-1, D] (moves on in place);
+    returns y [B, D]."""
+    fn, dev = "conv_step", x.device
+    _need(x.dim() == 2 and w.dim() == 2, fn, "x must be [B, D] and w [D, K]")
+    (B, D), K = x.shape, w.shape[1]
+    d = LzConvDims(B, 1, D, K, io_of(x.dtype), int(bool(silu)),
+                   _step_rows(fn, "x", x, x.shape, x.dtype, dev))
+    _whole(fn, (D, K), torch.float32, dev, w=w)
+    _whole(fn, (D,), torch.float32, dev, bias=bias)
+    _whole(fn, (B, K - 1, D), x.dtype, dev, hist=hist)
+    _whole(fn, (B, D), x.dtype, dev, y=y)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(B, D, dtype=x.dtype, device=dev)
+        lz_conv_step(d, hist, x, w, bias, y, stream)
+    return y
+
+
+def _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, step=False):
+    """Checks a scan call's inputs; returns its dims."""
+    lead = 1 if step else 2
+    _need(u.dim() == lead + 1 and A.dim() == 2, fn, "u must be %s and A [D, N]"
+          % ("[B, D]" if step else "[B, T, D]"))
+    _need(Bm.dim() in (lead + 1, lead + 2), fn, "Bm must be [.., N] or [.., G, N]")
+    dev, dtype, D, N = u.device, u.dtype, u.shape[-1], A.shape[1]
+    G = Bm.shape[-2] if Bm.dim() == lead + 2 else 1
+    bc = tuple(u.shape[:lead]) + ((G, N) if Bm.dim() == lead + 2 else (N,))
+    rows = _step_rows if step else _rows
+    r = [rows(fn, n, t, u.shape, dtype, dev) for n, t in (("u", u), ("dt", dt), ("z", z))]
+    r += [rows(fn, n, t, bc, dtype, dev) for n, t in (("Bm", Bm), ("Cm", Cm))]
+    _whole(fn, (D, N), torch.float32, dev, A=A)
+    _whole(fn, (D,), torch.float32, dev, Dskip=Dskip, dt_bias=dt_bias)
+    T = 1 if step else u.shape[1]
+    return LzScanDims(u.shape[0], T, D, G, N, io_of(dtype), int(bool(softplus)), *r)
+
+
+def scan_fwd(u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, softplus=True, h0=None,
+             lens=None, want_hT=False, want_states=False, stream=None):
+    """Selective state space scan (see lz_scan_fwd): u, dt, z [B, T, D], A [D, N]
+    fp32 (negative), Bm, Cm [B, T, N] or [B, T, G, N] (rows may be strided),
+    Dskip, dt_bias [D] fp32, h0 [B, D, N] fp32, lens an int64 tensor [B] of the
+    sequences' lengths in a right-padded batch.  Returns (y, hT), or (y, hT,
+    states) with want_states; `states` is for scan_bwd."""
+    fn, dev = "scan_fwd", u.device
+    d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus)
+    B, T, D = u.shape
+    _whole(fn, (B, D, A.shape[1]), torch.float32, dev, h0=h0)
+    _whole(fn, (B,), torch.int64, dev, lens=lens)
+    with _on(dev, stream):
+        y = torch.empty(B, T, D, dtype=u.dtype, device=dev)
+        hT = torch.empty(B, D, A.shape[1], dtype=torch.float32, device=dev) if want_hT else None
+        st = None
+        if want_states:
+            st = torch.empty(lz_layer_workspace_bytes(d, LZ_WS_SCAN_STATES) // 4,
+                             dtype=torch.float32, device=dev)
+        n = lz_layer_workspace_bytes(d, LZ_WS_SCAN_FWD)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        lz_scan_fwd(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, y, hT, st, ws, n, stream)
+    return (y, hT, st) if want_states else (y, hT)
+
+
+def scan_bwd(u, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, dt_bias=None, softplus=True, h0=None,
+             lens=None, dhT=None, states=None, want_dh0=False, stream=None):
+    """Gradients of scan_fwd: a dict of du, ddt, dA, dB, dC, dDskip, ddt_bias and
+    dz (None for what was not given) and dh0 (None unless wanted).  states: the
+    forward's (optional; saves a walk over the sequence)."""
+    fn, dev = "scan_bwd", u.device
+    d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus)
+    B, T, D = u.shape
+    N = A.shape[1]
+    _whole(fn, (B, T, D), u.dtype, dev, dy=dy)
+    _whole(fn, (B, D, N), torch.float32, dev, h0=h0, dhT=dhT)
+    _whole(fn, (B,), torch.int64, dev, lens=lens)
+    if states is not None:
+        _whole(fn, (lz_layer_workspace_bytes(d, LZ_WS_SCAN_STATES) // 4,), torch.float32, dev,
+               states=states)
+    with _on(dev, stream):
+        f32 = dict(dtype=torch.float32, device=dev)
+        new = lambda: torch.empty(B, T, D, dtype=u.dtype, device=dev)
+        du, ddt, dz = new(), new(), new() if z is not None else None
+        dB, dC = (torch.empty(Bm.shape, dtype=u.dtype, device=dev) for _ in range(2))
+        dA = torch.empty(D, N, **f32)
+        dD = torch.empty(D, **f32) if Dskip is not None else None
+        db = torch.empty(D, **f32) if dt_bias is not None else None
+        dh0 = torch.empty(B, D, N, **f32) if want_dh0 else None
+        n = lz_layer_workspace_bytes(d, LZ_WS_SCAN_BWD)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        lz_scan_bwd(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT, states, du, ddt,
+                    dA, dB, dC, dD, db, dz, dh0, ws, n, stream)
+    return {"du": du, "ddt": ddt, "dA": dA, "dB": dB, "dC": dC, "dDskip": dD, "ddt_bias": db,
+            "dz": dz, "dh0": dh0}
+
+
+def scan_step(state, u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, softplus=True, y=None,
+              stream=None):
+    """One generation step: u, dt, z [B, D], Bm, Cm [B, N] or [B, G, N], state
+    [B, D, N] fp32 in place; returns y [B, D]."""
+    fn, dev = "scan_step", u.device
+    d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, step=True)
+    _whole(fn, (u.shape[0], u.shape[1], A.shape[1]), torch.float32, dev, state=state)
+    _whole(fn, u.shape, u.dtype, dev, y=y)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+        lz_scan_step(d, state, u, dt, A, Bm, Cm, Dskip, z, dt_bias, y, stream)
+    return y
+
+
+def _norm_args(fn, o, z, r, groups, eps):
+    _need(o.dim() in (3, 4), fn, "o must be [B, T, D] or [B, H, T, d]")
+    heads = o.dim() == 4
+    if heads:
+        B, H, T, dv = o.shape
+        _need(groups in (1, H), fn, f"groups is the number of heads ({H}) for [B, H, T, d]")
+        groups, D = H, H * dv
+    else:
+        B, T, D = o.shape
+    dev, dtype = o.device, o.dtype
+    if heads:
+        _whole(fn, o.shape, dtype, dev, o=o)
+    ro = LzRows(0, 0) if heads else _rows(fn, "o", o, o.shape, dtype, dev)
+    return LzNormDims(B, T, D, groups, int(heads), io_of(dtype), float(eps), ro,
+                      _rows(fn, "z", z, (B, T, D), dtype, dev),
+                      _rows(fn, "r", r, (B, T, D), dtype, dev))
+
+
+def block_norm_fwd(o, *, w=None, z=None, s=None, r=None, w2=None, groups=1, eps=1e-5, stream=None):
+    """Norms before and after a block with its gate and residual scale (see
+    lz_block_norm_fwd): out = [r +] m [* silu(z)] [* s], m = rmsnorm over each
+    of `groups` runs of features of o times w (o itself without w), n =
+    rmsnorm(out) * w2.  o [B, T, D] (rows may be strided, as z's and r's), or
+    the attention's [B, H, T, d], normed a head and laid out as rows.  w, s, w2
+    [D] fp32.  Returns (out, n); n is None without w2."""
+    fn, dev = "block_norm_fwd", o.device
+    d = _norm_args(fn, o, z, r, groups, eps)
+    _whole(fn, (d.D,), torch.float32, dev, w=w, s=s, w2=w2)
+    with _on(dev, stream):
+        out = torch.empty(d.B, d.T, d.D, dtype=o.dtype, device=dev)
+        n = torch.empty_like(out) if w2 is not None else None
+        lz_block_norm_fwd(d, o, w, z, s, r, w2, out, n, stream)
+    return out, n
+
+
+def block_norm_bwd(o, *, w=None, z=None, s=None, w2=None, out=None, dout=None, dn=None, groups=1,
+                   eps=1e-5, want_dr=False, stream=None):
+    """Gradients of block_norm_fwd: a dict of do (o's shape), dz, dw, ds, dw2
+    (None for what was not given; dw2 needs dn) and dr (None unless wanted).
+    out: the forward's, needed with dn."""
+    fn, dev = "block_norm_bwd", o.device
+    d = _norm_args(fn, o, z, None, groups, eps)
+    _whole(fn, (d.D,), torch.float32, dev, w=w, s=s, w2=w2)
+    _whole(fn, (d.B, d.T, d.D), o.dtype, dev, out=out, dout=dout, dn=dn)
+    _need(dout is not None or dn is not None, fn, "dout or dn must be given")
+    _need(dn is None or (out is not None and w2 is not None), fn, "dn needs out and w2")
+    with _on(dev, stream):
+        rows = lambda: torch.empty(d.B, d.T, d.D, dtype=o.dtype, device=dev)
+        par = lambda on: torch.empty(d.D, dtype=torch.float32, device=dev) if on else None
+        do = torch.empty(o.shape, dtype=o.dtype, device=dev)
+        dz = rows() if z is not None else None
+        dr = rows() if want_dr else None
+        dw, ds, dw2 = par(w is not None), par(s is not None), par(dn is not None)
+        n = lz_layer_workspace_bytes(d, LZ_WS_NORM_BWD)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        lz_block_norm_bwd(d, o, w, z, s, w2, out, dout, dn, do, dz, dr, dw, ds, dw2, ws, n, stream)
+    return {"do": do, "dz": dz, "dr": dr, "dw": dw, "ds": ds, "dw2": dw2}

@@ -1,0 +1,549 @@
+// Norms before and after a block, fused with its gate and residual scale:
+//   m = rmsnorm_groups(o) w,  out = [r +] m [silu(z)] [s],  n = rmsnorm(out) w2
+//
+// A row of D features stays in registers between its two norms: every input
+// is read once and every output written once, a few operations an element, so
+// HBM bandwidth bounds it (forward up to 5 values an element, backward up to
+// 8).  A thread holds 16 elements; up to 512 elements a row belongs to one
+// warp (no block-wide synchronisation), longer rows to a block.  Blocks walk
+// the rows with a stride, so that the backward's parameter gradients stay in
+// registers and leave as one partial per block.
+#include "layer.cuh"
+
+namespace lz {
+namespace {
+
+constexpr int E = 16;         // elements of a thread
+constexpr int kMaxD = 16384;  // 1024 threads
+constexpr int kRowWarps = 4;  // rows of a block of one-warp rows
+
+// How the sums over a group of features are formed: the group is the whole
+// row; a power-of-two number of neighbouring lanes; anything else (partial
+// sums in shared memory, a warp per group).
+enum { GROUP_ROW = 0, GROUP_LANES = 1, GROUP_SMEM = 2 };
+
+struct NormParams {
+  int64_t rows;
+  int T, D, G, heads;
+  float eps;
+  Rows so, sz, sr;
+  const void* o;
+  const float* w;
+  const void* z;
+  const float* s;
+  const void* r;
+  const float* w2;
+  void* out;
+  void* n;
+  // backward
+  const void* dout;
+  const void* dn;
+  void* d_o;
+  void* dz;
+  void* dr;
+  float* part;  // [blocks][3][D]: dw, ds, dw2
+};
+
+// Sum over the team that holds a row: its warp, or its block
+template <bool WARP>
+__device__ __forceinline__ float team_sum(float v, float* red) {
+  v = warp_sum(v);
+  if constexpr (WARP) return v;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
+  __syncthreads();  // the previous sum's readers are done
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  return warp_sum(lane < nw ? red[lane] : 0.f);
+}
+
+// Per-vector partial sums ps[k] -> the sum over each vector's group
+template <int VW, bool WARP, int MODE>
+__device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int lane, int team, float* red,
+                                          float* sm) {
+  constexpr int NV = E / VW;
+  const int nvec = p.D / VW;
+  if constexpr (MODE == GROUP_ROW) {
+    float a = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) a += ps[k];
+    a = team_sum<WARP>(a, red);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) ps[k] = a;
+  } else if constexpr (MODE == GROUP_LANES) {
+    const int gv = nvec / p.G;  // lanes of a group: 1, 2, .. 32
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      for (int o = gv / 2; o > 0; o >>= 1) ps[k] += __shfl_xor_sync(0xffffffffu, ps[k], o);
+  } else {  // (block teams only) sm: nvec partials, then G sums
+    const int gv = nvec / p.G, warp = threadIdx.x / 32, l = threadIdx.x % 32;
+    float* gs = sm + nvec;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * team + lane;
+      if (v < nvec) sm[v] = ps[k];
+    }
+    __syncthreads();
+    for (int g = warp; g < p.G; g += blockDim.x / 32) {
+      float a = 0.f;
+      for (int x = l; x < gv; x += 32) a += sm[g * gv + x];
+      a = warp_sum(a);
+      if (l == 0) gs[g] = a;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * team + lane;
+      ps[k] = v < nvec ? gs[v / gv] : 0.f;
+    }
+  }
+}
+
+// Address of feature c of row (b, t) of the block's output o (or its gradient
+// when it has o's layout)
+__device__ __forceinline__ size_t o_at(const NormParams& p, const Rows& so, int b, int t, int c) {
+  if (!p.heads) return so.at(b, t) + c;
+  const int dv = p.D / p.G, g = c / dv;
+  return (((size_t)b * p.G + g) * p.T + t) * dv + (c - g * dv);
+}
+
+template <typename IO, int VW, bool WARP, int MODE, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
+  extern __shared__ float sm[];
+  __shared__ float red[32];
+  constexpr int NV = E / VW;
+  const int team = WARP ? 32 : blockDim.x;
+  const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+  const int nvec = p.D / VW;
+  const int64_t row0 = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
+  for (int64_t row = row0; row < p.rows; row += step) {
+    const int b = (int)(row / p.T), t = (int)(row % p.T);
+    float x[E];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * team + lane;
+      if (v < nvec) {
+        load_vec<VW>((const IO*)p.o + o_at(p, p.so, b, t, v * VW), x + k * VW);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) x[k * VW + e] = 0.f;
+      }
+    }
+    if (p.w) {
+      float ps[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        ps[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) ps[k] = fmaf(x[k * VW + e], x[k * VW + e], ps[k]);
+      }
+      group_sum<VW, WARP, MODE>(p, ps, lane, team, red, sm);
+      const float ig = (float)p.G / (float)p.D;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const float rs = rsqrtf(ps[k] * ig + p.eps);
+        const int v = k * team + lane;
+        if (v < nvec) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) x[k * VW + e] *= rs * p.w[v * VW + e];
+        }
+      }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * team + lane;
+      if (v < nvec) {
+        const int c = v * VW;
+        float* xv = x + k * VW;
+        if (p.z) {
+          float z[VW];
+          load_vec<VW>((const IO*)p.z + p.sz.at(b, t) + c, z);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) xv[e] *= z[e] * sigmoid(z[e]);
+        }
+        if (p.s) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) xv[e] *= p.s[c + e];
+        }
+        if (p.r) {
+          float r[VW];
+          load_vec<VW>((const IO*)p.r + p.sr.at(b, t) + c, r);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) xv[e] += r[e];
+        }
+        store_vec<VW>((IO*)p.out + (size_t)row * p.D + c, xv);
+        // the second norm is that of the stored stream, so that the backward
+        // finds the same values in it
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          xv[e] = to_f(from_f<IO>(xv[e]));
+          ss = fmaf(xv[e], xv[e], ss);
+        }
+      }
+    }
+    if (p.w2) {
+      const float rs = rsqrtf(team_sum<WARP>(ss, red) / (float)p.D + p.eps);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = k * team + lane;
+        if (v < nvec) {
+          float* xv = x + k * VW;
+#pragma unroll
+          for (int e = 0; e < VW; ++e) xv[e] *= rs * p.w2[v * VW + e];
+          store_vec<VW>((IO*)p.n + (size_t)row * p.D + v * VW, xv);
+        }
+      }
+    }
+  }
+}
+
+// Backward.  With xh = out rs2 and q = dn w2 the gradient at `out` is
+//   e = dout + rs2 (q - xh mean(q xh))           (= dr)
+// and with mh = o rs, core = mh w, f = e s:
+//   ds = sum e core silu(z)     dz = f core silu'(z)     dw = sum f silu(z) mh
+//   do = rs (k - mh mean_group(k mh)),  k = f silu(z) w
+template <typename IO, int VW, bool WARP, int MODE, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
+  extern __shared__ float sm[];
+  __shared__ float red[32];
+  constexpr int NV = E / VW;
+  const int team = WARP ? 32 : blockDim.x;
+  const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+  const int nvec = p.D / VW;
+  const int64_t row0 = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
+  const float ig = (float)p.G / (float)p.D, id = 1.f / (float)p.D;
+  const Rows cont{p.D, (int64_t)p.T * p.D};
+  float dw[E], ds[E], dw2[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) dw[i] = ds[i] = dw2[i] = 0.f;
+  for (int64_t row = row0; row < p.rows; row += step) {
+    const int b = (int)(row / p.T), t = (int)(row % p.T);
+    float e[E], x[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) e[i] = x[i] = 0.f;
+    if (p.dn) {
+      float ss = 0.f, qx = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = k * team + lane;
+        if (v < nvec) {
+          load_vec<VW>((const IO*)p.out + (size_t)row * p.D + v * VW, x + k * VW);
+          load_vec<VW>((const IO*)p.dn + (size_t)row * p.D + v * VW, e + k * VW);
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            const int i = k * VW + j;
+            ss = fmaf(x[i], x[i], ss);
+            qx = fmaf(e[i] * p.w2[v * VW + j], x[i], qx);
+          }
+        }
+      }
+      const float rs = rsqrtf(team_sum<WARP>(ss, red) * id + p.eps);
+      const float m = team_sum<WARP>(qx, red) * id * rs * rs;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = k * team + lane;
+        if (v < nvec) {
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            const int i = k * VW + j;
+            dw2[i] = fmaf(e[i] * rs, x[i], dw2[i]);
+            e[i] = rs * (e[i] * p.w2[v * VW + j] - x[i] * m);
+          }
+        }
+      }
+    }
+    float ps[NV], rs[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * team + lane;
+      ps[k] = 0.f;
+      if (v < nvec) {
+        load_vec<VW>((const IO*)p.o + o_at(p, p.so, b, t, v * VW), x + k * VW);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) ps[k] = fmaf(x[k * VW + j], x[k * VW + j], ps[k]);
+        if (p.dout) {
+          float g[VW];
+          load_vec<VW>((const IO*)p.dout + (size_t)row * p.D + v * VW, g);
+#pragma unroll
+          for (int j = 0; j < VW; ++j) e[k * VW + j] += g[j];
+        }
+        if (p.dr) store_vec<VW>((IO*)p.dr + (size_t)row * p.D + v * VW, e + k * VW);
+      }
+    }
+    if (p.w) group_sum<VW, WARP, MODE>(p, ps, lane, team, red, sm);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * team + lane;
+      rs[k] = p.w ? rsqrtf(ps[k] * ig + p.eps) : 1.f;
+      ps[k] = 0.f;
+      if (v < nvec) {
+        const int c = v * VW;
+        float z[VW], dz[VW];
+        if (p.z) load_vec<VW>((const IO*)p.z + p.sz.at(b, t) + c, z);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          const int i = k * VW + j;
+          const float wv = p.w ? p.w[c + j] : 1.f, sv = p.s ? p.s[c + j] : 1.f;
+          x[i] *= rs[k];  // mh
+          const float core = x[i] * wv;
+          float f = e[i] * sv;
+          if (p.z) {
+            const float sg = sigmoid(z[j]), si = z[j] * sg;
+            dz[j] = f * core * (sg + si * (1.f - sg));
+            ds[i] = fmaf(e[i] * core, si, ds[i]);
+            f *= si;
+          } else {
+            ds[i] = fmaf(e[i], core, ds[i]);
+          }
+          dw[i] = fmaf(f, x[i], dw[i]);
+          e[i] = f * wv;  // the gradient at mh
+          ps[k] = fmaf(e[i], x[i], ps[k]);
+        }
+        if (p.dz) store_vec<VW>((IO*)p.dz + (size_t)row * p.D + c, dz);
+      }
+    }
+    if (p.w) group_sum<VW, WARP, MODE>(p, ps, lane, team, red, sm);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = k * team + lane;
+      if (v < nvec) {
+        if (p.w) {
+          const float m = ps[k] * ig;
+#pragma unroll
+          for (int j = 0; j < VW; ++j) e[k * VW + j] = rs[k] * (e[k * VW + j] - x[k * VW + j] * m);
+        }
+        store_vec<VW>((IO*)p.d_o + o_at(p, cont, b, t, v * VW), e + k * VW);
+      }
+    }
+  }
+  // ---- the block's partials; the warps of a warp-per-row block are added in
+  // order in shared memory
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const float* a = q == 0 ? dw : q == 1 ? ds : dw2;
+    float* part = p.part + ((size_t)blockIdx.x * 3 + q) * p.D;
+    if constexpr (WARP) {
+      const int warp = threadIdx.x / 32, nw = blockDim.x / 32;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = (i / VW * 32 + lane) * VW + i % VW;
+        if (c < p.D) sm[warp * p.D + c] = a[i];
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
+        float tot = 0.f;
+        for (int w = 0; w < nw; ++w) tot += sm[w * p.D + c];
+        part[c] = tot;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = k * team + lane;
+        if (v < nvec) {
+#pragma unroll
+          for (int j = 0; j < VW; ++j) part[v * VW + j] = a[k * VW + j];
+        }
+      }
+    }
+  }
+}
+
+// ---- host -----------------------------------------------------------------
+
+struct Shape {
+  bool vec, warp;
+  int vw, threads, mode;
+  size_t smem;  // of the group sums
+};
+
+Shape shape_of(const lz_norm_dims* d, bool vec) {
+  Shape s;
+  s.vec = vec;
+  s.vw = vec ? (int)(16 / esize(d->io)) : 1;
+  const int nvec = d->D / s.vw;
+  const int gd = d->D / d->G;
+  const int gv = gd % s.vw == 0 ? gd / s.vw : 0;
+  s.mode = d->G == 1 ? GROUP_ROW : (gv >= 1 && gv <= 32 && (gv & (gv - 1)) == 0) ? GROUP_LANES : GROUP_SMEM;
+  s.warp = d->D <= 32 * E && s.mode != GROUP_SMEM;
+  s.threads = s.warp ? kRowWarps * 32 : (nvec * s.vw + E - 1) / E;
+  s.threads = (s.threads + 31) / 32 * 32;
+  s.smem = s.mode == GROUP_SMEM ? (size_t)(nvec + d->G) * sizeof(float) : 0;
+  return s;
+}
+
+// Blocks that walk the rows: as many as fit the device at once
+template <class Kern>
+int grid_rows(Kern k, int64_t rows, int threads, size_t smem, int rows_per_block) {
+  const int64_t want = (rows + rows_per_block - 1) / rows_per_block;
+  if (want <= 148) return (int)std::max<int64_t>(1, want);
+  int wave = resident_ctas(k, threads, smem);
+  if (wave <= 0) wave = 148;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(want, wave));
+}
+
+template <typename IO, int VW, bool WARP, int MODE>
+cudaError_t go_fwd(const NormParams& p, const Shape& sh, cudaStream_t s) {
+  constexpr int kT = WARP ? kRowWarps * 32 : 512;
+  // rows of more than 8192 features need blocks of up to 1024 threads
+  auto k = norm_fwd_kernel<IO, VW, WARP, MODE, kT>;
+  if constexpr (!WARP) {
+    if (sh.threads > kT) k = norm_fwd_kernel<IO, VW, WARP, MODE, 1024>;
+  }
+  if (sh.smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int grid = grid_rows(k, p.rows, sh.threads, sh.smem, WARP ? kRowWarps : 1);
+  ScopedTiming tm("block_norm_fwd", s);
+  k<<<grid, sh.threads, sh.smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Partials of the backward: a bound that needs no device
+constexpr int kMaxBlocks = 148 * 8;
+int bwd_part_rows(int64_t rows) { return (int)std::min<int64_t>(std::max<int64_t>(rows, 1), kMaxBlocks); }
+
+template <typename IO, int VW, bool WARP, int MODE>
+cudaError_t go_bwd(const NormParams& p, const Shape& sh, int* blocks, cudaStream_t s) {
+  constexpr int kT = WARP ? kRowWarps * 32 : 512;
+  // rows of more than 8192 features need blocks of up to 1024 threads
+  auto k = norm_bwd_kernel<IO, VW, WARP, MODE, kT>;
+  if constexpr (!WARP) {
+    if (sh.threads > kT) k = norm_bwd_kernel<IO, VW, WARP, MODE, 1024>;
+  }
+  const size_t smem = WARP ? std::max(sh.smem, (size_t)kRowWarps * p.D * sizeof(float)) : sh.smem;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int grid = std::min(grid_rows(k, p.rows, sh.threads, smem, WARP ? kRowWarps : 1), bwd_part_rows(p.rows));
+  *blocks = grid;
+  ScopedTiming tm("block_norm_bwd", s);
+  k<<<grid, sh.threads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+#define LZ_NORM_DISPATCH(CALL)                                              \
+  do {                                                                      \
+    if (d->io == LZ_BF16) {                                                 \
+      if (sh.vec) LZ_NORM_MODE(CALL, bf16, 8) else LZ_NORM_MODE(CALL, bf16, 1) \
+    } else {                                                                \
+      if (sh.vec) LZ_NORM_MODE(CALL, float, 4) else LZ_NORM_MODE(CALL, float, 1) \
+    }                                                                       \
+  } while (0)
+#define LZ_NORM_MODE(CALL, IO, VW)                                          \
+  {                                                                         \
+    if (sh.mode == GROUP_SMEM) e = CALL(IO, VW, false, GROUP_SMEM);         \
+    else if (sh.mode == GROUP_ROW) e = sh.warp ? CALL(IO, VW, true, GROUP_ROW) : CALL(IO, VW, false, GROUP_ROW); \
+    else e = sh.warp ? CALL(IO, VW, true, GROUP_LANES) : CALL(IO, VW, false, GROUP_LANES); \
+  }
+
+lz_status check_norm(const char* fn, const lz_norm_dims* d) {
+  if (!d) return layer_fail(LZ_ERR_INVALID_ARG, "%s: dims must not be NULL", fn);
+  if (d->B < 0 || d->T < 0 || d->D < 0)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: B, T, D must be >= 0 (got %d, %d, %d)", fn, d->B, d->T, d->D);
+  if (!io_ok(d->io))
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: io dtype %d is not LZ_F32 or LZ_BF16", fn, (int)d->io);
+  if (d->D > kMaxD) return layer_fail(LZ_ERR_UNSUPPORTED, "%s: D must be <= %d (got %d)", fn, kMaxD, d->D);
+  if (d->G < 1 || d->D % d->G)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: G must be a divisor of D (got %d of %d)", fn, d->G, d->D);
+  if (d->heads != 0 && d->heads != 1)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: heads must be 0 or 1 (got %d)", fn, d->heads);
+  if (!(d->eps > 0.f && d->eps < 3.0e38f))
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: eps must be finite and > 0", fn);
+  if (!rows_ok(d->o) || !rows_ok(d->z) || !rows_ok(d->r))
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: bad row strides", fn);
+  return LZ_OK;
+}
+
+// heads: a vector must lie within a head
+bool norm_vec(const lz_norm_dims* d, const NormParams& p) {
+  const size_t es = esize(d->io);
+  const int vw = (int)(16 / es);
+  if (d->D % vw || (d->D / d->G) % vw) return false;
+  return (d->heads || rows_vec(p.o, p.so, vw, es)) && rows_vec(p.z, p.sz, vw, es) && rows_vec(p.r, p.sr, vw, es);
+}
+
+}  // namespace
+
+size_t norm_bwd_ws(const lz_norm_dims* d) {
+  if (check_norm("lz_layer_workspace_bytes", d) != LZ_OK) return 0;
+  return ws_round((size_t)bwd_part_rows((int64_t)d->B * d->T) * 3 * d->D * sizeof(float));
+}
+
+}  // namespace lz
+
+using namespace lz;
+
+extern "C" lz_status lz_block_norm_fwd(const lz_norm_dims* d, const void* o, const float* w, const void* z,
+                                       const float* s, const void* r, const float* w2, void* out, void* n,
+                                       lz_stream stream) {
+  const char* fn = "lz_block_norm_fwd";
+  lz_status st = check_norm(fn, d);
+  if (st != LZ_OK) return st;
+  if (d->B == 0 || d->T == 0 || d->D == 0) return layer_done(cudaSuccess, fn);
+  const unsigned es = (unsigned)esize(d->io);
+  st = check_ptrs(fn, {{o, "o", true, d->heads ? 16 : es}, {w, "w", false, 16}, {z, "z", false, es},
+                       {s, "s", false, 16}, {r, "r", false, es}, {w2, "w2", false, 16}, {out, "out", true, 16},
+                       {n, "n", w2 != nullptr, 16}});
+  if (st == LZ_OK) st = check_distinct(fn, {out, w2 ? n : nullptr}, {o, z, r});
+  if (st != LZ_OK) return st;
+  NormParams p{};
+  p.rows = (int64_t)d->B * d->T;
+  p.T = d->T; p.D = d->D; p.G = d->G; p.heads = d->heads; p.eps = d->eps;
+  p.so = rows_of(d->o, d->T, d->D);
+  p.sz = rows_of(d->z, d->T, d->D);
+  p.sr = rows_of(d->r, d->T, d->D);
+  p.o = o; p.w = w; p.z = z; p.s = s; p.r = r; p.w2 = w2; p.out = out; p.n = n;
+  const Shape sh = shape_of(d, norm_vec(d, p));
+  cudaError_t e = cudaSuccess;
+#define LZ_CALL(IO, VW, WARP, MODE) go_fwd<IO, VW, WARP, MODE>(p, sh, (cudaStream_t)stream)
+  LZ_NORM_DISPATCH(LZ_CALL);
+#undef LZ_CALL
+  return layer_done(e, fn);
+}
+
+extern "C" lz_status lz_block_norm_bwd(const lz_norm_dims* d, const void* o, const float* w, const void* z,
+                                       const float* s, const float* w2, const void* out, const void* dout,
+                                       const void* dn, void* dOo, void* dz, void* dr, float* dw, float* ds,
+                                       float* dw2, void* ws, size_t ws_bytes, lz_stream stream) {
+  const char* fn = "lz_block_norm_bwd";
+  lz_status st = check_norm(fn, d);
+  if (st != LZ_OK) return st;
+  if (d->D == 0) return layer_done(cudaSuccess, fn);
+  const int64_t rows = (int64_t)d->B * d->T;
+  const bool data = rows > 0;
+  const unsigned es = (unsigned)esize(d->io);
+  if (data && !dout && !dn) return layer_fail(LZ_ERR_INVALID_ARG, "%s: dout and dn must not both be NULL", fn);
+  st = check_ptrs(fn, {{o, "o", data, d->heads ? 16 : es}, {w, "w", dw != nullptr, 16}, {z, "z", dz != nullptr, es},
+                       {s, "s", ds != nullptr, 16}, {w2, "w2", data && (dn || dw2), 16}, {out, "out", data && dn, 16},
+                       {dout, "dout", false, 16}, {dn, "dn", data && dw2, 16}, {dOo, "dOo", data, 16},
+                       {dz, "dz", false, 16}, {dr, "dr", false, 16}, {dw, "dw", false, 16}, {ds, "ds", false, 16},
+                       {dw2, "dw2", false, 16}, {ws, "workspace", true, 256}});
+  if (st == LZ_OK) st = check_distinct(fn, {dOo, dz, dr, dw, ds, dw2, ws}, {o, w, z, s, w2, out, dout, dn});
+  if (st != LZ_OK) return st;
+  const size_t need = norm_bwd_ws(d);
+  if (ws_bytes < need)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: workspace too small (%zu bytes, need %zu)", fn, ws_bytes, need);
+  NormParams p{};
+  p.rows = rows;
+  p.T = std::max(d->T, 1); p.D = d->D; p.G = d->G; p.heads = d->heads; p.eps = d->eps;
+  p.so = rows_of(d->o, d->T, d->D);
+  p.sz = rows_of(d->z, d->T, d->D);
+  p.o = o; p.w = w; p.z = z; p.s = s; p.w2 = w2; p.out = const_cast<void*>(out);
+  p.dout = dout; p.dn = dn; p.d_o = dOo; p.dz = dz; p.dr = dr; p.part = (float*)ws;
+  const Shape sh = shape_of(d, norm_vec(d, p));
+  cudaError_t e = cudaSuccess;
+  int blocks = 0;
+#define LZ_CALL(IO, VW, WARP, MODE) go_bwd<IO, VW, WARP, MODE>(p, sh, &blocks, (cudaStream_t)stream)
+  LZ_NORM_DISPATCH(LZ_CALL);
+#undef LZ_CALL
+  if (e == cudaSuccess && (dw || ds || dw2))
+    e = launch_sum_rows({p.part, blocks, (size_t)3 * d->D, dw, (size_t)d->D, ds, (size_t)d->D, dw2, (size_t)d->D},
+                        (cudaStream_t)stream);
+  return layer_done(e, fn);
+}

@@ -1,0 +1,409 @@
+// Short causal convolution over the tokens, a channel at a time, with its
+// activation: y_t = act(bias + sum_{j<K} w_j x_{t-K+1+j}).
+//
+// Every element is read and written once (forward 2 values, backward 3), with
+// 2K + a few operations in between: bound by HBM bandwidth.  A thread holds a
+// vector of neighbouring channels and walks a run of tokens with the last K-1
+// inputs in registers, so that a token is read once and only the K-1 tokens
+// before a run are read twice (they come out of L2).
+#include "layer.cuh"
+
+namespace lz {
+namespace {
+
+constexpr int NT = 128;
+
+struct ConvParams {
+  int B, T, D, silu, run;  // run: tokens of a thread
+  Rows x;
+  const void* px;
+  const float* w;
+  const float* bias;
+  const void* x0;
+  const int64_t* lens;
+  void* y;
+  void* xT;
+};
+
+// x at token t of sequence b; the history where t < 0
+template <typename IO, int K, int VW>
+__device__ __forceinline__ void load_x(const ConvParams& p, int b, int t, int c, float* v) {
+  if (t >= 0) {
+    load_vec<VW>((const IO*)p.px + p.x.at(b, t) + c, v);
+  } else if (p.x0) {
+    load_vec<VW>((const IO*)p.x0 + ((size_t)b * (K - 1) + (t + K - 1)) * p.D + c, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) v[e] = 0.f;
+  }
+}
+
+template <typename IO, int K, int VW>
+__global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvParams p) {
+  const int nvec = p.D / VW;
+  const int nrun = (p.T + p.run - 1) / p.run;
+  const size_t idx = (size_t)blockIdx.x * NT + threadIdx.x;
+  const int b = blockIdx.y;
+  const int c = (int)(idx % nvec) * VW;
+  const int run = (int)(idx / nvec);
+  if (run >= (nrun > 0 ? nrun : 1)) return;
+  const int L = seq_len(p.lens, b, p.T);
+  if (run == 0 && p.xT) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      float v[VW];
+      load_x<IO, K, VW>(p, b, L - (K - 1) + j, c, v);
+      store_vec<VW>((IO*)p.xT + ((size_t)b * (K - 1) + j) * p.D + c, v);
+    }
+  }
+  const int t0 = run * p.run, t1 = min(p.T, t0 + p.run), te = min(t1, L);
+  float w[K][VW], bias[VW], h[K][VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j][e] = p.w[(size_t)(c + e) * K + j];
+    bias[e] = p.bias ? p.bias[c + e] : 0.f;
+  }
+  IO* y = (IO*)p.y + ((size_t)b * p.T) * p.D + c;
+  if (t0 < te) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) load_x<IO, K, VW>(p, b, t0 - (K - 1) + j, c, h[j]);
+#pragma unroll 4
+    for (int t = t0; t < te; ++t) {
+      load_vec<VW>((const IO*)p.px + p.x.at(b, t) + c, h[K - 1]);
+      float o[VW];
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        float a = bias[e];
+#pragma unroll
+        for (int j = 0; j < K; ++j) a = fmaf(w[j][e], h[j][e], a);
+        o[e] = p.silu ? a * sigmoid(a) : a;
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) h[j][e] = h[j + 1][e];
+      }
+      store_vec<VW>(y + (size_t)t * p.D, o);
+    }
+  }
+  float zero[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) zero[e] = 0.f;
+  for (int t = max(t0, te); t < t1; ++t) store_vec<VW>(y + (size_t)t * p.D, zero);
+}
+
+template <typename IO, int K, int VW>
+__global__ void __launch_bounds__(NT) conv_step_kernel(ConvParams p, void* hist) {
+  const int nvec = p.D / VW;
+  const size_t idx = (size_t)blockIdx.x * NT + threadIdx.x;
+  const int c = (int)(idx % nvec) * VW;
+  const int b = (int)(idx / nvec);
+  if (b >= p.B) return;
+  float h[K][VW];
+  IO* hp = (IO*)hist + (size_t)b * (K - 1) * p.D + c;
+  load_vec<VW>((const IO*)p.px + p.x.at(b, 0) + c, h[K - 1]);
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) load_vec<VW>(hp + (size_t)j * p.D, h[j]);
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) store_vec<VW>(hp + (size_t)j * p.D, h[j + 1]);
+  float o[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    float a = p.bias ? p.bias[c + e] : 0.f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) a = fmaf(p.w[(size_t)(c + e) * K + j], h[j][e], a);
+    o[e] = p.silu ? a * sigmoid(a) : a;
+  }
+  store_vec<VW>((IO*)p.y + (size_t)b * p.D + c, o);
+}
+
+// ---- backward -------------------------------------------------------------
+// dp_t = dy_t act'(p_t) needs the inputs up to K-1 tokens back, dx_t =
+// sum_j w_j dp_{t+K-1-j} the dp up to K-1 tokens ahead: a run of tokens
+// [t0, t1) forms dp for [t0, t1 + K-1) with both windows in registers.  A warp
+// holds 32 channel vectors, the block's warps neighbouring runs; the parameter
+// gradients stay in registers over the run and are added across the warps in
+// shared memory, one partial per block, which launch_sum_rows adds up.
+constexpr int kWarps = 4;
+
+struct ConvBwdParams {
+  ConvParams f;
+  const void* dy;
+  const void* dxT;
+  void* dx;
+  void* dx0;
+  float* part;  // [blocks over (b, runs)][D*K + D]
+};
+
+template <typename IO, int K, int VW>
+__global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) {
+  __shared__ float red[kWarps][32 * VW];
+  const ConvParams& p = q.f;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int b = blockIdx.z;
+  const int c = (blockIdx.x * 32 + lane) * VW;
+  const bool on = c < p.D;
+  const int L = seq_len(p.lens, b, p.T);
+  const int t0 = (blockIdx.y * kWarps + warp) * p.run, t1 = min(p.T, t0 + p.run);
+  const bool first = t0 == 0;
+  float w[K][VW], bias[VW], xw[K][VW], dpw[K][VW], dw[K][VW], db[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      w[j][e] = on ? p.w[(size_t)(c + e) * K + j] : 0.f;
+      dw[j][e] = 0.f;
+      dpw[j][e] = 0.f;
+    }
+    bias[e] = on && p.bias ? p.bias[c + e] : 0.f;
+    db[e] = 0.f;
+  }
+  if (on && (t0 < t1 || (first && q.dx0))) {
+    IO* dx = (IO*)q.dx + (size_t)b * p.T * p.D + c;
+    if (t0 < L) {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) load_x<IO, K, VW>(p, b, t0 - (K - 1) + j, c, xw[j]);
+    }
+    // s walks the tokens whose dp is formed; dx of token s - (K-1) is then complete
+#pragma unroll 4
+    for (int s = t0; s < t1 + K - 1; ++s) {
+      if (s < L) {
+        float dyv[VW];
+        load_vec<VW>((const IO*)p.px + p.x.at(b, s) + c, xw[K - 1]);
+        load_vec<VW>((const IO*)q.dy + ((size_t)b * p.T + s) * p.D + c, dyv);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          float dp = dyv[e];
+          if (p.silu) {
+            float a = bias[e];
+#pragma unroll
+            for (int j = 0; j < K; ++j) a = fmaf(w[j][e], xw[j][e], a);
+            const float sg = sigmoid(a);
+            dp *= sg * (1.f + a * (1.f - sg));
+          }
+          dpw[K - 1][e] = dp;
+          if (s < t1) {
+            db[e] += dp;
+#pragma unroll
+            for (int j = 0; j < K; ++j) dw[j][e] = fmaf(dp, xw[j][e], dw[j][e]);
+          }
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) xw[j][e] = xw[j + 1][e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) dpw[K - 1][e] = 0.f;
+      }
+      const int t = s - (K - 1);
+      if (t >= t0 || (first && q.dx0)) {
+        float o[VW];
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          o[e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < K; ++j) o[e] = fmaf(w[j][e], dpw[K - 1 - j][e], o[e]);
+        }
+        const int jT = t - (L - (K - 1));  // token t is row jT of the final history
+        if (q.dxT && jT >= 0 && t < L) {
+          float g[VW];
+          load_vec<VW>((const IO*)q.dxT + ((size_t)b * (K - 1) + jT) * p.D + c, g);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) o[e] += g[e];
+        }
+        if (t >= 0)
+          store_vec<VW>(dx + (size_t)t * p.D, o);
+        else
+          store_vec<VW>((IO*)q.dx0 + ((size_t)b * (K - 1) + t + K - 1) * p.D + c, o);
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e)
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) dpw[j][e] = dpw[j + 1][e];
+    }
+  }
+  // ---- the block's partial of dw, dbias: warps added in order
+  const size_t C = (size_t)p.D * (K + 1);
+  float* part = q.part + ((size_t)b * gridDim.y + blockIdx.y) * C;
+#pragma unroll
+  for (int j = 0; j <= K; ++j) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VW; ++e) red[warp][lane * VW + e] = j < K ? dw[j < K ? j : 0][e] : db[e];
+    __syncthreads();
+    for (int x = threadIdx.x; x < 32 * VW; x += kWarps * 32) {
+      const int ch = blockIdx.x * 32 * VW + x;
+      if (ch < p.D) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) t += red[k][x];
+        part[j < K ? (size_t)ch * K + j : (size_t)p.D * K + ch] = t;
+      }
+    }
+  }
+}
+
+// ---- host -----------------------------------------------------------------
+
+lz_status check_conv(const char* fn, const lz_conv_dims* d) {
+  if (!d) return layer_fail(LZ_ERR_INVALID_ARG, "%s: dims must not be NULL", fn);
+  if (d->B < 0 || d->T < 0 || d->D < 0)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: B, T, D must be >= 0 (got %d, %d, %d)", fn, d->B, d->T, d->D);
+  if (!io_ok(d->io))
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: io dtype %d is not LZ_F32 or LZ_BF16", fn, (int)d->io);
+  if (d->K < 1 || d->K > 8)
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: taps K must be in [1, 8] (got %d)", fn, d->K);
+  if (d->silu != 0 && d->silu != 1)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: silu must be 0 or 1 (got %d)", fn, d->silu);
+  if (!rows_ok(d->x)) return layer_fail(LZ_ERR_INVALID_ARG, "%s: bad row strides", fn);
+  if (d->B > 65535) return layer_fail(LZ_ERR_UNSUPPORTED, "%s: B must be <= 65535 (got %d)", fn, d->B);
+  // keeps grid dimensions and 32-bit token indices in range
+  if (d->T > (1 << 23) || (double)d->T * d->D > (double)(1ll << 36))
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: problem too large (T %d, D %d)", fn, d->T, d->D);
+  return LZ_OK;
+}
+
+// Vectors of 16 bytes where rows and pointers allow it, else single elements
+bool conv_vec(const lz_conv_dims* d, const void* x, const Rows& r) {
+  const int vw = d->io == LZ_BF16 ? 8 : 4;
+  return d->D % vw == 0 && rows_vec(x, r, vw, esize(d->io));
+}
+
+template <template <typename, int, int> class Launch, typename P>
+cudaError_t dispatch_k(const P& p, int K, bool bf, bool vec, cudaStream_t s) {
+  switch (K) {
+#define LZ_K(k)                                                                       \
+  case k:                                                                             \
+    if (bf) return vec ? Launch<bf16, k, 8>::go(p, s) : Launch<bf16, k, 1>::go(p, s); \
+    return vec ? Launch<float, k, 4>::go(p, s) : Launch<float, k, 1>::go(p, s);
+    LZ_K(1) LZ_K(2) LZ_K(3) LZ_K(4) LZ_K(5) LZ_K(6) LZ_K(7) LZ_K(8)
+#undef LZ_K
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename IO, int K, int VW>
+struct FwdLaunch {
+  static cudaError_t go(const ConvParams& p, cudaStream_t s) {
+    const size_t nrun = std::max(1, (p.T + p.run - 1) / p.run);
+    const dim3 grid((unsigned)((nrun * (p.D / VW) + NT - 1) / NT), p.B);
+    ScopedTiming tm("conv_fwd", s);
+    conv_fwd_kernel<IO, K, VW><<<grid, NT, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+};
+
+struct StepParams {
+  ConvParams p;
+  void* hist;
+};
+template <typename IO, int K, int VW>
+struct StepLaunch {
+  static cudaError_t go(const StepParams& q, cudaStream_t s) {
+    const size_t n = (size_t)q.p.B * (q.p.D / VW);
+    ScopedTiming tm("conv_step", s);
+    conv_step_kernel<IO, K, VW><<<(unsigned)((n + NT - 1) / NT), NT, 0, s>>>(q.p, q.hist);
+    return cudaGetLastError();
+  }
+};
+
+// tokens of a block of the backward
+int bwd_blocks(const lz_conv_dims* d, int* run) {
+  // long runs re-read the least; short ones keep every SM busy (at least two
+  // blocks each) when there are few tokens and channels
+  int r = 64;
+  const int cb = (d->D + 127) / 128;
+  while (r > 8 && (size_t)d->B * cb * ((d->T + r * kWarps - 1) / (r * kWarps)) < 296) r /= 2;
+  *run = r;
+  return std::max(1, (d->T + r * kWarps - 1) / (r * kWarps));
+}
+
+template <typename IO, int K, int VW>
+struct BwdLaunch {
+  static cudaError_t go(const ConvBwdParams& q, cudaStream_t s) {
+    constexpr int W = VW == 8 ? 4 : VW;  // 8-byte vectors: the windows of 8 channels do not fit
+    const ConvParams& p = q.f;
+    const int tb = std::max(1, (p.T + p.run * kWarps - 1) / (p.run * kWarps));
+    const dim3 grid((p.D + 32 * W - 1) / (32 * W), tb, p.B);
+    ScopedTiming tm("conv_bwd", s);
+    conv_bwd_kernel<IO, K, W><<<grid, kWarps * 32, 0, s>>>(q);
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+
+size_t conv_bwd_ws(const lz_conv_dims* d) {
+  if (check_conv("lz_layer_workspace_bytes", d) != LZ_OK || d->B == 0 || d->D == 0) return 0;
+  int run;
+  return ws_round((size_t)d->B * bwd_blocks(d, &run) * d->D * (d->K + 1) * sizeof(float));
+}
+
+}  // namespace lz
+
+using namespace lz;
+
+extern "C" lz_status lz_conv_fwd(const lz_conv_dims* d, const void* x, const float* w, const float* bias,
+                                 const void* x0, const int64_t* lens, void* y, void* xT,
+                                 lz_stream stream) {
+  const char* fn = "lz_conv_fwd";
+  lz_status st = check_conv(fn, d);
+  if (st != LZ_OK) return st;
+  if (d->B == 0 || d->D == 0 || (d->T == 0 && !xT)) return layer_done(cudaSuccess, fn);
+  const bool data = d->T > 0;
+  st = check_ptrs(fn, {{x, "x", data, (unsigned)esize(d->io)}, {w, "w", true, 16}, {bias, "bias", false, 16},
+                       {x0, "x0", false, 16}, {lens, "lens", false, 8}, {y, "y", data, 16}, {xT, "xT", false, 16}});
+  if (st == LZ_OK) st = check_distinct(fn, {y, xT}, {x, x0});
+  if (st != LZ_OK) return st;
+  ConvParams p{d->B, d->T, d->D, d->silu, 16, rows_of(d->x, d->T, d->D), x, w, bias, x0, lens, y, xT};
+  const bool vec = conv_vec(d, x, p.x);
+  // runs of 16 tokens re-read 3/16 of the input from L2; with few of them
+  // (short prompts) runs of 4 put four times the threads on the machine
+  const size_t threads = (size_t)d->B * ((d->T + 15) / 16) * (d->D / (vec ? 16 / esize(d->io) : 1));
+  if (threads < 148 * 1024) p.run = 4;
+  return layer_done(dispatch_k<FwdLaunch>(p, d->K, d->io == LZ_BF16, vec, (cudaStream_t)stream), fn);
+}
+
+extern "C" lz_status lz_conv_bwd(const lz_conv_dims* d, const void* x, const float* w, const float* bias,
+                                 const void* x0, const int64_t* lens, const void* dy, const void* dxT, void* dx,
+                                 float* dw, float* dbias, void* dx0, void* ws, size_t ws_bytes,
+                                 lz_stream stream) {
+  const char* fn = "lz_conv_bwd";
+  lz_status st = check_conv(fn, d);
+  if (st != LZ_OK) return st;
+  if (d->D == 0) return layer_done(cudaSuccess, fn);
+  const bool data = d->T > 0 && d->B > 0;
+  st = check_ptrs(fn, {{x, "x", data, (unsigned)esize(d->io)}, {w, "w", true, 16}, {bias, "bias", false, 16},
+                       {x0, "x0", false, 16}, {lens, "lens", false, 8}, {dy, "dy", data, 16},
+                       {dxT, "dxT", false, 16}, {dx, "dx", data, 16}, {dw, "dw", true, 16},
+                       {dbias, "dbias", false, 16}, {dx0, "dx0", false, 16}, {ws, "workspace", d->B > 0, 256}});
+  if (st == LZ_OK) st = check_distinct(fn, {dx, dw, dbias, dx0, ws}, {x, w, bias, x0, dy, dxT});
+  if (st != LZ_OK) return st;
+  const size_t need = conv_bwd_ws(d);
+  if (ws_bytes < need)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: workspace too small (%zu bytes, need %zu)", fn, ws_bytes, need);
+  int run;
+  const int tb = bwd_blocks(d, &run);
+  ConvBwdParams q{{d->B, d->T, d->D, d->silu, run, rows_of(d->x, d->T, d->D), x, w, bias, x0, lens, nullptr, nullptr},
+                  dy, dxT, dx, dx0, (float*)ws};
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
+  if (d->B > 0) e = dispatch_k<BwdLaunch>(q, d->K, d->io == LZ_BF16, conv_vec(d, x, q.f.x), s);
+  if (e == cudaSuccess)
+    e = launch_sum_rows({(const float*)ws, d->B * tb, (size_t)d->D * (d->K + 1), dw, (size_t)d->D * d->K, dbias,
+                         (size_t)d->D, nullptr, 0},
+                        s);
+  return layer_done(e, fn);
+}
+
+extern "C" lz_status lz_conv_step(const lz_conv_dims* d, void* hist, const void* x, const float* w,
+                                  const float* bias, void* y, lz_stream stream) {
+  const char* fn = "lz_conv_step";
+  lz_status st = check_conv(fn, d);
+  if (st != LZ_OK) return st;
+  if (d->B == 0 || d->D == 0) return layer_done(cudaSuccess, fn);
+  st = check_ptrs(fn, {{hist, "hist", d->K > 1, 16}, {x, "x", true, (unsigned)esize(d->io)}, {w, "w", true, 16},
+                       {bias, "bias", false, 16}, {y, "y", true, 16}});
+  if (st == LZ_OK) st = check_distinct(fn, {hist, y}, {x});
+  if (st != LZ_OK) return st;
+  StepParams q{{d->B, 1, d->D, d->silu, 1, rows_of(d->x, 1, d->D), x, w, bias, nullptr, nullptr, y, nullptr}, hist};
+  return layer_done(
+      dispatch_k<StepLaunch>(q, d->K, d->io == LZ_BF16, conv_vec(d, x, q.p.x), (cudaStream_t)stream), fn);
+}

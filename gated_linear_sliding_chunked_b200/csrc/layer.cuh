@@ -1,0 +1,187 @@
+// Shared parts of the layer operators (short convolution, selective scan,
+// block norms): strided rows, vector access, host-side checks.
+#pragma once
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+#include <initializer_list>
+
+#include "../../include/lizard.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace lz {
+
+// ---- device ---------------------------------------------------------------
+
+// Rows of a strided input: element (b, t, 0) stands at b * bs + t * ld.
+struct Rows {
+  int64_t ld, bs;
+  __host__ __device__ size_t at(int b, int t) const { return (size_t)b * bs + (size_t)t * ld; }
+};
+
+// VW consecutive elements as floats (one 16- or 8-byte access, or one element)
+template <int VW>
+__device__ __forceinline__ void load_vec(const float* p, float* x) {
+  if constexpr (VW == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  } else {
+    x[0] = *p;
+  }
+}
+template <int VW>
+__device__ __forceinline__ void load_vec(const bf16* p, float* x) {
+  if constexpr (VW == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(q[e] << 16);
+      x[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
+    }
+  } else if constexpr (VW == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    x[0] = __uint_as_float(u.x << 16);
+    x[1] = __uint_as_float(u.x & 0xffff0000u);
+    x[2] = __uint_as_float(u.y << 16);
+    x[3] = __uint_as_float(u.y & 0xffff0000u);
+  } else {
+    x[0] = __bfloat162float(*p);
+  }
+}
+template <int VW>
+__device__ __forceinline__ void store_vec(float* p, const float* x) {
+  if constexpr (VW == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  else
+    *p = x[0];
+}
+template <int VW>
+__device__ __forceinline__ void store_vec(bf16* p, const float* x) {
+  if constexpr (VW >= 4) {
+    uint32_t q[VW / 2];
+#pragma unroll
+    for (int e = 0; e < VW / 2; ++e) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+      q[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if constexpr (VW == 8)
+      *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+  } else {
+    *p = __float2bfloat16_rn(x[0]);
+  }
+}
+
+// sigma(x): exp's overflow for very negative x gives 1 / inf = 0, the limit
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// Tokens of sequence b (lens nullable, clamped to [0, T])
+__device__ __forceinline__ int seq_len(const int64_t* lens, int b, int T) {
+  if (!lens) return T;
+  const long long l = lens[b];
+  return l < 0 ? 0 : (l > T ? T : (int)l);
+}
+
+// ---- host -----------------------------------------------------------------
+
+inline lz_status layer_fail(lz_status st, const char* fmt, ...) {
+  char buf[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return (lz_status)set_last_error(st, buf);
+}
+
+inline lz_status layer_done(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return (lz_status)set_last_error(LZ_OK, "");
+  return layer_fail(LZ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// A pointer of the call: its name for messages, whether it must be given, and
+// the alignment that it needs.
+struct PtrRule {
+  const void* p;
+  const char* name;
+  bool required;
+  unsigned align;
+};
+
+inline lz_status check_ptrs(const char* fn, std::initializer_list<PtrRule> rules) {
+  for (const PtrRule& r : rules) {
+    if (!r.p) {
+      if (r.required) return layer_fail(LZ_ERR_INVALID_ARG, "%s: %s must not be NULL", fn, r.name);
+      continue;
+    }
+    if (reinterpret_cast<uintptr_t>(r.p) % r.align)
+      return layer_fail(LZ_ERR_INVALID_ARG, "%s: %s must be %u-byte aligned", fn, r.name, r.align);
+  }
+  return LZ_OK;
+}
+
+// An output that is also an input or another output (by its pointer)
+inline lz_status check_distinct(const char* fn, std::initializer_list<const void*> outs,
+                                std::initializer_list<const void*> ins) {
+  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    for (const void* const* q = o + 1; q != outs.end(); ++q)
+      if (*o == *q) return layer_fail(LZ_ERR_INVALID_ARG, "%s: two outputs overlap", fn);
+    for (const void* i : ins)
+      if (*o == i) return layer_fail(LZ_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+  }
+  return LZ_OK;
+}
+
+inline size_t esize(lz_dtype io) { return io == LZ_BF16 ? 2 : 4; }
+inline bool io_ok(lz_dtype io) { return io == LZ_BF16 || io == LZ_F32; }
+
+inline Rows rows_of(const lz_rows& r, int T, int width) {
+  if (r.ld == 0) return Rows{width, (int64_t)T * width};
+  return Rows{r.ld, r.bs};
+}
+inline bool rows_ok(const lz_rows& r) {
+  return r.ld >= 0 && r.bs >= 0 && r.ld < (int64_t(1) << 40) && r.bs < (int64_t(1) << 50);
+}
+
+// Whether 16-byte vectors of VW elements can be read from these rows
+inline bool rows_vec(const void* p, const Rows& r, int vw, size_t es) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (vw * es) == 0 && r.ld % vw == 0 && r.bs % vw == 0);
+}
+
+constexpr size_t kWsAlign = 256;
+inline size_t ws_round(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
+
+// Sum of P rows (ld floats apart) of c0 + c1 + c2 columns, in a fixed order,
+// handed out to up to three outputs (a NULL output is skipped).
+struct SumRowsParams {
+  const float* part;
+  int P;
+  size_t ld;
+  float* out0;
+  size_t c0;
+  float* out1;
+  size_t c1;
+  float* out2;
+  size_t c2;
+};
+cudaError_t launch_sum_rows(const SumRowsParams& p, cudaStream_t s);
+
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 148;
+  }
+  return n;
+}
+
+size_t conv_bwd_ws(const lz_conv_dims* d);
+size_t scan_ws(const lz_scan_dims* d, int which);
+size_t norm_bwd_ws(const lz_norm_dims* d);
+
+}  // namespace lz

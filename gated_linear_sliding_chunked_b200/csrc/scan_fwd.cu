@@ -1,0 +1,479 @@
+// Selective state space scan, forward and single tokens.
+#include "scan.cuh"
+
+namespace lz {
+namespace scan {
+namespace {
+
+// tokens of a tile
+template <int L>
+constexpr int tile() { return L >= 4 ? 32 : 16; }
+
+template <typename IO, int L>
+struct alignas(16) Smem {
+  static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP, TT = tile<L>();
+  IO u[2][TT * CH], dt[2][TT * CH], z[2][TT * CH];
+  IO b[2][TT * NP], c[2][TT * NP];
+  float2 dd[TT * CH];  // delta, delta * u
+  float bf[TT * NP], cf[TT * NP];
+  float ys[TT * Geo<L>::YS];
+};
+
+// One block: 128/L channels of one sequence over one segment of its tokens.
+// END: only the segment's effect on the state (its end value from a zero
+// start and the sum of delta), which the blocks of the later segments fold
+// into the state they start from.
+template <typename IO, int L, bool END>
+__global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
+  using G = Geo<L>;
+  using S = Smem<IO, L>;
+  constexpr int CH = G::CH, NP = G::NP, TT = S::TT, U = G::U;
+  constexpr int VW = 16 / (int)sizeof(IO);
+  extern __shared__ __align__(16) char raw[];
+  S& sm = *reinterpret_cast<S*>(raw);
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int g = blockIdx.x / p.nct, ct = blockIdx.x % p.nct;
+  const int b = blockIdx.y, seg = blockIdx.z;
+  const int per = p.D / p.G;
+  const int c0 = g * per + ct * CH, cmax = (g + 1) * per;  // channels of the block
+  const int cl = tid / L, l = tid % L, c = c0 + cl;        // this thread's channel and lane
+  const int n0 = 4 * l;
+  const bool on = c < cmax && n0 < p.N;
+  const int Tb = seq_len(p.lens, b, p.T);
+  const int t0 = seg * p.seg, t1 = min(p.T, t0 + p.seg), te = min(t1, Tb);
+  const size_t sidx = ((size_t)b * p.D + c) * p.N + n0;  // [B][D][N]
+  const size_t sstep = (size_t)p.B * p.D * p.N;
+
+  f2 A2[2] = {0, 0}, h[2] = {0, 0};
+  if (on) {
+    const float4 a = *reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0);
+    A2[0] = pk(a.x * kLog2e, a.y * kLog2e);
+    A2[1] = pk(a.z * kLog2e, a.w * kLog2e);
+    if (!END) {
+      if (p.h0) {
+        const float4 x = *reinterpret_cast<const float4*>(p.h0 + sidx);
+        h[0] = pk(x.x, x.y);
+        h[1] = pk(x.z, x.w);
+      }
+      for (int s = 0; s < seg; ++s) {
+        const float4 x = *reinterpret_cast<const float4*>(p.segE + s * sstep + sidx);
+        const float d = p.segD[((size_t)s * p.B + b) * p.D + c];
+        h[0] = fma2(ex2v(mul2(A2[0], pk(d, d))), h[0], pk(x.x, x.y));
+        h[1] = fma2(ex2v(mul2(A2[1], pk(d, d))), h[1], pk(x.z, x.w));
+      }
+    }
+  }
+  float sumd = 0.f;
+
+  auto load = [&](int t, int st) {
+    stage<IO, TT, CH, VW>(sm.u[st], p.u, p.ru, b, t, te, c0, cmax, p.vec);
+    stage<IO, TT, CH, VW>(sm.dt[st], p.dt, p.rdt, b, t, te, c0, cmax, p.vec);
+    stage<IO, TT, NP, 4>(sm.b[st], p.Bm, p.rb, b, t, te, g * p.N, g * p.N + p.N, p.vecbc);
+    if (!END) {
+      if (p.z) stage<IO, TT, CH, VW>(sm.z[st], p.z, p.rz, b, t, te, c0, cmax, p.vec);
+      stage<IO, TT, NP, 4>(sm.c[st], p.Cm, p.rc, b, t, te, g * p.N, g * p.N + p.N, p.vecbc);
+    }
+    cp_commit();
+  };
+  if (t0 < te) load(t0, 0);
+  int st = 0;
+  for (int t = t0; t < te; t += TT, st ^= 1) {
+    cp_wait_all();
+    __syncthreads();
+    for (int i = tid; i < TT * CH; i += NT) {
+      float dl = 0.f, u = 0.f;
+      const int cc = c0 + i % CH;
+      if (t + i / CH < te && cc < cmax) {
+        dl = to_f(sm.dt[st][i]) + (p.dtb ? p.dtb[cc] : 0.f);
+        if (p.softplus) dl = softplus(dl);
+        u = to_f(sm.u[st][i]);
+      }
+      sm.dd[i] = make_float2(dl, dl * u);
+    }
+    for (int i = tid; i < TT * NP; i += NT) {
+      sm.bf[i] = to_f(sm.b[st][i]);
+      if (!END) sm.cf[i] = to_f(sm.c[st][i]);
+    }
+    __syncthreads();
+    if (t + TT < te) load(t + TT, st ^ 1);
+#pragma unroll 2
+    for (int i = 0; i < TT; i += U) {
+      float yv[U];
+      if (!END && p.states && on && i % kCk == 0 && t + i < te) {
+        const size_t k = ((size_t)b * ((p.T + kCk - 1) / kCk) + (t + i) / kCk) * p.D + c;
+        *reinterpret_cast<float4*>(p.states + k * p.N + n0) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const float2 dd = sm.dd[(i + j) * CH + cl];
+        const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(&sm.bf[(i + j) * NP + n0]);
+        const f2 d2 = pk(dd.x, dd.x), du2 = pk(dd.y, dd.y);
+        h[0] = fma2(ex2v(mul2(A2[0], d2)), h[0], mul2(du2, B4.x));
+        h[1] = fma2(ex2v(mul2(A2[1], d2)), h[1], mul2(du2, B4.y));
+        if (END) {
+          sumd += dd.x;
+        } else {
+          const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(&sm.cf[(i + j) * NP + n0]);
+          const f2 y2 = fma2(h[1], C4.y, mul2(h[0], C4.x));
+          yv[j] = lo(y2) + hi(y2);
+        }
+      }
+      if (!END) {
+        int j = 0;
+        reduce_scatter<U, L / 2, 1>(yv, lane, j);
+        if (l % (L / U) == 0) sm.ys[(i + j) * G::YS + cl] = yv[0];
+      }
+    }
+    if (!END && p.y) {
+      __syncthreads();
+      if (p.vec) {
+        for (int i = tid; i < TT * (CH / VW); i += NT) {
+          const int tt = i / (CH / VW), cc = i % (CH / VW) * VW;
+          if (t + tt < te && c0 + cc < cmax) {
+            float o[VW], u[VW], z[VW];
+            load_vec<VW>(&sm.u[st][tt * CH + cc], u);
+            if (p.z) load_vec<VW>(&sm.z[st][tt * CH + cc], z);
+#pragma unroll
+            for (int e = 0; e < VW; ++e) {
+              o[e] = sm.ys[tt * G::YS + cc + e];
+              if (p.Dskip) o[e] = fmaf(p.Dskip[c0 + cc + e], u[e], o[e]);
+              if (p.z) o[e] *= z[e] * sigmoid(z[e]);
+            }
+            store_vec<VW>((IO*)p.y + ((size_t)b * p.T + t + tt) * p.D + c0 + cc, o);
+          }
+        }
+      } else {
+        for (int i = tid; i < TT * CH; i += NT) {
+          const int tt = i / CH, cc = i % CH;
+          if (t + tt < te && c0 + cc < cmax) {
+            float o = sm.ys[tt * G::YS + cc];
+            if (p.Dskip) o = fmaf(p.Dskip[c0 + cc], to_f(sm.u[st][i]), o);
+            if (p.z) {
+              const float z = to_f(sm.z[st][i]);
+              o *= z * sigmoid(z);
+            }
+            ((IO*)p.y)[((size_t)b * p.T + t + tt) * p.D + c0 + cc] = from_f<IO>(o);
+          }
+        }
+      }
+    }
+  }
+  const float4 hv = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
+  if (END) {
+    if (on) *reinterpret_cast<float4*>(p.segE + seg * sstep + sidx) = hv;
+    if (c < cmax && l == 0) p.segD[((size_t)seg * p.B + b) * p.D + c] = sumd;
+    return;
+  }
+  // a segment behind the sequence's end passes the state on
+  if (p.hT && on && seg == p.nseg - 1) *reinterpret_cast<float4*>(p.hT + sidx) = hv;
+  if (p.y) {
+    for (int t = max(t0, te); t < t1; ++t)
+      for (int i = tid; i < CH; i += NT)
+        if (c0 + i < cmax) ((IO*)p.y)[((size_t)b * p.T + t) * p.D + c0 + i] = from_f<IO>(0.f);
+  }
+}
+
+template <typename IO, int L>
+cudaError_t go(const ScanParams& p, cudaStream_t s) {
+  const size_t smem = sizeof(Smem<IO, L>);
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.nseg > 1) {
+    ScopedTiming tm("scan_fwd_ends", s);
+    scan_fwd_kernel<IO, L, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), NT, smem, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  ScopedTiming tm("scan_fwd", s);
+  scan_fwd_kernel<IO, L, false><<<dim3(p.G * p.nct, p.B, p.nseg), NT, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+// ---- single tokens --------------------------------------------------------
+// The state is read and written once: bound by HBM (or L2, when it fits).
+// One thread per 4 states; the L lanes of a channel add their share of y.
+template <typename IO, int L>
+__global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p, float* state) {
+  const size_t idx = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const int l = threadIdx.x % L;
+  const size_t bc = idx / L;
+  const bool row = bc < (size_t)p.B * p.D;
+  const int b = row ? (int)(bc / p.D) : 0, c = row ? (int)(bc % p.D) : 0;
+  const int g = c / (p.D / p.G), n0 = 4 * l;
+  const bool on = row && n0 < p.N;
+  float y = 0.f, u = 0.f;
+  if (on) {
+    float4* hp = reinterpret_cast<float4*>(state + bc * p.N + n0);
+    float4 h = *hp;
+    const float4 a = *reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0);
+    const IO* bp = (const IO*)p.Bm + p.rb.at(b, 0) + (size_t)g * p.N + n0;
+    const IO* cp = (const IO*)p.Cm + p.rc.at(b, 0) + (size_t)g * p.N + n0;
+    u = to_f(((const IO*)p.u)[p.ru.at(b, 0) + c]);
+    float d = to_f(((const IO*)p.dt)[p.rdt.at(b, 0) + c]) + (p.dtb ? p.dtb[c] : 0.f);
+    if (p.softplus) d = softplus(d);
+    const float du = d * u, d2 = d * kLog2e;
+    float B4[4], C4[4];
+    if (p.vecbc) {
+      load_vec<4>(bp, B4);
+      load_vec<4>(cp, C4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        B4[e] = to_f(bp[e]);
+        C4[e] = to_f(cp[e]);
+      }
+    }
+    h.x = fmaf(ex2(d2 * a.x), h.x, du * B4[0]);
+    h.y = fmaf(ex2(d2 * a.y), h.y, du * B4[1]);
+    h.z = fmaf(ex2(d2 * a.z), h.z, du * B4[2]);
+    h.w = fmaf(ex2(d2 * a.w), h.w, du * B4[3]);
+    *hp = h;
+    y = h.x * C4[0] + h.y * C4[1] + h.z * C4[2] + h.w * C4[3];
+  }
+#pragma unroll
+  for (int m = L / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+  if (row && l == 0) {
+    if (p.Dskip) y = fmaf(p.Dskip[c], u, y);
+    if (p.z) {
+      const float z = to_f(((const IO*)p.z)[p.rz.at(b, 0) + c]);
+      y *= z * sigmoid(z);
+    }
+    ((IO*)p.y)[bc] = from_f<IO>(y);
+  }
+}
+
+template <typename IO, int L>
+cudaError_t go_step(const ScanParams& p, float* state, cudaStream_t s) {
+  const size_t n = (size_t)p.B * p.D * L;
+  ScopedTiming tm("scan_step", s);
+  scan_step_kernel<IO, L><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, state);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace scan
+
+#define LZ_LANES(CALL)                                       \
+  switch (L) {                                               \
+    case 1: return bf ? CALL(bf16, 1) : CALL(float, 1);      \
+    case 2: return bf ? CALL(bf16, 2) : CALL(float, 2);      \
+    case 4: return bf ? CALL(bf16, 4) : CALL(float, 4);      \
+    case 8: return bf ? CALL(bf16, 8) : CALL(float, 8);      \
+    case 16: return bf ? CALL(bf16, 16) : CALL(float, 16);   \
+  }                                                          \
+  return cudaErrorInvalidValue;
+
+cudaError_t launch_scan_fwd(const scan::ScanParams& p, int L, bool bf, cudaStream_t s) {
+#define LZ_CALL(IO, LL) scan::go<IO, LL>(p, s)
+  LZ_LANES(LZ_CALL)
+#undef LZ_CALL
+}
+
+static cudaError_t launch_scan_step(const scan::ScanParams& p, float* state, int L, bool bf, cudaStream_t s) {
+#define LZ_CALL(IO, LL) scan::go_step<IO, LL>(p, state, s)
+  LZ_LANES(LZ_CALL)
+#undef LZ_CALL
+}
+
+// ---- host -----------------------------------------------------------------
+
+namespace {
+
+using scan::ScanParams;
+
+lz_status check_scan(const char* fn, const lz_scan_dims* d) {
+  if (!d) return layer_fail(LZ_ERR_INVALID_ARG, "%s: dims must not be NULL", fn);
+  if (d->B < 0 || d->T < 0 || d->D < 0)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: B, T, D must be >= 0 (got %d, %d, %d)", fn, d->B, d->T, d->D);
+  if (!io_ok(d->io))
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: io dtype %d is not LZ_F32 or LZ_BF16", fn, (int)d->io);
+  if (d->N < 4 || d->N > 64 || d->N % 4)
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: N must be a multiple of 4 in [4, 64] (got %d)", fn, d->N);
+  if (d->G < 1 || d->D % d->G)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: G must be a divisor of D (got %d of %d)", fn, d->G, d->D);
+  if (d->softplus != 0 && d->softplus != 1)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: softplus must be 0 or 1 (got %d)", fn, d->softplus);
+  if (!rows_ok(d->u) || !rows_ok(d->dt) || !rows_ok(d->z) || !rows_ok(d->b) || !rows_ok(d->c))
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: bad row strides", fn);
+  // keeps grid dimensions and 32-bit token indices in range
+  if (d->B > 65535 || d->T > (1 << 23) || d->D > (1 << 24))
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: problem too large (B %d, T %d, D %d)", fn, d->B, d->T, d->D);
+  return LZ_OK;
+}
+
+// Channel tiles, and the segments that a sequence is cut into when there are
+// too few channels and sequences to fill the device.  A segmented call runs
+// the recurrence twice (ends, then outputs), so it pays from three segments
+// on; kFull blocks are taken as a full device.
+constexpr int kFull = 148;
+void plan(const lz_scan_dims* d, int* nct, int* seg, int* nseg) {
+  const int L = scan::lanes_of(d->N), CH = scan::NT / L;
+  const int per = d->D / d->G;
+  *nct = (per + CH - 1) / CH;
+  const int64_t base = (int64_t)*nct * d->G * d->B;
+  int n = 1;
+  if (base > 0 && base * 3 <= kFull * 2) n = (int)std::min<int64_t>(32, kFull * 4 / base);
+  int len = ((d->T + n - 1) / n + 31) / 32 * 32;
+  len = std::max(len, 64);
+  *seg = len;
+  *nseg = std::max(1, (d->T + len - 1) / len);
+}
+
+size_t state_bytes(const lz_scan_dims* d) {
+  return (size_t)d->B * ((d->T + scan::kCk - 1) / scan::kCk) * d->D * d->N * sizeof(float);
+}
+
+struct Ws {
+  size_t segE, segD, part, bc, states, total;
+};
+Ws ws_of(const lz_scan_dims* d, bool bwd) {
+  int nct, seg, nseg;
+  plan(d, &nct, &seg, &nseg);
+  const size_t bd = (size_t)d->B * d->D;
+  Ws w{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o += ws_round(bytes); return at; };
+  w.segE = take(nseg > 1 ? nseg * bd * d->N * sizeof(float) : 0);
+  w.segD = take(nseg > 1 ? nseg * bd * sizeof(float) : 0);
+  if (bwd) {
+    w.part = take((size_t)d->B * nseg * scan::part_ld(d->D, d->N) * sizeof(float));
+    w.bc = take((size_t)nct * d->B * d->T * d->G * 2 * d->N * sizeof(float));
+    w.states = take(state_bytes(d));  // used when the caller gives none
+  }
+  w.total = o;
+  return w;
+}
+
+ScanParams params_of(const lz_scan_dims* d, const void* u, const void* dt, const float* A, const void* Bm,
+                     const void* Cm, const float* Dskip, const void* z, const float* dtb) {
+  ScanParams p{};
+  p.B = d->B; p.T = d->T; p.D = d->D; p.G = d->G; p.N = d->N; p.softplus = d->softplus;
+  plan(d, &p.nct, &p.seg, &p.nseg);
+  const int bcw = d->G * d->N;
+  p.ru = rows_of(d->u, d->T, d->D);
+  p.rdt = rows_of(d->dt, d->T, d->D);
+  p.rz = rows_of(d->z, d->T, d->D);
+  p.rb = rows_of(d->b, d->T, bcw);
+  p.rc = rows_of(d->c, d->T, bcw);
+  p.u = u; p.dt = dt; p.A = A; p.Bm = Bm; p.Cm = Cm; p.Dskip = Dskip; p.z = z; p.dtb = dtb;
+  const size_t es = esize(d->io);
+  const int vw = (int)(16 / es);
+  p.vec = (d->D / d->G) % vw == 0 && rows_vec(u, p.ru, vw, es) && rows_vec(dt, p.rdt, vw, es) &&
+          rows_vec(z, p.rz, vw, es);
+  p.vecbc = rows_vec(Bm, p.rb, 4, es) && rows_vec(Cm, p.rc, 4, es);
+  return p;
+}
+
+}  // namespace
+
+size_t scan_ws(const lz_scan_dims* d, int which) {
+  if (check_scan("lz_layer_workspace_bytes", d) != LZ_OK) return 0;
+  if (which == LZ_WS_SCAN_STATES) return state_bytes(d);
+  return ws_of(d, which == LZ_WS_SCAN_BWD).total;
+}
+
+}  // namespace lz
+
+using namespace lz;
+
+extern "C" lz_status lz_scan_fwd(const lz_scan_dims* d, const void* u, const void* dt, const float* A,
+                                 const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                 const float* dt_bias, const float* h0, const int64_t* lens, void* y, float* hT,
+                                 float* states, void* ws, size_t ws_bytes, lz_stream stream) {
+  const char* fn = "lz_scan_fwd";
+  lz_status st = check_scan(fn, d);
+  if (st != LZ_OK) return st;
+  if (d->B == 0 || d->D == 0 || (d->T == 0 && !hT)) return layer_done(cudaSuccess, fn);
+  const unsigned es = (unsigned)esize(d->io);
+  const bool data = d->T > 0;
+  const Ws w = ws_of(d, false);
+  st = check_ptrs(fn, {{u, "u", data, es}, {dt, "dt", data, es}, {A, "A", true, 16}, {Bm, "Bm", data, es},
+                       {Cm, "Cm", data, es}, {Dskip, "Dskip", false, 16}, {z, "z", false, es},
+                       {dt_bias, "dt_bias", false, 16}, {h0, "h0", false, 16}, {lens, "lens", false, 8},
+                       {y, "y", false, 16}, {hT, "hT", false, 16}, {states, "states", false, 16},
+                       {ws, "workspace", w.total > 0, 256}});
+  if (st == LZ_OK) st = check_distinct(fn, {y, hT, states, w.total ? ws : nullptr}, {u, dt, A, Bm, Cm, z, h0});
+  if (st != LZ_OK) return st;
+  if (ws_bytes < w.total)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: workspace too small (%zu bytes, need %zu)", fn, ws_bytes, w.total);
+  ScanParams p = params_of(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias);
+  p.h0 = h0; p.lens = lens; p.y = y; p.hT = hT; p.states = states;
+  p.segE = (float*)((char*)ws + w.segE);
+  p.segD = (float*)((char*)ws + w.segD);
+  return layer_done(launch_scan_fwd(p, scan::lanes_of(d->N), d->io == LZ_BF16, (cudaStream_t)stream), fn);
+}
+
+extern "C" lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const void* dt, const float* A,
+                                 const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                 const float* dt_bias, const float* h0, const int64_t* lens, const void* dy,
+                                 const float* dhT, const float* states, void* du, void* ddt, float* dA, void* dB,
+                                 void* dC, float* dDskip, float* ddt_bias, void* dz, float* dh0, void* ws,
+                                 size_t ws_bytes, lz_stream stream) {
+  const char* fn = "lz_scan_bwd";
+  lz_status st = check_scan(fn, d);
+  if (st != LZ_OK) return st;
+  if (d->D == 0) return layer_done(cudaSuccess, fn);
+  const unsigned es = (unsigned)esize(d->io);
+  const bool data = d->T > 0 && d->B > 0;
+  const Ws w = ws_of(d, true);
+  st = check_ptrs(fn, {{u, "u", data, es}, {dt, "dt", data, es}, {A, "A", true, 16}, {Bm, "Bm", data, es},
+                       {Cm, "Cm", data, es}, {Dskip, "Dskip", false, 16}, {z, "z", data && dz, es},
+                       {dt_bias, "dt_bias", false, 16}, {h0, "h0", false, 16}, {lens, "lens", false, 8},
+                       {dy, "dy", data, 16}, {dhT, "dhT", false, 16}, {states, "states", false, 16},
+                       {du, "du", data, 16}, {ddt, "ddt", data, 16}, {dA, "dA", true, 16}, {dB, "dB", data, 16},
+                       {dC, "dC", data, 16}, {dDskip, "dDskip", false, 16}, {ddt_bias, "ddt_bias", false, 16},
+                       {dz, "dz", false, 16}, {dh0, "dh0", false, 16}, {ws, "workspace", w.total > 0, 256}});
+  if (st == LZ_OK)
+    st = check_distinct(fn, {du, ddt, dA, dB, dC, dDskip, ddt_bias, dz, dh0, ws},
+                        {u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, dy, dhT, states});
+  if (st != LZ_OK) return st;
+  if (ws_bytes < w.total)
+    return layer_fail(LZ_ERR_INVALID_ARG, "%s: workspace too small (%zu bytes, need %zu)", fn, ws_bytes, w.total);
+  ScanParams p = params_of(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias);
+  const int L = scan::lanes_of(d->N);
+  const bool bf = d->io == LZ_BF16;
+  cudaStream_t s = (cudaStream_t)stream;
+  p.h0 = h0; p.lens = lens;
+  p.segE = (float*)((char*)ws + w.segE);
+  p.segD = (float*)((char*)ws + w.segD);
+  cudaError_t e = cudaSuccess;
+  p.states = const_cast<float*>(states);
+  if (!states && data) {
+    p.states = (float*)((char*)ws + w.states);
+    e = launch_scan_fwd(p, L, bf, s);
+  }
+  p.dy = dy; p.dhT = dhT; p.du = du; p.ddt = ddt; p.dz = dz; p.dh0 = dh0; p.dB = dB; p.dC = dC;
+  p.part = (float*)((char*)ws + w.part);
+  p.bc = (float*)((char*)ws + w.bc);
+  if (e == cudaSuccess && d->B > 0) e = launch_scan_bwd(p, L, bf, s);
+  if (e == cudaSuccess)
+    e = launch_sum_rows({p.part, d->B * p.nseg, scan::part_ld(d->D, d->N), dA, (size_t)d->D * d->N, dDskip,
+                         (size_t)d->D, ddt_bias, (size_t)d->D},
+                        s);
+  return layer_done(e, fn);
+}
+
+extern "C" lz_status lz_scan_step(const lz_scan_dims* d, float* state, const void* u, const void* dt,
+                                  const float* A, const void* Bm, const void* Cm, const float* Dskip,
+                                  const void* z, const float* dt_bias, void* y, lz_stream stream) {
+  const char* fn = "lz_scan_step";
+  lz_status st = check_scan(fn, d);
+  if (st != LZ_OK) return st;
+  if (d->B == 0 || d->D == 0) return layer_done(cudaSuccess, fn);
+  const unsigned es = (unsigned)esize(d->io);
+  st = check_ptrs(fn, {{state, "state", true, 16}, {u, "u", true, es}, {dt, "dt", true, es}, {A, "A", true, 16},
+                       {Bm, "Bm", true, es}, {Cm, "Cm", true, es}, {Dskip, "Dskip", false, 16}, {z, "z", false, es},
+                       {dt_bias, "dt_bias", false, 16}, {y, "y", true, 16}});
+  if (st == LZ_OK) st = check_distinct(fn, {state, y}, {u, dt, A, Bm, Cm, Dskip, z, dt_bias});
+  if (st != LZ_OK) return st;
+  lz_scan_dims one = *d;
+  one.T = 1;
+  ScanParams p = params_of(&one, u, dt, A, Bm, Cm, Dskip, z, dt_bias);
+  p.y = y;
+  return layer_done(
+      launch_scan_step(p, state, scan::lanes_of(d->N), d->io == LZ_BF16, (cudaStream_t)stream), fn);
+}

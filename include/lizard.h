@@ -303,6 +303,163 @@ lz_status lz_qkg_projection(int B, int T, int Dm, int H, int dk, const void* x,
                             float gate_scale, void* q, void* k, float* g,
                             lz_stream stream);
 
+/* ---- Layer operators around the recurrences ------------------------------
+ * What stands between the mixers of a layer stack: a short causal
+ * convolution in front of a recurrence, the selective state space scan (a
+ * recurrence whose decay depends on channel, state and token, which the gated
+ * branch's per-key-dim gates cannot express), and the norms before and after
+ * a block with its gate and residual scale.  The pages have no counterpart.
+ *
+ * Conventions of this section, beside those at the top:
+ * - Activations are [B, T, D] rows of D channels, io dtype.  The inputs that
+ *   the dims structs give an lz_rows for may be strided (a slice of a joint
+ *   projection's rows, a range of tokens, one sequence shared by the batch)
+ *   and only need their element's alignment; everything else is contiguous
+ *   and 16-byte aligned.  Outputs and gradients are contiguous, and no output
+ *   may overlap an input or another output (what is "in place" excepted).
+ * - Parameters (taps, rates, biases, norm weights), states and parameter
+ *   gradients are fp32.  Sums, states and statistics are held in fp32;
+ *   outputs are rounded once.  Parameter gradients are summed in a fixed
+ *   order: the same bits on every run.
+ * - lens (nullable): [B] int64 on the device, the tokens of each sequence of
+ *   a right-padded batch (clamped to [0, T]).  Inputs behind a sequence's end
+ *   are not read (NaN may stand there), outputs and gradients behind it are
+ *   written as zeros, and final states are those after its last token.
+ * - Scratch: lz_layer_workspace_bytes; it needs no clearing. */
+
+/* Rows of a strided input: elements from token to token, and from sequence to
+ * sequence.  ld = 0: contiguous rows ([B, T, width]; bs is then ignored).
+ * ld > 0: both as given (bs = 0: every sequence reads the same rows). */
+typedef struct {
+  int64_t ld, bs;
+} lz_rows;
+
+/* Short causal convolution over the tokens, a channel at a time:
+ *   p_t = bias + sum_{j < K} taps[j] x_{t-K+1+j},   y_t = silu(p_t) or p_t
+ * x before the first token is the history x0 [B,K-1,D] (oldest first). */
+typedef struct {
+  int B, T, D;
+  int K;        /* taps, 1 .. 8 */
+  lz_dtype io;
+  int silu;     /* 1: y = p sigma(p); 0: y = p */
+  lz_rows x;
+} lz_conv_dims;
+
+/* w [D,K], bias [D] (nullable = 0), x0 nullable = zeros; xT (nullable)
+ * receives the history after the last token, [B,K-1,D] io dtype: the x0 of
+ * the tokens that follow, or the history that lz_conv_step continues. */
+lz_status lz_conv_fwd(const lz_conv_dims* d, const void* x, const float* w,
+                      const float* bias, const void* x0, const int64_t* lens,
+                      void* y, void* xT, lz_stream stream);
+
+/* Gradient of lz_conv_fwd.  dy [B,T,D]; dxT (nullable) = dL/dxT.  Writes dx
+ * [B,T,D], dw [D,K], dbias [D] (nullable), dx0 [B,K-1,D] (nullable).
+ * Scratch: LZ_WS_CONV_BWD. */
+lz_status lz_conv_bwd(const lz_conv_dims* d, const void* x, const float* w,
+                      const float* bias, const void* x0, const int64_t* lens,
+                      const void* dy, const void* dxT, void* dx, float* dw,
+                      float* dbias, void* dx0, void* ws, size_t ws_bytes,
+                      lz_stream stream);
+
+/* One generation step of B sequences: y [B,D] from x (sequence to sequence
+ * x.bs elements when x.ld > 0) and the history hist [B,K-1,D], which moves on
+ * by one token in place.  T is not used. */
+lz_status lz_conv_step(const lz_conv_dims* d, void* hist, const void* x,
+                       const float* w, const float* bias, void* y,
+                       lz_stream stream);
+
+/* Selective state space scan: per sequence, channel c and state n
+ *   delta_t = softplus(dt_t + dt_bias)  (or dt_t + dt_bias)
+ *   h_t = exp(delta_t A[c,n]) h_{t-1} + delta_t u_t B_t[g,n]
+ *   y_t = (sum_n C_t[g,n] h_t + Dskip u_t) * silu(z_t)
+ * with g the channel's group (consecutive runs of D/G channels). */
+typedef struct {
+  int B, T, D;
+  int G, N;       /* groups of B and C (a divisor of D); states per channel: a
+                   * multiple of 4, 4 .. 64 */
+  lz_dtype io;
+  int softplus;   /* 1: delta = softplus(dt + dt_bias); 0: delta = dt + dt_bias */
+  lz_rows u, dt, z, b, c;  /* rows of b and c: [G,N], contiguous within a token */
+} lz_scan_dims;
+
+/* u, dt [B,T,D]; A [D,N] (negative rates: delta A is the log-decay, at most
+ * 0 where the state is not to grow); Bm, Cm [B,T,G,N]; Dskip, dt_bias [D]
+ * (nullable = 0); z [B,T,D] (nullable: no gate); h0 [B,D,N] (nullable = 0).
+ * y [B,T,D] (nullable: states only); hT (nullable) [B,D,N]; states (nullable)
+ * receives what lz_scan_bwd takes, lz_layer_workspace_bytes(d,
+ * LZ_WS_SCAN_STATES) bytes.  Scratch: LZ_WS_SCAN_FWD. */
+lz_status lz_scan_fwd(const lz_scan_dims* d, const void* u, const void* dt,
+                      const float* A, const void* Bm, const void* Cm,
+                      const float* Dskip, const void* z, const float* dt_bias,
+                      const float* h0, const int64_t* lens, void* y, float* hT,
+                      float* states, void* ws, size_t ws_bytes,
+                      lz_stream stream);
+
+/* Gradient of lz_scan_fwd.  dy [B,T,D]; dhT (nullable) = dL/dhT; states
+ * (nullable): the forward's for these inputs (without them the call walks the
+ * sequence once more).  Writes du, ddt [B,T,D], dA [D,N], dB, dC [B,T,G,N]
+ * (io dtype) and, where the pointer is given, dDskip, ddt_bias [D], dz
+ * [B,T,D] (z must be given) and dh0 [B,D,N].  Scratch: LZ_WS_SCAN_BWD. */
+lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const void* dt,
+                      const float* A, const void* Bm, const void* Cm,
+                      const float* Dskip, const void* z, const float* dt_bias,
+                      const float* h0, const int64_t* lens, const void* dy,
+                      const float* dhT, const float* states, void* du,
+                      void* ddt, float* dA, void* dB, void* dC, float* dDskip,
+                      float* ddt_bias, void* dz, float* dh0, void* ws,
+                      size_t ws_bytes, lz_stream stream);
+
+/* One generation step of B sequences: state [B,D,N] in place; u, dt, z [B,D],
+ * Bm, Cm [B,G,N] (sequence to sequence bs elements when ld > 0); y [B,D].  T
+ * is not used. */
+lz_status lz_scan_step(const lz_scan_dims* d, float* state, const void* u,
+                       const void* dt, const float* A, const void* Bm,
+                       const void* Cm, const float* Dskip, const void* z,
+                       const float* dt_bias, void* y, lz_stream stream);
+
+/* Norms before and after a block, fused with its gate and residual scale:
+ *   m   = w ? rmsnorm over each of G groups of features (o) * w : o
+ *   out = [r +] m [* silu(z)] [* s]
+ *   n   = rmsnorm over all features (out as stored) * w2
+ * with rmsnorm(x) = x / sqrt(mean(x^2) + eps); z, s, r are left out when
+ * NULL, n is computed when w2 is given.  o is the block's output: rows
+ * [B,T,D], or with heads = 1 the attention's [B,G,T,D/G] (contiguous), which
+ * leaves as rows.  A norm alone is o and w (before a block), a residual
+ * update with the next block's norm is o, r, s and w2. */
+typedef struct {
+  int B, T, D;   /* D <= 16384 */
+  int G;         /* groups of the first norm, a divisor of D */
+  int heads;     /* 1: o is [B,G,T,D/G] */
+  lz_dtype io;
+  float eps;     /* > 0 */
+  lz_rows o, z, r;
+} lz_norm_dims;
+
+/* w, s, w2 [D]; out [B,T,D]; n [B,T,D] (with w2). */
+lz_status lz_block_norm_fwd(const lz_norm_dims* d, const void* o,
+                            const float* w, const void* z, const float* s,
+                            const void* r, const float* w2, void* out, void* n,
+                            lz_stream stream);
+
+/* Gradient of lz_block_norm_fwd.  dout, dn [B,T,D]: dL/d(out) and dL/dn (at
+ * least one; dn needs w2 and `out`, the forward's stored out).  Writes dOo
+ * (dL/do, o's shape) and, where the pointer is given, dz (with z), dr (dL/dr,
+ * [B,T,D]), dw, ds, dw2 [D] (dw2 with dn; dw with w; ds with s).  Scratch:
+ * LZ_WS_NORM_BWD. */
+lz_status lz_block_norm_bwd(const lz_norm_dims* d, const void* o,
+                            const float* w, const void* z, const float* s,
+                            const float* w2, const void* out, const void* dout,
+                            const void* dn, void* dOo, void* dz, void* dr,
+                            float* dw, float* ds, float* dw2, void* ws,
+                            size_t ws_bytes, lz_stream stream);
+
+/* Bytes of scratch (LZ_WS_SCAN_STATES: of the forward's `states`) for the
+ * dims struct that the entry point takes.  0 is possible, and returned for
+ * dims that the entry point refuses. */
+enum { LZ_WS_CONV_BWD = 16, LZ_WS_SCAN_FWD = 17, LZ_WS_SCAN_BWD = 18,
+       LZ_WS_SCAN_STATES = 19, LZ_WS_NORM_BWD = 20 };
+size_t lz_layer_workspace_bytes(const void* d, int which);
+
 /* ---- Context parallelism: one sequence over R ranks ----------------------
  * The pages run each layer on one device; splitting a long sequence into R
  * contiguous segments (rank r holds tokens [r Ts, (r+1) Ts) of every
