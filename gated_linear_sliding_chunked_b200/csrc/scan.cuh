@@ -1,11 +1,19 @@
 // Shared parts of the selective state space scan kernels.
 //
 // Layout of the work: a channel's N states lie across L = ceil(N/4) lanes
-// (rounded up to a power of two) of a warp, 4 states a lane, and a block of
-// 128 threads holds 128/L neighbouring channels of one sequence.  The tokens
-// are walked in tiles that are staged in shared memory; the state stays in
-// registers.  One exp per (token, channel, state) cannot be done without:
-// 16 a cycle and SM, which outweighs the tokens' bytes.
+// (rounded up to a power of two) of a warp, 4 states a lane, and the four scan
+// warps of a block hold 128/L neighbouring channels of one sequence, with the
+// state in registers.  The tokens are walked in tiles.  Four more warps do
+// what is elementwise in (token, channel): while the scan warps walk a tile,
+// they finish the outputs of the tile before and prepare the steps (softplus),
+// inputs and gates of the tile behind, whose global loads they issued a tile
+// earlier.  One block-wide barrier a tile hands the shared memory buffers over.
+// Without the split the scan warps would wait out the loads, the softplus and
+// the stores of every tile, with too few warps on an SM to hide it: a layer
+// has only (sequences x channels x N/4)/32 of them.
+//
+// One exp per (token, channel, state) cannot be done without: 16 a cycle and
+// SM, which outweighs the tokens' bytes.
 #pragma once
 
 #include "layer.cuh"
@@ -13,7 +21,9 @@
 namespace lz {
 namespace scan {
 
-constexpr int NT = 128;      // threads of a block
+constexpr int NS = 128;      // scan threads of a block
+constexpr int NE = 128;      // elementwise threads
+constexpr int NT = NS + NE;
 constexpr int kCk = 16;      // tokens between two saved states
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -22,7 +32,7 @@ struct ScanParams {
   int B, T, D, G, N, softplus;
   int nct;       // channel tiles of a group
   int seg, nseg; // tokens of a segment, segments
-  bool vec, vecbc;  // 16-byte rows of u, dt, z, dy and outputs; 4-element rows of B, C
+  bool vec, vecbc;  // rows of 16-byte vectors: u, dt, z, dy and outputs; of 4 elements: B, C
   Rows ru, rdt, rz, rb, rc;
   const void* u;
   const void* dt;
@@ -86,42 +96,92 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ f2 ex2v(f2 x) { return pk(ex2(lo(x)), ex2(hi(x))); }
 
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-
-template <int BYTES>
-__device__ __forceinline__ void cp_async(void* dst, const void* src) {
-  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative
+// sigma(x).  log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3, by the series
+// s + s^3/3 + .. + s^15/15 (the rest is below 2^-29 of it): accurate relative
+// to the result also where e is small, which is where steps live.
+__device__ __forceinline__ float softplus_parts(float x, float& e) {
+  e = ex2(-kLog2e * fabsf(x));
+  const float s = __fdividef(e, 2.f + e), q = s * s;
+  float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
+  p = fmaf(q, p, 1.f / 11.f);
+  p = fmaf(q, p, 1.f / 9.f);
+  p = fmaf(q, p, 1.f / 7.f);
+  p = fmaf(q, p, 1.f / 5.f);
+  p = fmaf(q, p, 1.f / 3.f);
+  const float t = s + s;
+  return fmaxf(x, 0.f) + fmaf(t * q, p, t);
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ float softplus(float x) {
+  float e;
+  return softplus_parts(x, e);
+}
 
-// Stages a tile of TT rows x W elements: rows t0 .. of sequence b, columns c0
-// .. ; what lies outside (t >= tmax, column >= cmax) becomes zero.  VW-element
-// asynchronous copies where the rows allow them, else plain loads.
-template <typename IO, int TT, int W, int VW>
-__device__ __forceinline__ void stage(IO* dst, const void* src, const Rows& r, int b, int t0, int tmax, int c0,
-                                      int cmax, bool vec) {
-  const IO* s = (const IO*)src;
-  if (vec) {
-    for (int i = threadIdx.x; i < TT * (W / VW); i += NT) {
-      const int t = i / (W / VW), c = i % (W / VW) * VW;
-      IO* d = dst + t * W + c;
-      if (t0 + t < tmax && c0 + c < cmax) {
-        cp_async<VW * (int)sizeof(IO)>(d, s + r.at(b, t0 + t) + c0 + c);
-      } else {
+// V consecutive elements of a row as they are in memory
+template <typename IO, int V>
+struct Pack {
+  static constexpr int W = V * (int)sizeof(IO) / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int e = 0; e < VW; ++e) d[e] = from_f<IO>(0.f);
+    for (int i = 0; i < W; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  // in 16-, 8- or 4-byte accesses when vec (the row allows it), else element
+  // by element; n of the V elements exist (all or none of them when vec)
+  __device__ __forceinline__ void load(const IO* p, int n, bool vec) {
+    if (vec) {
+      if (n <= 0) {
+        zero();
+        return;
+      }
+      if constexpr (W % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+          w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+        }
+      } else if constexpr (W % 2 == 0) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+        w[0] = x.x; w[1] = x.y;
+      } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      }
+    } else {
+      zero();
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) {
+          if constexpr (sizeof(IO) == 4) w[i] = __float_as_uint(p[i]);
+          else w[i / 2] |= (uint32_t)reinterpret_cast<const unsigned short*>(p)[i] << (16 * (i & 1));
+        }
+    }
+  }
+};
+
+// V values to consecutive elements, n of which exist
+template <typename IO, int V>
+__device__ __forceinline__ void store_n(IO* p, const float* x, int n, bool vec) {
+  constexpr int M = 16 / (int)sizeof(IO) < V ? 16 / (int)sizeof(IO) : V;
+  if (vec && M > 1) {
+    if (n > 0) {
+#pragma unroll
+      for (int i = 0; i < V; i += M) {
+        if constexpr (M == 2) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[i], x[i + 1]);
+          *reinterpret_cast<__nv_bfloat162*>(p + i) = h;
+        } else {
+          store_vec<M>(p + i, x + i);
+        }
       }
     }
   } else {
-    for (int i = threadIdx.x; i < TT * W; i += NT) {
-      const int t = i / W, c = i % W;
-      dst[i] = t0 + t < tmax && c0 + c < cmax ? s[r.at(b, t0 + t) + c0 + c] : from_f<IO>(0.f);
-    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = from_f<IO>(x[i]);
   }
 }
 
@@ -151,7 +211,7 @@ __device__ __forceinline__ void reduce_scatter(float (&v)[SZ], int lane, int& ba
 
 template <int L>
 struct Geo {
-  static constexpr int CH = NT / L;         // channels of a block
+  static constexpr int CH = NS / L;         // channels of a block
   static constexpr int NP = 4 * L;          // states, padded
   static constexpr int U = L < 4 ? L : 4;   // tokens whose lane sums are formed together
   static constexpr int PAD = 32 / L < 4 ? 4 : 32 / L;

@@ -20,44 +20,229 @@ namespace scan {
 namespace {
 
 constexpr int TB = kCk;  // tokens of a tile
-constexpr int kWarps = NT / 32;
+constexpr int kWarps = NS / 32;
 
-template <typename IO, int L>
+template <int L>
 struct alignas(16) Smem {
   static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP;
-  IO u[2][TB * CH], dt[2][TB * CH], z[2][TB * CH], dy[2][TB * CH];
-  IO b[2][TB * NP], c[2][TB * NP];
-  float4 q[TB * CH];  // delta, delta u, e, u
-  float bf[TB * NP], cf[TB * NP];
-  float gB[TB * Geo<L>::YS], gA[TB * Geo<L>::YS], yc[TB * Geo<L>::YS];
-  float red[kWarps][TB][2 * NP];  // dB, dC over a warp's channels
+  float4 q[2][TB * CH];  // delta, delta u, e
+  float bf[2][TB * NP], cf[2][TB * NP];
+  float gB[2][TB * Geo<L>::YS], gA[2][TB * Geo<L>::YS], yc[2][TB * Geo<L>::YS];
+  float red[2][kWarps][TB][2 * NP];  // dB, dC over a warp's channels
 };
 
 // END: only the gradient that the segment hands to the one before it when
 // none comes from behind (the state gradient before its first token).
 template <typename IO, int L, bool END>
-__global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams p) {
   using G = Geo<L>;
-  using S = Smem<IO, L>;
   constexpr int CH = G::CH, NP = G::NP, U = G::U, YS = G::YS;
-  constexpr int VW = 16 / (int)sizeof(IO);
+  constexpr int EV = TB * CH / NE > 1 ? (TB * CH / NE < 8 ? TB * CH / NE : 8) : 2;  // channels of an elementwise thread
+  constexpr int ROWT = CH / EV;                                 // threads of a token
+  constexpr int PASS = (TB * ROWT + NE - 1) / NE;               // tokens of a thread
+  constexpr int BN = TB * L > NE ? TB * L / NE : 1;             // its 4-element vectors of B and of C
   extern __shared__ __align__(16) char raw[];
-  S& sm = *reinterpret_cast<S*>(raw);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  Smem<L>& sm = *reinterpret_cast<Smem<L>*>(raw);
+  const int tid = threadIdx.x;
   const int g = blockIdx.x / p.nct, ct = blockIdx.x % p.nct;
   const int b = blockIdx.y, seg = END ? blockIdx.z + 1 : blockIdx.z;
   const int per = p.D / p.G;
   const int c0 = g * per + ct * CH, cmax = (g + 1) * per;
+  const int Tb = seq_len(p.lens, b, p.T);
+  const int t0 = seg * p.seg, t1 = min(p.T, t0 + p.seg), te = min(t1, Tb);
+  const int ntile = t0 < te ? (te - t0 + TB - 1) / TB : 0;
+  // step k of the walk back is tile ntile - 1 - k
+  float* part = p.part + ((size_t)b * p.nseg + seg) * part_ld(p.D, p.N);
+
+  if (tid >= NS) {
+    // ---- elementwise warps
+    const int et = tid - NS;
+    const int cl = et % ROWT * EV, c = c0 + cl, i0 = et / ROWT;  // channels; first token of the tile
+    constexpr int IS = NE / ROWT;                                // tokens between a thread's
+    const int nc = min(EV, cmax - c);
+    struct Next {
+      Pack<IO, EV> u, dt, z, dy;
+    };
+    struct Tok {  // what the outputs of a token need
+      float delta[EV], e[EV], u[EV], sg[EV], dzf[EV];
+    };
+    Next nx[PASS];
+    Pack<IO, 4> nb[BN], ncv[BN];
+    Tok cur[PASS], last[PASS];
+    float Ds[EV], bias[EV], sD[EV], sT[EV];
+#pragma unroll
+    for (int e = 0; e < EV; ++e) {
+      Ds[e] = p.Dskip && e < nc ? p.Dskip[c + e] : 0.f;
+      bias[e] = p.dtb && e < nc ? p.dtb[c + e] : 0.f;
+      sD[e] = sT[e] = 0.f;
+    }
+    const Rows rdy{p.D, (int64_t)p.T * p.D};
+    auto load = [&](int k) {
+      const int tt = t0 + (ntile - 1 - k) * TB;
+#pragma unroll
+      for (int s = 0; s < PASS; ++s) {
+        const int i = i0 + s * IS, t = tt + i;
+        const int n = i < TB && t < te ? nc : 0;
+        nx[s].dt.load((const IO*)p.dt + p.rdt.at(b, t) + c, n, p.vec);
+        nx[s].dy.load((const IO*)p.dy + rdy.at(b, t) + c, n, p.vec);
+        if (p.z) nx[s].z.load((const IO*)p.z + p.rz.at(b, t) + c, n, p.vec);
+        if (!END) nx[s].u.load((const IO*)p.u + p.ru.at(b, t) + c, n, p.vec);
+      }
+#pragma unroll
+      for (int j = 0; j < BN; ++j) {
+        const int v = et + j * NE, t = tt + v / L, n0 = v % L * 4;
+        const int n = v < TB * L && t < te ? p.N - n0 : 0;
+        ncv[j].load((const IO*)p.Cm + p.rc.at(b, t) + g * p.N + n0, n, p.vecbc);
+        if (!END) nb[j].load((const IO*)p.Bm + p.rb.at(b, t) + g * p.N + n0, n, p.vecbc);
+      }
+    };
+    auto prepare = [&](int k, Tok (&tok)[PASS]) {
+      const int tt = t0 + (ntile - 1 - k) * TB;
+#pragma unroll
+      for (int s = 0; s < PASS; ++s) {
+        const int i = i0 + s * IS;
+        if (i >= TB) continue;
+        const bool live = tt + i < te;
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+          float dl = 0.f, ee = 0.f, u = 0.f, sg = 1.f, dzf = 0.f;
+          if (live && e < nc) {
+            dl = nx[s].dt.get(e) + bias[e];
+            if (p.softplus) {
+              float x;
+              const float pre = dl;
+              dl = softplus_parts(pre, x);
+              sg = __fdividef(pre >= 0.f ? 1.f : x, 1.f + x);
+            }
+            ee = nx[s].dy.get(e);
+            if (p.z) {
+              const float z = nx[s].z.get(e), sz = sigmoid(z);
+              dzf = ee * sz * (1.f + z * (1.f - sz));
+              ee *= z * sz;
+            }
+            if (!END) u = nx[s].u.get(e);
+          }
+          tok[s].delta[e] = dl;
+          tok[s].e[e] = ee;
+          tok[s].u[e] = u;
+          tok[s].sg[e] = sg;
+          tok[s].dzf[e] = dzf;
+          sm.q[k & 1][i * CH + cl + e] = make_float4(dl, dl * u, ee, 0.f);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < BN; ++j) {
+        const int v = et + j * NE;
+        if (v < TB * L) {
+          *reinterpret_cast<float4*>(&sm.cf[k & 1][v * 4]) =
+              make_float4(ncv[j].get(0), ncv[j].get(1), ncv[j].get(2), ncv[j].get(3));
+          if (!END)
+            *reinterpret_cast<float4*>(&sm.bf[k & 1][v * 4]) =
+                make_float4(nb[j].get(0), nb[j].get(1), nb[j].get(2), nb[j].get(3));
+        }
+      }
+    };
+    auto finish = [&](int k, const Tok (&tok)[PASS]) {
+      const int tt = t0 + (ntile - 1 - k) * TB, w = k & 1;
+#pragma unroll
+      for (int s = 0; s < PASS; ++s) {
+        const int i = i0 + s * IS, t = tt + i;
+        if (i >= TB || t >= te) continue;
+        float du[EV], dd[EV], dz[EV];
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+          const float gB = sm.gB[w][i * YS + cl + e];
+          du[e] = fmaf(tok[s].delta[e], gB, Ds[e] * tok[s].e[e]);
+          dd[e] = fmaf(tok[s].u[e], gB, kLn2 * sm.gA[w][i * YS + cl + e]) * tok[s].sg[e];
+          sD[e] = fmaf(tok[s].e[e], tok[s].u[e], sD[e]);
+          sT[e] += dd[e];
+          if (p.dz) dz[e] = tok[s].dzf[e] * fmaf(Ds[e], tok[s].u[e], sm.yc[w][i * YS + cl + e]);
+        }
+        const size_t at = ((size_t)b * p.T + t) * p.D + c;
+        store_n<IO, EV>((IO*)p.du + at, du, nc, p.vec);
+        store_n<IO, EV>((IO*)p.ddt + at, dd, nc, p.vec);
+        if (p.dz) store_n<IO, EV>((IO*)p.dz + at, dz, nc, p.vec);
+      }
+      for (int v = et; v < TB * 2 * L; v += NE) {
+        const int i = v / (2 * L), n = v % L * 4, m = v % (2 * L) / L;
+        if (tt + i < te && n < p.N) {
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) {
+            const float4 r = *reinterpret_cast<const float4*>(&sm.red[w][x][i][m * NP + n]);
+            s.x += r.x; s.y += r.y; s.z += r.z; s.w += r.w;
+          }
+          *reinterpret_cast<float4*>(
+              &p.bc[(((((size_t)ct * p.B + b) * p.T + tt + i) * p.G + g) * 2 + m) * p.N + n]) = s;
+        }
+      }
+    };
+    if (!END) {
+      // behind the sequence's end: zeros
+      for (int t = max(t0, te); t < t1; ++t)
+        for (int x = et; x < CH; x += NE)
+          if (c0 + x < cmax) {
+            const size_t at = ((size_t)b * p.T + t) * p.D + c0 + x;
+            ((IO*)p.du)[at] = from_f<IO>(0.f);
+            ((IO*)p.ddt)[at] = from_f<IO>(0.f);
+            if (p.dz) ((IO*)p.dz)[at] = from_f<IO>(0.f);
+          }
+    }
+    if (ntile > 0) {
+      load(0);
+      prepare(0, cur);
+      if (ntile > 1) load(1);
+    }
+    __syncthreads();
+    for (int k = 0; k < ntile; ++k) {
+      // outputs of tile k - 1 first: its registers then take tile k + 1
+      if (!END && k > 0) finish(k - 1, last);
+#pragma unroll
+      for (int s = 0; s < PASS; ++s) last[s] = cur[s];
+      if (k + 1 < ntile) prepare(k + 1, cur);
+      if (k + 2 < ntile) load(k + 2);
+      __syncthreads();
+    }
+    if constexpr (!END) {
+      if (ntile > 0) finish(ntile - 1, last);
+      // sums of e u and ddt over the block's token rows, in order
+      float* s1 = &sm.red[0][0][0][0];
+      float* s2 = reinterpret_cast<float*>(sm.q);
+      asm volatile("bar.sync 1, %0;" ::"n"(NE) : "memory");
+#pragma unroll
+      for (int e = 0; e < EV; ++e) {
+        s1[i0 * CH + cl + e] = sD[e];
+        s2[i0 * CH + cl + e] = sT[e];
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(NE) : "memory");
+      for (int x = et; x < CH; x += NE)
+        if (c0 + x < cmax) {
+          float u = 0.f, v = 0.f;
+          for (int k = 0; k < IS && k < TB; ++k) {
+            u += s1[k * CH + x];
+            v += s2[k * CH + x];
+          }
+          part[(size_t)p.D * p.N + c0 + x] = u;
+          part[(size_t)p.D * (p.N + 1) + c0 + x] = v;
+        }
+    }
+    return;
+  }
+
+  // ---- scan warps
+  const int lane = tid % 32, warp = tid / 32;
   const int cl = tid / L, l = tid % L, c = c0 + cl;
   const int n0 = 4 * l;
   const bool on = c < cmax && n0 < p.N;
-  const int Tb = seq_len(p.lens, b, p.T);
-  const int t0 = seg * p.seg, t1 = min(p.T, t0 + p.seg), te = min(t1, Tb);
   const int nck = (p.T + kCk - 1) / kCk;
   const size_t sidx = ((size_t)b * p.D + c) * p.N + n0;
   const size_t sstep = (size_t)p.B * p.D * p.N;
-
-  f2 A2[2] = {0, 0}, gr[2] = {0, 0}, dA[2] = {0, 0};
+  const float* ckp = p.states + ((size_t)b * nck * p.D + c) * p.N + n0;
+  f2 A2[2] = {0, 0}, gr[2] = {0, 0}, dA[2] = {0, 0}, dAc[2] = {0, 0};
+  float4 ck = make_float4(0.f, 0.f, 0.f, 0.f);  // the state before the tile, loaded a tile ahead
+  auto load_ck = [&](int k) {
+    if (on) ck = __ldg(reinterpret_cast<const float4*>(ckp + (size_t)(t0 / kCk + ntile - 1 - k) * p.D * p.N));
+  };
   if (on) {
     const float4 a = *reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0);
     A2[0] = pk(a.x * kLog2e, a.y * kLog2e);
@@ -74,206 +259,115 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
         gr[0] = fma2(ex2v(mul2(A2[0], pk(d, d))), gr[0], pk(x.x, x.y));
         gr[1] = fma2(ex2v(mul2(A2[1], pk(d, d))), gr[1], pk(x.z, x.w));
       }
+      if (ntile > 0) load_ck(0);
     }
   }
   float sumd = 0.f;
-  // elementwise work: 4 neighbouring channels and every (NT / (CH/4))-th token
-  constexpr int QV = CH / 4, QT = NT / QV;
-  const int qc = tid % QV * 4, qt = tid / QV;
-  float sD[4] = {0, 0, 0, 0}, sT[4] = {0, 0, 0, 0};  // sums of e u and of ddt
-
-  auto load = [&](int t, int st) {
-    stage<IO, TB, CH, VW>(sm.dt[st], p.dt, p.rdt, b, t, te, c0, cmax, p.vec);
-    stage<IO, TB, CH, VW>(sm.dy[st], p.dy, Rows{p.D, (int64_t)p.T * p.D}, b, t, te, c0, cmax, p.vec);
-    if (p.z) stage<IO, TB, CH, VW>(sm.z[st], p.z, p.rz, b, t, te, c0, cmax, p.vec);
-    stage<IO, TB, NP, 4>(sm.c[st], p.Cm, p.rc, b, t, te, g * p.N, g * p.N + p.N, p.vecbc);
-    if (!END) {
-      stage<IO, TB, CH, VW>(sm.u[st], p.u, p.ru, b, t, te, c0, cmax, p.vec);
-      stage<IO, TB, NP, 4>(sm.b[st], p.Bm, p.rb, b, t, te, g * p.N, g * p.N + p.N, p.vecbc);
-    }
-    cp_commit();
-  };
-  // behind the sequence's end: zeros
-  if (!END) {
-    for (int t = max(t0, te); t < t1; ++t)
-      for (int i = tid; i < CH; i += NT)
-        if (c0 + i < cmax) {
-          const size_t at = ((size_t)b * p.T + t) * p.D + c0 + i;
-          ((IO*)p.du)[at] = from_f<IO>(0.f);
-          ((IO*)p.ddt)[at] = from_f<IO>(0.f);
-          if (p.dz) ((IO*)p.dz)[at] = from_f<IO>(0.f);
-        }
-  }
-  int t = t0 < te ? t0 + (te - 1 - t0) / TB * TB : t0 - 1;  // the last tile
-  if (t >= t0) load(t, 0);
-  int st = 0;
-  for (; t >= t0; t -= TB, st ^= 1) {
-    f2 h[2] = {0, 0};
-    if (!END && on) {
-      const float4 x = *reinterpret_cast<const float4*>(p.states + (((size_t)b * nck + t / kCk) * p.D + c) * p.N + n0);
-      h[0] = pk(x.x, x.y);
-      h[1] = pk(x.z, x.w);
-    }
-    cp_wait_all();
-    __syncthreads();
-    for (int i = tid; i < TB * CH; i += NT) {
-      float dl = 0.f, u = 0.f, e = 0.f;
-      const int cc = c0 + i % CH;
-      if (t + i / CH < te && cc < cmax) {
-        dl = to_f(sm.dt[st][i]) + (p.dtb ? p.dtb[cc] : 0.f);
-        if (p.softplus) dl = softplus(dl);
-        e = to_f(sm.dy[st][i]);
-        if (p.z) {
-          const float z = to_f(sm.z[st][i]);
-          e *= z * sigmoid(z);
-        }
-        if (!END) u = to_f(sm.u[st][i]);
-      }
-      sm.q[i] = make_float4(dl, dl * u, e, u);
-    }
-    for (int i = tid; i < TB * NP; i += NT) {
-      sm.cf[i] = to_f(sm.c[st][i]);
-      if (!END) sm.bf[i] = to_f(sm.b[st][i]);
-    }
-    __syncthreads();
-    if (t - TB >= t0) load(t - TB, st ^ 1);
-
+  __syncthreads();
+  for (int k = 0; k < ntile; ++k) {
+    const int w = k & 1;
+    const float4* q = sm.q[w] + cl;
+    const float* bf = sm.bf[w] + n0;
+    const float* cf = sm.cf[w] + n0;
     if constexpr (END) {
 #pragma unroll 4
       for (int i = TB - 1; i >= 0; --i) {
-        const float4 q = sm.q[i * CH + cl];
-        const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(&sm.cf[i * NP + n0]);
-        const f2 e2 = pk(q.z, q.z), d2 = pk(q.x, q.x);
+        const float4 x = q[i * CH];
+        const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(cf + i * NP);
+        const f2 e2 = pk(x.z, x.z), d2 = pk(x.x, x.x);
         gr[0] = mul2(fma2(e2, C4.x, gr[0]), ex2v(mul2(A2[0], d2)));
         gr[1] = mul2(fma2(e2, C4.y, gr[1]), ex2v(mul2(A2[1], d2)));
-        sumd += q.x;
+        sumd += x.x;
       }
     } else {
-    // ---- forward over the tile: a and p = a h_{t-1} of every token
-    f2 a[TB][2], pr[TB][2];
+      // forward over the tile: the state after every token, h[i + 1]
+      f2 h[TB + 1][2];
+      h[0][0] = pk(ck.x, ck.y);
+      h[0][1] = pk(ck.z, ck.w);
+      if (k + 1 < ntile) load_ck(k + 1);
 #pragma unroll
-    for (int i = 0; i < TB; i += U) {
-      float yv[U];
+      for (int i = 0; i < TB; i += U) {
+        float yv[U];
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const float4 q = sm.q[(i + j) * CH + cl];
-        const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(&sm.bf[(i + j) * NP + n0]);
-        const f2 d2 = pk(q.x, q.x), du2 = pk(q.y, q.y);
-        a[i + j][0] = ex2v(mul2(A2[0], d2));
-        a[i + j][1] = ex2v(mul2(A2[1], d2));
-        pr[i + j][0] = mul2(a[i + j][0], h[0]);
-        pr[i + j][1] = mul2(a[i + j][1], h[1]);
-        h[0] = fma2(du2, B4.x, pr[i + j][0]);
-        h[1] = fma2(du2, B4.y, pr[i + j][1]);
-        if (p.dz) {
-          const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(&sm.cf[(i + j) * NP + n0]);
-          const f2 y2 = fma2(h[1], C4.y, mul2(h[0], C4.x));
-          yv[j] = lo(y2) + hi(y2);
-        }
-      }
-      if (p.dz) {
-        int j = 0;
-        reduce_scatter<U, L / 2, 1>(yv, lane, j);
-        if (l % (L / U) == 0) sm.yc[(i + j) * YS + cl] = yv[0];
-      }
-    }
-    // ---- and back
-#pragma unroll
-    for (int i = TB - U; i >= 0; i -= U) {
-      float vB[U], vA[U];
-#pragma unroll
-      for (int j = U - 1; j >= 0; --j) {
-        const int k = i + j;
-        const float4 q = sm.q[k * CH + cl];
-        const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(&sm.bf[k * NP + n0]);
-        const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(&sm.cf[k * NP + n0]);
-        const f2 d2 = pk(q.x, q.x), du2 = pk(q.y, q.y), e2 = pk(q.z, q.z);
-        gr[0] = fma2(e2, C4.x, gr[0]);
-        gr[1] = fma2(e2, C4.y, gr[1]);
-        const f2 dB0 = mul2(gr[0], du2), dB1 = mul2(gr[1], du2);
-        const f2 dC0 = mul2(fma2(du2, B4.x, pr[k][0]), e2), dC1 = mul2(fma2(du2, B4.y, pr[k][1]), e2);
-        const f2 sB = fma2(gr[1], B4.y, mul2(gr[0], B4.x));
-        const f2 gp0 = mul2(gr[0], pr[k][0]), gp1 = mul2(gr[1], pr[k][1]);
-        const f2 sA = fma2(gp1, A2[1], mul2(gp0, A2[0]));
-        dA[0] = fma2(gp0, d2, dA[0]);
-        dA[1] = fma2(gp1, d2, dA[1]);
-        gr[0] = mul2(gr[0], a[k][0]);
-        gr[1] = mul2(gr[1], a[k][1]);
-        vB[j] = lo(sB) + hi(sB);
-        vA[j] = lo(sA) + hi(sA);
-        float v[8] = {lo(dB0), hi(dB0), lo(dB1), hi(dB1), lo(dC0), hi(dC0), lo(dC1), hi(dC1)};
-        int base = 0;
-        reduce_scatter<8, 16, L>(v, lane, base);
-        // what is left of the 8: 1 for L <= 4 (equal in lanes that differ below
-        // bit 2 and from L up), 2 for L = 8, 4 for L = 16
-        constexpr int LEFT = L <= 4 ? 1 : L / 4;
-        if (L >= 4 || (lane & 3 & ~(L - 1)) == 0) {
-#pragma unroll
-          for (int x = 0; x < LEFT; ++x) {
-            const int y = base + x;
-            sm.red[warp][k][(y >> 2) * NP + n0 + (y & 3)] = v[x];
+        for (int j = 0; j < U; ++j) {
+          const float2 x = *reinterpret_cast<const float2*>(&q[(i + j) * CH]);
+          const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(bf + (i + j) * NP);
+          const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y);
+          const int m = i + j;
+          h[m + 1][0] = fma2(ex2v(mul2(A2[0], d2)), h[m][0], mul2(du2, B4.x));
+          h[m + 1][1] = fma2(ex2v(mul2(A2[1], d2)), h[m][1], mul2(du2, B4.y));
+          if (p.dz) {
+            const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(cf + m * NP);
+            const f2 y2 = fma2(h[m + 1][1], C4.y, mul2(h[m + 1][0], C4.x));
+            yv[j] = lo(y2) + hi(y2);
           }
         }
+        if (p.dz) {
+          int j = 0;
+          reduce_scatter<U, L / 2, 1>(yv, lane, j);
+          if (l % (L / U) == 0) sm.yc[w][(i + j) * YS + cl] = yv[0];
+        }
       }
-      int j = 0;
-      reduce_scatter<U, L / 2, 1>(vB, lane, j);
-      j = 0;
-      reduce_scatter<U, L / 2, 1>(vA, lane, j);
-      if (l % (L / U) == 0) {
-        sm.gB[(i + j) * YS + cl] = vB[0];
-        sm.gA[(i + j) * YS + cl] = vA[0];
+      // and back; a is taken again, which costs less than keeping it (and the
+      // compiler is kept from keeping it: 64 more registers would be spilled)
+      f2 R2[2] = {A2[0], A2[1]};
+      asm volatile("" : "+l"(R2[0]), "+l"(R2[1]));
+      f2 dt0 = 0, dt1 = 0;  // dA of the tile
+#pragma unroll
+      for (int i = TB - U; i >= 0; i -= U) {
+        float vB[U], vA[U];
+#pragma unroll
+        for (int j = U - 1; j >= 0; --j) {
+          const int m = i + j;
+          const float4 x = q[m * CH];
+          const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(bf + m * NP);
+          const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(cf + m * NP);
+          const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y), e2 = pk(x.z, x.z);
+          gr[0] = fma2(e2, C4.x, gr[0]);
+          gr[1] = fma2(e2, C4.y, gr[1]);
+          const f2 dB0 = mul2(gr[0], du2), dB1 = mul2(gr[1], du2);
+          const f2 dC0 = mul2(h[m + 1][0], e2), dC1 = mul2(h[m + 1][1], e2);
+          const f2 sB = fma2(gr[1], B4.y, mul2(gr[0], B4.x));
+          gr[0] = mul2(gr[0], ex2v(mul2(R2[0], d2)));
+          gr[1] = mul2(gr[1], ex2v(mul2(R2[1], d2)));
+          const f2 gp0 = mul2(gr[0], h[m][0]), gp1 = mul2(gr[1], h[m][1]);
+          const f2 sA = fma2(gp1, A2[1], mul2(gp0, A2[0]));
+          dt0 = fma2(gp0, d2, dt0);
+          dt1 = fma2(gp1, d2, dt1);
+          vB[j] = lo(sB) + hi(sB);
+          vA[j] = lo(sA) + hi(sA);
+          float v[8] = {lo(dB0), hi(dB0), lo(dB1), hi(dB1), lo(dC0), hi(dC0), lo(dC1), hi(dC1)};
+          int base = 0;
+          reduce_scatter<8, 16, L>(v, lane, base);
+          // what is left of the 8: 1 for L <= 4 (equal in the lanes that differ
+          // below bit 2 and from L up), 2 for L = 8, 4 for L = 16
+          constexpr int LEFT = L <= 4 ? 1 : L / 4;
+          if (L >= 4 || (lane & 3 & ~(L - 1)) == 0) {
+#pragma unroll
+            for (int y = 0; y < LEFT; ++y) {
+              const int z = base + y;
+              sm.red[w][warp][m][(z >> 2) * NP + n0 + (z & 3)] = v[y];
+            }
+          }
+        }
+        int j = 0;
+        reduce_scatter<U, L / 2, 1>(vB, lane, j);
+        j = 0;
+        reduce_scatter<U, L / 2, 1>(vA, lane, j);
+        if (l % (L / U) == 0) {
+          sm.gB[w][(i + j) * YS + cl] = vB[0];
+          sm.gA[w][(i + j) * YS + cl] = vA[0];
+        }
+      }
+      // dA over thousands of tiles: the sum carries the rounding of each addition on
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const f2 y = add2(x ? dt1 : dt0, dAc[x]), s = add2(dA[x], y);
+        dAc[x] = add2(y, mul2(pk(-1.f, -1.f), add2(s, mul2(pk(-1.f, -1.f), dA[x]))));
+        dA[x] = s;
       }
     }
     __syncthreads();
-    // ---- the tile's gradients
-    for (int i = qt; i < TB; i += QT) {
-      const bool live = t + i < te;
-      float du[4], dd[4], dz[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int x = i * CH + qc + e, cc = c0 + qc + e;
-        if (!live || cc >= cmax) continue;
-        const float4 q = sm.q[x];
-        const float Ds = p.Dskip ? p.Dskip[cc] : 0.f;
-        const float gB = sm.gB[i * YS + qc + e];
-        du[e] = fmaf(q.x, gB, Ds * q.z);
-        dd[e] = fmaf(q.w, gB, kLn2 * sm.gA[i * YS + qc + e]);
-        if (p.softplus) dd[e] *= sigmoid(to_f(sm.dt[st][x]) + (p.dtb ? p.dtb[cc] : 0.f));
-        sD[e] = fmaf(q.z, q.w, sD[e]);
-        sT[e] += dd[e];
-        if (p.dz) {
-          const float z = to_f(sm.z[st][x]), sg = sigmoid(z);
-          dz[e] = to_f(sm.dy[st][x]) * fmaf(Ds, q.w, sm.yc[i * YS + qc + e]) * sg * (1.f + z * (1.f - sg));
-        }
-      }
-      if (!live) continue;
-      const size_t at = ((size_t)b * p.T + t + i) * p.D + c0 + qc;
-      if (p.vec) {
-        if (c0 + qc < cmax) {
-          store_vec<4>((IO*)p.du + at, du);
-          store_vec<4>((IO*)p.ddt + at, dd);
-          if (p.dz) store_vec<4>((IO*)p.dz + at, dz);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c0 + qc + e < cmax) {
-            ((IO*)p.du)[at + e] = from_f<IO>(du[e]);
-            ((IO*)p.ddt)[at + e] = from_f<IO>(dd[e]);
-            if (p.dz) ((IO*)p.dz)[at + e] = from_f<IO>(dz[e]);
-          }
-      }
-    }
-    for (int i = tid; i < TB * 2 * NP; i += NT) {
-      const int k = i / (2 * NP), n = i % (2 * NP) % NP, w = i % (2 * NP) / NP;
-      if (t + k < te && n < p.N) {
-        float s = 0.f;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) s += sm.red[x][k][w * NP + n];
-        p.bc[(((((size_t)ct * p.B + b) * p.T + t + k) * p.G + g) * 2 + w) * p.N + n] = s;
-      }
-    }
-    }  // !END
   }
   const float4 gv = make_float4(lo(gr[0]), hi(gr[0]), lo(gr[1]), hi(gr[1]));
   if (END) {
@@ -282,30 +376,9 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
     return;
   }
   if (p.dh0 && on && seg == 0) *reinterpret_cast<float4*>(p.dh0 + sidx) = gv;
-  float* part = p.part + ((size_t)b * p.nseg + seg) * part_ld(p.D, p.N);
   if (on)
     *reinterpret_cast<float4*>(part + (size_t)c * p.N + n0) =
         make_float4(lo(dA[0]), hi(dA[0]), lo(dA[1]), hi(dA[1]));
-  // sums of e u and ddt over the block's token rows, in order
-  __syncthreads();
-  float* s1 = &sm.red[0][0][0];
-  float* s2 = reinterpret_cast<float*>(sm.q);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    s1[qt * CH + qc + e] = sD[e];
-    s2[qt * CH + qc + e] = sT[e];
-  }
-  __syncthreads();
-  for (int i = tid; i < CH; i += NT)
-    if (c0 + i < cmax) {
-      float x = 0.f, y = 0.f;
-      for (int k = 0; k < QT; ++k) {
-        x += s1[k * CH + i];
-        y += s2[k * CH + i];
-      }
-      part[(size_t)p.D * p.N + c0 + i] = x;
-      part[(size_t)p.D * (p.N + 1) + c0 + i] = y;
-    }
 }
 
 // dB, dC of a token: the channel tiles' shares added in order.  One thread per
@@ -331,7 +404,7 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(ScanParams p) {
 
 template <typename IO, int L>
 cudaError_t go(const ScanParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(Smem<IO, L>);
+  const size_t smem = sizeof(Smem<L>);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -5,18 +5,22 @@ namespace lz {
 namespace scan {
 namespace {
 
-// tokens of a tile
+// Tile: 8 elements of (token, channel) for each elementwise thread, as long as
+// that is at most 32 tokens.
 template <int L>
-constexpr int tile() { return L >= 4 ? 32 : 16; }
+struct Tile {
+  static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP;
+  static constexpr int TT = L >= 4 ? 32 : 8 * L;
+  static constexpr int EV = TT * CH / NE;                    // elements of a thread: neighbours in a row
+  static constexpr int BN = TT * L > NE ? TT * L / NE : 1;   // its 4-element vectors of B and of C
+};
 
-template <typename IO, int L>
+template <int L>
 struct alignas(16) Smem {
-  static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP, TT = tile<L>();
-  IO u[2][TT * CH], dt[2][TT * CH], z[2][TT * CH];
-  IO b[2][TT * NP], c[2][TT * NP];
-  float2 dd[TT * CH];  // delta, delta * u
-  float bf[TT * NP], cf[TT * NP];
-  float ys[TT * Geo<L>::YS];
+  using X = Tile<L>;
+  float2 dd[2][X::TT * X::CH];  // delta, delta * u
+  float bf[2][X::TT * X::NP], cf[2][X::TT * X::NP];
+  float ys[2][X::TT * Geo<L>::YS];
 };
 
 // One block: 128/L channels of one sequence over one segment of its tokens.
@@ -26,24 +30,124 @@ struct alignas(16) Smem {
 template <typename IO, int L, bool END>
 __global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
   using G = Geo<L>;
-  using S = Smem<IO, L>;
-  constexpr int CH = G::CH, NP = G::NP, TT = S::TT, U = G::U;
-  constexpr int VW = 16 / (int)sizeof(IO);
+  using X = Tile<L>;
+  constexpr int CH = G::CH, NP = G::NP, U = G::U, TT = X::TT, EV = X::EV, BN = X::BN;
   extern __shared__ __align__(16) char raw[];
-  S& sm = *reinterpret_cast<S*>(raw);
-  const int tid = threadIdx.x, lane = tid % 32;
+  Smem<L>& sm = *reinterpret_cast<Smem<L>*>(raw);
+  const int tid = threadIdx.x;
   const int g = blockIdx.x / p.nct, ct = blockIdx.x % p.nct;
   const int b = blockIdx.y, seg = blockIdx.z;
   const int per = p.D / p.G;
   const int c0 = g * per + ct * CH, cmax = (g + 1) * per;  // channels of the block
-  const int cl = tid / L, l = tid % L, c = c0 + cl;        // this thread's channel and lane
-  const int n0 = 4 * l;
-  const bool on = c < cmax && n0 < p.N;
   const int Tb = seq_len(p.lens, b, p.T);
   const int t0 = seg * p.seg, t1 = min(p.T, t0 + p.seg), te = min(t1, Tb);
+  const int ntile = t0 < te ? (te - t0 + TT - 1) / TT : 0;
+
+  if (tid >= NS) {
+    // ---- elementwise warps
+    const int et = tid - NS;
+    const int i = et / (CH / EV), cl = et % (CH / EV) * EV, c = c0 + cl;  // token of the tile, channels
+    const int nc = min(EV, cmax - c);                                      // how many of them exist
+    struct Tok {
+      Pack<IO, EV> u, z;
+    };
+    struct Next {
+      Tok a;
+      Pack<IO, EV> dt;
+      Pack<IO, 4> b[BN], c[BN];
+    };
+    auto load = [&](int k, Next& x) {
+      const int t = t0 + k * TT + i;
+      const int n = t < te ? nc : 0;
+      x.dt.load((const IO*)p.dt + p.rdt.at(b, t) + c, n, p.vec);
+      x.a.u.load((const IO*)p.u + p.ru.at(b, t) + c, n, p.vec);
+      if (!END && p.z) x.a.z.load((const IO*)p.z + p.rz.at(b, t) + c, n, p.vec);
+#pragma unroll
+      for (int j = 0; j < BN; ++j) {
+        const int v = et + j * NE, tb = t0 + k * TT + v / L, n0 = v % L * 4;
+        const int nb = v < TT * L && tb < te ? p.N - n0 : 0;
+        x.b[j].load((const IO*)p.Bm + p.rb.at(b, tb) + g * p.N + n0, nb, p.vecbc);
+        if (!END) x.c[j].load((const IO*)p.Cm + p.rc.at(b, tb) + g * p.N + n0, nb, p.vecbc);
+      }
+    };
+    auto prepare = [&](int k, const Next& x) {
+      const bool live = t0 + k * TT + i < te;
+      float2* dd = &sm.dd[k & 1][i * CH + cl];
+#pragma unroll
+      for (int e = 0; e < EV; ++e) {
+        float dl = 0.f;
+        if (live && e < nc) {
+          dl = x.dt.get(e) + (p.dtb ? p.dtb[c + e] : 0.f);
+          if (p.softplus) dl = softplus(dl);
+        }
+        dd[e] = make_float2(dl, dl * x.a.u.get(e));
+      }
+#pragma unroll
+      for (int j = 0; j < BN; ++j) {
+        const int v = et + j * NE;
+        if (v < TT * L) {
+          *reinterpret_cast<float4*>(&sm.bf[k & 1][v * 4]) =
+              make_float4(x.b[j].get(0), x.b[j].get(1), x.b[j].get(2), x.b[j].get(3));
+          if (!END)
+            *reinterpret_cast<float4*>(&sm.cf[k & 1][v * 4]) =
+                make_float4(x.c[j].get(0), x.c[j].get(1), x.c[j].get(2), x.c[j].get(3));
+        }
+      }
+    };
+    auto finish = [&](int k, const Tok& x) {
+      const int t = t0 + k * TT + i;
+      if (!p.y || t >= te) return;
+      float o[EV];
+#pragma unroll
+      for (int e = 0; e < EV; ++e) {
+        o[e] = sm.ys[k & 1][i * G::YS + cl + e];
+        if (p.Dskip && e < nc) o[e] = fmaf(p.Dskip[c + e], x.u.get(e), o[e]);
+        if (p.z) {
+          const float z = x.z.get(e);
+          o[e] *= z * sigmoid(z);
+        }
+      }
+      store_n<IO, EV>((IO*)p.y + ((size_t)b * p.T + t) * p.D + c, o, nc, p.vec);
+    };
+    // registers: the tokens of the last tile (outputs due), of this one, and
+    // the loads of the next
+    Next nx;
+    Tok last, cur;
+    if (ntile > 0) {
+      load(0, nx);
+      prepare(0, nx);
+      cur = nx.a;
+      if (ntile > 1) load(1, nx);
+    }
+    __syncthreads();
+    for (int k = 0; k < ntile; ++k) {
+      if (k + 1 < ntile) prepare(k + 1, nx);
+      const Tok next = nx.a;
+      if (k + 2 < ntile) load(k + 2, nx);
+      if constexpr (!END)
+        if (k > 0) finish(k - 1, last);
+      last = cur;
+      cur = next;
+      __syncthreads();
+    }
+    if constexpr (!END)
+      if (ntile > 0) finish(ntile - 1, last);
+    if (!END && p.y) {
+      // behind the sequence's end: zeros
+      for (int t = max(t0, te); t < t1; ++t)
+        for (int x = et; x < CH; x += NE)
+          if (c0 + x < cmax) ((IO*)p.y)[((size_t)b * p.T + t) * p.D + c0 + x] = from_f<IO>(0.f);
+    }
+    return;
+  }
+
+  // ---- scan warps
+  const int lane = tid % 32;
+  const int cl = tid / L, l = tid % L, c = c0 + cl;  // this thread's channel and lane
+  const int n0 = 4 * l;
+  const bool on = c < cmax && n0 < p.N;
   const size_t sidx = ((size_t)b * p.D + c) * p.N + n0;  // [B][D][N]
   const size_t sstep = (size_t)p.B * p.D * p.N;
-
   f2 A2[2] = {0, 0}, h[2] = {0, 0};
   if (on) {
     const float4 a = *reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0);
@@ -64,56 +168,31 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
     }
   }
   float sumd = 0.f;
-
-  auto load = [&](int t, int st) {
-    stage<IO, TT, CH, VW>(sm.u[st], p.u, p.ru, b, t, te, c0, cmax, p.vec);
-    stage<IO, TT, CH, VW>(sm.dt[st], p.dt, p.rdt, b, t, te, c0, cmax, p.vec);
-    stage<IO, TT, NP, 4>(sm.b[st], p.Bm, p.rb, b, t, te, g * p.N, g * p.N + p.N, p.vecbc);
-    if (!END) {
-      if (p.z) stage<IO, TT, CH, VW>(sm.z[st], p.z, p.rz, b, t, te, c0, cmax, p.vec);
-      stage<IO, TT, NP, 4>(sm.c[st], p.Cm, p.rc, b, t, te, g * p.N, g * p.N + p.N, p.vecbc);
-    }
-    cp_commit();
-  };
-  if (t0 < te) load(t0, 0);
-  int st = 0;
-  for (int t = t0; t < te; t += TT, st ^= 1) {
-    cp_wait_all();
-    __syncthreads();
-    for (int i = tid; i < TT * CH; i += NT) {
-      float dl = 0.f, u = 0.f;
-      const int cc = c0 + i % CH;
-      if (t + i / CH < te && cc < cmax) {
-        dl = to_f(sm.dt[st][i]) + (p.dtb ? p.dtb[cc] : 0.f);
-        if (p.softplus) dl = softplus(dl);
-        u = to_f(sm.u[st][i]);
-      }
-      sm.dd[i] = make_float2(dl, dl * u);
-    }
-    for (int i = tid; i < TT * NP; i += NT) {
-      sm.bf[i] = to_f(sm.b[st][i]);
-      if (!END) sm.cf[i] = to_f(sm.c[st][i]);
-    }
-    __syncthreads();
-    if (t + TT < te) load(t + TT, st ^ 1);
+  __syncthreads();
+  for (int k = 0; k < ntile; ++k) {
+    const float2* dd = sm.dd[k & 1] + cl;
+    const float* bf = sm.bf[k & 1] + n0;
+    const float* cf = sm.cf[k & 1] + n0;
+    float* ys = sm.ys[k & 1] + cl;
+    const int t = t0 + k * TT;
 #pragma unroll 2
     for (int i = 0; i < TT; i += U) {
       float yv[U];
-      if (!END && p.states && on && i % kCk == 0 && t + i < te) {
-        const size_t k = ((size_t)b * ((p.T + kCk - 1) / kCk) + (t + i) / kCk) * p.D + c;
-        *reinterpret_cast<float4*>(p.states + k * p.N + n0) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
+      if (!END && p.states && on && (t + i) % kCk == 0 && t + i < te) {
+        const size_t s = ((size_t)b * ((p.T + kCk - 1) / kCk) + (t + i) / kCk) * p.D + c;
+        *reinterpret_cast<float4*>(p.states + s * p.N + n0) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
       }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const float2 dd = sm.dd[(i + j) * CH + cl];
-        const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(&sm.bf[(i + j) * NP + n0]);
-        const f2 d2 = pk(dd.x, dd.x), du2 = pk(dd.y, dd.y);
+        const float2 d = dd[(i + j) * CH];
+        const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(bf + (i + j) * NP);
+        const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
         h[0] = fma2(ex2v(mul2(A2[0], d2)), h[0], mul2(du2, B4.x));
         h[1] = fma2(ex2v(mul2(A2[1], d2)), h[1], mul2(du2, B4.y));
         if (END) {
-          sumd += dd.x;
+          sumd += d.x;
         } else {
-          const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(&sm.cf[(i + j) * NP + n0]);
+          const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(cf + (i + j) * NP);
           const f2 y2 = fma2(h[1], C4.y, mul2(h[0], C4.x));
           yv[j] = lo(y2) + hi(y2);
         }
@@ -121,61 +200,24 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
       if (!END) {
         int j = 0;
         reduce_scatter<U, L / 2, 1>(yv, lane, j);
-        if (l % (L / U) == 0) sm.ys[(i + j) * G::YS + cl] = yv[0];
+        if (l % (L / U) == 0) ys[(i + j) * G::YS] = yv[0];
       }
     }
-    if (!END && p.y) {
-      __syncthreads();
-      if (p.vec) {
-        for (int i = tid; i < TT * (CH / VW); i += NT) {
-          const int tt = i / (CH / VW), cc = i % (CH / VW) * VW;
-          if (t + tt < te && c0 + cc < cmax) {
-            float o[VW], u[VW], z[VW];
-            load_vec<VW>(&sm.u[st][tt * CH + cc], u);
-            if (p.z) load_vec<VW>(&sm.z[st][tt * CH + cc], z);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              o[e] = sm.ys[tt * G::YS + cc + e];
-              if (p.Dskip) o[e] = fmaf(p.Dskip[c0 + cc + e], u[e], o[e]);
-              if (p.z) o[e] *= z[e] * sigmoid(z[e]);
-            }
-            store_vec<VW>((IO*)p.y + ((size_t)b * p.T + t + tt) * p.D + c0 + cc, o);
-          }
-        }
-      } else {
-        for (int i = tid; i < TT * CH; i += NT) {
-          const int tt = i / CH, cc = i % CH;
-          if (t + tt < te && c0 + cc < cmax) {
-            float o = sm.ys[tt * G::YS + cc];
-            if (p.Dskip) o = fmaf(p.Dskip[c0 + cc], to_f(sm.u[st][i]), o);
-            if (p.z) {
-              const float z = to_f(sm.z[st][i]);
-              o *= z * sigmoid(z);
-            }
-            ((IO*)p.y)[((size_t)b * p.T + t + tt) * p.D + c0 + cc] = from_f<IO>(o);
-          }
-        }
-      }
-    }
+    __syncthreads();
   }
   const float4 hv = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
   if (END) {
     if (on) *reinterpret_cast<float4*>(p.segE + seg * sstep + sidx) = hv;
     if (c < cmax && l == 0) p.segD[((size_t)seg * p.B + b) * p.D + c] = sumd;
-    return;
-  }
-  // a segment behind the sequence's end passes the state on
-  if (p.hT && on && seg == p.nseg - 1) *reinterpret_cast<float4*>(p.hT + sidx) = hv;
-  if (p.y) {
-    for (int t = max(t0, te); t < t1; ++t)
-      for (int i = tid; i < CH; i += NT)
-        if (c0 + i < cmax) ((IO*)p.y)[((size_t)b * p.T + t) * p.D + c0 + i] = from_f<IO>(0.f);
+  } else if (p.hT && on && seg == p.nseg - 1) {
+    // (a segment behind the sequence's end passes the state on)
+    *reinterpret_cast<float4*>(p.hT + sidx) = hv;
   }
 }
 
 template <typename IO, int L>
 cudaError_t go(const ScanParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(Smem<IO, L>);
+  const size_t smem = sizeof(Smem<L>);
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
@@ -311,7 +353,7 @@ lz_status check_scan(const char* fn, const lz_scan_dims* d) {
 // on; kFull blocks are taken as a full device.
 constexpr int kFull = 148;
 void plan(const lz_scan_dims* d, int* nct, int* seg, int* nseg) {
-  const int L = scan::lanes_of(d->N), CH = scan::NT / L;
+  const int L = scan::lanes_of(d->N), CH = scan::NS / L;
   const int per = d->D / d->G;
   *nct = (per + CH - 1) / CH;
   const int64_t base = (int64_t)*nct * d->G * d->B;
@@ -362,7 +404,8 @@ ScanParams params_of(const lz_scan_dims* d, const void* u, const void* dt, const
   p.u = u; p.dt = dt; p.A = A; p.Bm = Bm; p.Cm = Cm; p.Dskip = Dskip; p.z = z; p.dtb = dtb;
   const size_t es = esize(d->io);
   const int vw = (int)(16 / es);
-  p.vec = (d->D / d->G) % vw == 0 && rows_vec(u, p.ru, vw, es) && rows_vec(dt, p.rdt, vw, es) &&
+  // the widest run of channels that a thread takes at once is 8: whole runs only
+  p.vec = (d->D / d->G) % 8 == 0 && rows_vec(u, p.ru, vw, es) && rows_vec(dt, p.rdt, vw, es) &&
           rows_vec(z, p.rz, vw, es);
   p.vecbc = rows_vec(Bm, p.rb, 4, es) && rows_vec(Cm, p.rc, 4, es);
   return p;
