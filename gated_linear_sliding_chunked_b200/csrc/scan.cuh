@@ -94,6 +94,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// sigma(x) (1 / inf = 0 where exp(-x) overflows)
+__device__ __forceinline__ float sigm(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 __device__ __forceinline__ f2 ex2v(f2 x) { return pk(ex2(lo(x)), ex2(hi(x))); }
 
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative
@@ -102,7 +109,7 @@ __device__ __forceinline__ f2 ex2v(f2 x) { return pk(ex2(lo(x)), ex2(hi(x))); }
 // to the result also where e is small, which is where steps live.
 __device__ __forceinline__ float softplus_parts(float x, float& e) {
   e = ex2(-kLog2e * fabsf(x));
-  const float s = __fdividef(e, 2.f + e), q = s * s;
+  const float s = e * rcp(2.f + e), q = s * s;
   float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
   p = fmaf(q, p, 1.f / 11.f);
   p = fmaf(q, p, 1.f / 9.f);
@@ -129,6 +136,10 @@ struct Pack {
   __device__ __forceinline__ float get(int i) const {
     if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
     else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ void put(IO* p) const {  // to shared memory
+    if constexpr (W == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   }
   // in 16-, 8- or 4-byte accesses when vec (the row allows it), else element
   // by element; n of the V elements exist (all or none of them when vec)
@@ -161,6 +172,41 @@ struct Pack {
     }
   }
 };
+
+// 4 elements of B or C as the scan warps read them from shared memory, as pairs
+// of floats.  They stay in the I/O type there: what a warp's shared memory
+// loads return to registers, 128 bytes a cycle and SM however many lanes read
+// the same words, is what the scan runs out of first.
+template <typename IO>
+__device__ __forceinline__ void load_bc(const IO* p, f2& x, f2& y) {
+  if constexpr (sizeof(IO) == 4) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    x = v.x;
+    y = v.y;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    x = pk(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    y = pk(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  }
+}
+
+// V floats from shared memory (16- or 8-byte aligned as V allows)
+template <int V>
+__device__ __forceinline__ void load_f(const float* p, float* x) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(p + i);
+      x[i] = a.x; x[i + 1] = a.y; x[i + 2] = a.z; x[i + 3] = a.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 a = *reinterpret_cast<const float2*>(p + i);
+      x[i] = a.x; x[i + 1] = a.y;
+    }
+  }
+}
 
 // V values to consecutive elements, n of which exist
 template <typename IO, int V>

@@ -22,14 +22,108 @@ namespace {
 constexpr int TB = kCk;  // tokens of a tile
 constexpr int kWarps = NS / 32;
 
-template <int L>
+template <typename IO, int L>
 struct alignas(16) Smem {
   static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP;
-  float4 q[2][TB * CH];  // delta, delta u, e
-  float bf[2][TB * NP], cf[2][TB * NP];
+  float2 q[2][TB * CH];  // delta, delta u
+  float qe[2][TB * CH];  // e
+  IO bf[2][TB * NP], cf[2][TB * NP];
   float gB[2][TB * Geo<L>::YS], gA[2][TB * Geo<L>::YS], yc[2][TB * Geo<L>::YS];
   float red[2][kWarps][TB][2 * NP];  // dB, dC over a warp's channels
 };
+
+// The scan warps' walk over one tile, forward and back.
+template <typename IO, int L>
+__device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const float2* q,
+                                          const float* qe, const IO* bf,
+                                          const IO* cf, float* gB,
+                                          float* gA, float* yc,
+                                          float* red, const f2 (&A2)[2], f2 (&gr)[2], f2& dt0,
+                                          f2& dt1, int lane, int l) {
+  using G = Geo<L>;
+  constexpr int CH = G::CH, NP = G::NP, U = G::U, YS = G::YS;
+  // forward over the tile: the state after every token, h[i + 1]
+  f2 h[TB + 1][2];
+  h[0][0] = pk(h0.x, h0.y);
+  h[0][1] = pk(h0.z, h0.w);
+#pragma unroll
+  for (int i = 0; i < TB; i += U) {
+    float yv[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int m = i + j;
+      const float2 x = q[m * CH];
+      f2 B0, B1;
+      load_bc(bf + m * NP, B0, B1);
+      const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y);
+      h[m + 1][0] = fma2(ex2v(mul2(A2[0], d2)), h[m][0], mul2(du2, B0));
+      h[m + 1][1] = fma2(ex2v(mul2(A2[1], d2)), h[m][1], mul2(du2, B1));
+      if (want_y) {
+        f2 C0, C1;
+      load_bc(cf + m * NP, C0, C1);
+        const f2 y2 = fma2(h[m + 1][1], C1, mul2(h[m + 1][0], C0));
+        yv[j] = lo(y2) + hi(y2);
+      }
+    }
+    if (want_y) {
+      int j = 0;
+      reduce_scatter<U, L / 2, 1>(yv, lane, j);
+      if (l % (L / U) == 0) yc[(i + j) * YS] = yv[0];
+    }
+  }
+  // and back; a is taken again, which costs less than keeping it (and the
+  // compiler is kept from keeping it: 64 more registers would be spilled)
+  f2 R2[2] = {A2[0], A2[1]};
+  asm volatile("" : "+l"(R2[0]), "+l"(R2[1]));
+#pragma unroll
+  for (int i = TB - U; i >= 0; i -= U) {
+    float vB[U], vA[U];
+#pragma unroll
+    for (int j = U - 1; j >= 0; --j) {
+      const int m = i + j;
+      const float2 x = q[m * CH];
+      f2 B0, B1;
+      load_bc(bf + m * NP, B0, B1);
+      f2 C0, C1;
+      load_bc(cf + m * NP, C0, C1);
+      const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y), e2 = pk(qe[m * CH], qe[m * CH]);
+      gr[0] = fma2(e2, C0, gr[0]);
+      gr[1] = fma2(e2, C1, gr[1]);
+      const f2 dB0 = mul2(gr[0], du2), dB1 = mul2(gr[1], du2);
+      const f2 dC0 = mul2(h[m + 1][0], e2), dC1 = mul2(h[m + 1][1], e2);
+      const f2 sB = fma2(gr[1], B1, mul2(gr[0], B0));
+      gr[0] = mul2(gr[0], ex2v(mul2(R2[0], d2)));
+      gr[1] = mul2(gr[1], ex2v(mul2(R2[1], d2)));
+      const f2 gp0 = mul2(gr[0], h[m][0]), gp1 = mul2(gr[1], h[m][1]);
+      const f2 sA = fma2(gp1, A2[1], mul2(gp0, A2[0]));
+      dt0 = fma2(gp0, d2, dt0);
+      dt1 = fma2(gp1, d2, dt1);
+      vB[j] = lo(sB) + hi(sB);
+      vA[j] = lo(sA) + hi(sA);
+      float v[8] = {lo(dB0), hi(dB0), lo(dB1), hi(dB1), lo(dC0), hi(dC0), lo(dC1), hi(dC1)};
+      int base = 0;
+      reduce_scatter<8, 16, L>(v, lane, base);
+      // what is left of the 8: 1 for L <= 4 (equal in the lanes that differ
+      // below bit 2 and from L up), 2 for L = 8, 4 for L = 16
+      constexpr int LEFT = L <= 4 ? 1 : L / 4;
+      if (L >= 4 || (lane & 3 & ~(L - 1)) == 0) {
+#pragma unroll
+        for (int y = 0; y < LEFT; ++y) {
+          const int z = base + y;
+          red[m * 2 * NP + (z >> 2) * NP + (z & 3)] = v[y];
+        }
+      }
+    }
+    int j = 0;
+    reduce_scatter<U, L / 2, 1>(vB, lane, j);
+    j = 0;
+    reduce_scatter<U, L / 2, 1>(vA, lane, j);
+    if (l % (L / U) == 0) {
+      gB[(i + j) * YS] = vB[0];
+      gA[(i + j) * YS] = vA[0];
+    }
+  }
+}
 
 // END: only the gradient that the segment hands to the one before it when
 // none comes from behind (the state gradient before its first token).
@@ -42,7 +136,8 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
   constexpr int PASS = (TB * ROWT + NE - 1) / NE;               // tokens of a thread
   constexpr int BN = TB * L > NE ? TB * L / NE : 1;             // its 4-element vectors of B and of C
   extern __shared__ __align__(16) char raw[];
-  Smem<L>& sm = *reinterpret_cast<Smem<L>*>(raw);
+  using S = Smem<IO, L>;
+  S& sm = *reinterpret_cast<S*>(raw);
   const int tid = threadIdx.x;
   const int g = blockIdx.x / p.nct, ct = blockIdx.x % p.nct;
   const int b = blockIdx.y, seg = END ? blockIdx.z + 1 : blockIdx.z;
@@ -76,24 +171,44 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
       bias[e] = p.dtb && e < nc ? p.dtb[c + e] : 0.f;
       sD[e] = sT[e] = 0.f;
     }
+    // this thread's elements of the next tile to load (from the last tile down)
+    const int tl = t0 + (ntile - 1) * TB;
     const Rows rdy{p.D, (int64_t)p.T * p.D};
+    const IO* pu = (const IO*)p.u + (p.ru.at(b, 0) + c) + (int64_t)(tl + i0) * p.ru.ld;
+    const IO* pdt = (const IO*)p.dt + (p.rdt.at(b, 0) + c) + (int64_t)(tl + i0) * p.rdt.ld;
+    const IO* pdy = (const IO*)p.dy + (rdy.at(b, 0) + c) + (int64_t)(tl + i0) * rdy.ld;
+    const IO* pz = p.z ? (const IO*)p.z + (p.rz.at(b, 0) + c) + (int64_t)(tl + i0) * p.rz.ld : nullptr;
+    const IO *pb[BN], *pc[BN];
+    int nbn[BN];
+#pragma unroll
+    for (int j = 0; j < BN; ++j) {
+      const int v = et + j * NE, n0 = v % L * 4;
+      nbn[j] = v < TB * L ? p.N - n0 : 0;
+      pb[j] = (const IO*)p.Bm + (p.rb.at(b, 0) + g * p.N + n0) + (int64_t)(tl + v / L) * p.rb.ld;
+      pc[j] = (const IO*)p.Cm + (p.rc.at(b, 0) + g * p.N + n0) + (int64_t)(tl + v / L) * p.rc.ld;
+    }
     auto load = [&](int k) {
       const int tt = t0 + (ntile - 1 - k) * TB;
 #pragma unroll
       for (int s = 0; s < PASS; ++s) {
         const int i = i0 + s * IS, t = tt + i;
         const int n = i < TB && t < te ? nc : 0;
-        nx[s].dt.load((const IO*)p.dt + p.rdt.at(b, t) + c, n, p.vec);
-        nx[s].dy.load((const IO*)p.dy + rdy.at(b, t) + c, n, p.vec);
-        if (p.z) nx[s].z.load((const IO*)p.z + p.rz.at(b, t) + c, n, p.vec);
-        if (!END) nx[s].u.load((const IO*)p.u + p.ru.at(b, t) + c, n, p.vec);
+        nx[s].dt.load(pdt + s * IS * p.rdt.ld, n, p.vec);
+        nx[s].dy.load(pdy + s * IS * rdy.ld, n, p.vec);
+        if (p.z) nx[s].z.load(pz + s * IS * p.rz.ld, n, p.vec);
+        if (!END) nx[s].u.load(pu + s * IS * p.ru.ld, n, p.vec);
       }
+      pdt -= TB * p.rdt.ld;
+      pdy -= TB * rdy.ld;
+      pz -= TB * p.rz.ld;
+      pu -= TB * p.ru.ld;
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
-        const int v = et + j * NE, t = tt + v / L, n0 = v % L * 4;
-        const int n = v < TB * L && t < te ? p.N - n0 : 0;
-        ncv[j].load((const IO*)p.Cm + p.rc.at(b, t) + g * p.N + n0, n, p.vecbc);
-        if (!END) nb[j].load((const IO*)p.Bm + p.rb.at(b, t) + g * p.N + n0, n, p.vecbc);
+        const int n = tt + (et + j * NE) / L < te ? nbn[j] : 0;
+        ncv[j].load(pc[j], n, p.vecbc);
+        if (!END) nb[j].load(pb[j], n, p.vecbc);
+        pc[j] -= TB * p.rc.ld;
+        pb[j] -= TB * p.rb.ld;
       }
     };
     auto prepare = [&](int k, Tok (&tok)[PASS]) {
@@ -105,40 +220,38 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
         const bool live = tt + i < te;
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
-          float dl = 0.f, ee = 0.f, u = 0.f, sg = 1.f, dzf = 0.f;
-          if (live && e < nc) {
-            dl = nx[s].dt.get(e) + bias[e];
-            if (p.softplus) {
-              float x;
-              const float pre = dl;
-              dl = softplus_parts(pre, x);
-              sg = __fdividef(pre >= 0.f ? 1.f : x, 1.f + x);
-            }
-            ee = nx[s].dy.get(e);
-            if (p.z) {
-              const float z = nx[s].z.get(e), sz = sigmoid(z);
-              dzf = ee * sz * (1.f + z * (1.f - sz));
-              ee *= z * sz;
-            }
-            if (!END) u = nx[s].u.get(e);
+          // behind the sequence's end the loads left zeros: e = u = 0, and delta is
+          // made 0 (a channel that is not there only needs e = u = 0)
+          float sg = 1.f, dzf = 0.f, dl = nx[s].dt.get(e) + bias[e];
+          if (p.softplus) {
+            float x;
+            const float pre = dl;
+            dl = softplus_parts(pre, x);
+            sg = rcp(1.f + x) * (pre >= 0.f ? 1.f : x);
           }
+          dl = live ? dl : 0.f;
+          float ee = nx[s].dy.get(e);
+          if (p.z) {
+            const float z = nx[s].z.get(e), sz = sigm(z), zs = z * sz;
+            dzf = ee * fmaf(-zs, sz, sz + zs);
+            ee *= zs;
+          }
+          const float u = END ? 0.f : nx[s].u.get(e), du = dl * u;
           tok[s].delta[e] = dl;
           tok[s].e[e] = ee;
           tok[s].u[e] = u;
           tok[s].sg[e] = sg;
           tok[s].dzf[e] = dzf;
-          sm.q[k & 1][i * CH + cl + e] = make_float4(dl, dl * u, ee, 0.f);
+          sm.q[k & 1][i * CH + cl + e] = make_float2(dl, du);
+          sm.qe[k & 1][i * CH + cl + e] = ee;
         }
       }
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
         const int v = et + j * NE;
         if (v < TB * L) {
-          *reinterpret_cast<float4*>(&sm.cf[k & 1][v * 4]) =
-              make_float4(ncv[j].get(0), ncv[j].get(1), ncv[j].get(2), ncv[j].get(3));
-          if (!END)
-            *reinterpret_cast<float4*>(&sm.bf[k & 1][v * 4]) =
-                make_float4(nb[j].get(0), nb[j].get(1), nb[j].get(2), nb[j].get(3));
+          ncv[j].put(&sm.cf[k & 1][v * 4]);
+          if (!END) nb[j].put(&sm.bf[k & 1][v * 4]);
         }
       }
     };
@@ -148,15 +261,17 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
       for (int s = 0; s < PASS; ++s) {
         const int i = i0 + s * IS, t = tt + i;
         if (i >= TB || t >= te) continue;
-        float du[EV], dd[EV], dz[EV];
+        float du[EV], dd[EV], dz[EV], gB[EV], gA[EV], yc[EV];
+        load_f<EV>(&sm.gB[w][i * YS + cl], gB);
+        load_f<EV>(&sm.gA[w][i * YS + cl], gA);
+        if (p.dz) load_f<EV>(&sm.yc[w][i * YS + cl], yc);
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
-          const float gB = sm.gB[w][i * YS + cl + e];
-          du[e] = fmaf(tok[s].delta[e], gB, Ds[e] * tok[s].e[e]);
-          dd[e] = fmaf(tok[s].u[e], gB, kLn2 * sm.gA[w][i * YS + cl + e]) * tok[s].sg[e];
+          du[e] = fmaf(tok[s].delta[e], gB[e], Ds[e] * tok[s].e[e]);
+          dd[e] = fmaf(tok[s].u[e], gB[e], kLn2 * gA[e]) * tok[s].sg[e];
           sD[e] = fmaf(tok[s].e[e], tok[s].u[e], sD[e]);
           sT[e] += dd[e];
-          if (p.dz) dz[e] = tok[s].dzf[e] * fmaf(Ds[e], tok[s].u[e], sm.yc[w][i * YS + cl + e]);
+          if (p.dz) dz[e] = tok[s].dzf[e] * fmaf(Ds[e], tok[s].u[e], yc[e]);
         }
         const size_t at = ((size_t)b * p.T + t) * p.D + c;
         store_n<IO, EV>((IO*)p.du + at, du, nc, p.vec);
@@ -207,7 +322,8 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
       if (ntile > 0) finish(ntile - 1, last);
       // sums of e u and ddt over the block's token rows, in order
       float* s1 = &sm.red[0][0][0][0];
-      float* s2 = reinterpret_cast<float*>(sm.q);
+      float* s2 = &sm.gB[0][0];
+      static_assert(IS * CH <= 2 * kWarps * TB * 2 * NP && IS * CH <= 2 * TB * YS, "room for the sums");
       asm volatile("bar.sync 1, %0;" ::"n"(NE) : "memory");
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
@@ -266,99 +382,27 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
   __syncthreads();
   for (int k = 0; k < ntile; ++k) {
     const int w = k & 1;
-    const float4* q = sm.q[w] + cl;
-    const float* bf = sm.bf[w] + n0;
-    const float* cf = sm.cf[w] + n0;
+    const float2* q = sm.q[w] + cl;
+    const float* qe = sm.qe[w] + cl;
+    const IO* bf = sm.bf[w] + n0;
+    const IO* cf = sm.cf[w] + n0;
     if constexpr (END) {
 #pragma unroll 4
       for (int i = TB - 1; i >= 0; --i) {
-        const float4 x = q[i * CH];
-        const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(cf + i * NP);
-        const f2 e2 = pk(x.z, x.z), d2 = pk(x.x, x.x);
-        gr[0] = mul2(fma2(e2, C4.x, gr[0]), ex2v(mul2(A2[0], d2)));
-        gr[1] = mul2(fma2(e2, C4.y, gr[1]), ex2v(mul2(A2[1], d2)));
-        sumd += x.x;
+        const float d = q[i * CH].x, e = qe[i * CH];
+        const f2 d2 = pk(d, d), e2 = pk(e, e);
+        f2 C0, C1;
+        load_bc(cf + i * NP, C0, C1);
+        gr[0] = mul2(fma2(e2, C0, gr[0]), ex2v(mul2(A2[0], d2)));
+        gr[1] = mul2(fma2(e2, C1, gr[1]), ex2v(mul2(A2[1], d2)));
+        sumd += d;
       }
     } else {
-      // forward over the tile: the state after every token, h[i + 1]
-      f2 h[TB + 1][2];
-      h[0][0] = pk(ck.x, ck.y);
-      h[0][1] = pk(ck.z, ck.w);
-      if (k + 1 < ntile) load_ck(k + 1);
-#pragma unroll
-      for (int i = 0; i < TB; i += U) {
-        float yv[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const float2 x = *reinterpret_cast<const float2*>(&q[(i + j) * CH]);
-          const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(bf + (i + j) * NP);
-          const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y);
-          const int m = i + j;
-          h[m + 1][0] = fma2(ex2v(mul2(A2[0], d2)), h[m][0], mul2(du2, B4.x));
-          h[m + 1][1] = fma2(ex2v(mul2(A2[1], d2)), h[m][1], mul2(du2, B4.y));
-          if (p.dz) {
-            const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(cf + m * NP);
-            const f2 y2 = fma2(h[m + 1][1], C4.y, mul2(h[m + 1][0], C4.x));
-            yv[j] = lo(y2) + hi(y2);
-          }
-        }
-        if (p.dz) {
-          int j = 0;
-          reduce_scatter<U, L / 2, 1>(yv, lane, j);
-          if (l % (L / U) == 0) sm.yc[w][(i + j) * YS + cl] = yv[0];
-        }
-      }
-      // and back; a is taken again, which costs less than keeping it (and the
-      // compiler is kept from keeping it: 64 more registers would be spilled)
-      f2 R2[2] = {A2[0], A2[1]};
-      asm volatile("" : "+l"(R2[0]), "+l"(R2[1]));
       f2 dt0 = 0, dt1 = 0;  // dA of the tile
-#pragma unroll
-      for (int i = TB - U; i >= 0; i -= U) {
-        float vB[U], vA[U];
-#pragma unroll
-        for (int j = U - 1; j >= 0; --j) {
-          const int m = i + j;
-          const float4 x = q[m * CH];
-          const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(bf + m * NP);
-          const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(cf + m * NP);
-          const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y), e2 = pk(x.z, x.z);
-          gr[0] = fma2(e2, C4.x, gr[0]);
-          gr[1] = fma2(e2, C4.y, gr[1]);
-          const f2 dB0 = mul2(gr[0], du2), dB1 = mul2(gr[1], du2);
-          const f2 dC0 = mul2(h[m + 1][0], e2), dC1 = mul2(h[m + 1][1], e2);
-          const f2 sB = fma2(gr[1], B4.y, mul2(gr[0], B4.x));
-          gr[0] = mul2(gr[0], ex2v(mul2(R2[0], d2)));
-          gr[1] = mul2(gr[1], ex2v(mul2(R2[1], d2)));
-          const f2 gp0 = mul2(gr[0], h[m][0]), gp1 = mul2(gr[1], h[m][1]);
-          const f2 sA = fma2(gp1, A2[1], mul2(gp0, A2[0]));
-          dt0 = fma2(gp0, d2, dt0);
-          dt1 = fma2(gp1, d2, dt1);
-          vB[j] = lo(sB) + hi(sB);
-          vA[j] = lo(sA) + hi(sA);
-          float v[8] = {lo(dB0), hi(dB0), lo(dB1), hi(dB1), lo(dC0), hi(dC0), lo(dC1), hi(dC1)};
-          int base = 0;
-          reduce_scatter<8, 16, L>(v, lane, base);
-          // what is left of the 8: 1 for L <= 4 (equal in the lanes that differ
-          // below bit 2 and from L up), 2 for L = 8, 4 for L = 16
-          constexpr int LEFT = L <= 4 ? 1 : L / 4;
-          if (L >= 4 || (lane & 3 & ~(L - 1)) == 0) {
-#pragma unroll
-            for (int y = 0; y < LEFT; ++y) {
-              const int z = base + y;
-              sm.red[w][warp][m][(z >> 2) * NP + n0 + (z & 3)] = v[y];
-            }
-          }
-        }
-        int j = 0;
-        reduce_scatter<U, L / 2, 1>(vB, lane, j);
-        j = 0;
-        reduce_scatter<U, L / 2, 1>(vA, lane, j);
-        if (l % (L / U) == 0) {
-          sm.gB[w][(i + j) * YS + cl] = vB[0];
-          sm.gA[w][(i + j) * YS + cl] = vA[0];
-        }
-      }
+      const float4 h0 = ck;
+      if (k + 1 < ntile) load_ck(k + 1);
+      walk_tile<IO, L>(p.dz != nullptr, h0, q, qe, bf, cf, sm.gB[w] + cl, sm.gA[w] + cl, sm.yc[w] + cl,
+                   &sm.red[w][warp][0][0] + n0, A2, gr, dt0, dt1, lane, l);
       // dA over thousands of tiles: the sum carries the rounding of each addition on
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -404,7 +448,7 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(ScanParams p) {
 
 template <typename IO, int L>
 cudaError_t go(const ScanParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(Smem<L>);
+  const size_t smem = sizeof(Smem<IO, L>);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -15,25 +15,69 @@ struct Tile {
   static constexpr int BN = TT * L > NE ? TT * L / NE : 1;   // its 4-element vectors of B and of C
 };
 
-template <int L>
+template <typename IO, int L>
 struct alignas(16) Smem {
   using X = Tile<L>;
   float2 dd[2][X::TT * X::CH];  // delta, delta * u
-  float bf[2][X::TT * X::NP], cf[2][X::TT * X::NP];
+  IO bf[2][X::TT * X::NP], cf[2][X::TT * X::NP];
   float ys[2][X::TT * Geo<L>::YS];
 };
+
+// The scan warps' walk over one tile.  (The tile's inputs and its results do
+// not overlap; told so, the compiler loads the next tokens' operands before
+// it has stored the last ones' sums.)
+template <typename IO, int L, bool END>
+__device__ __forceinline__ void scan_tile(const ScanParams& p, const float2* __restrict__ dd,
+                                          const IO* __restrict__ bf, const IO* __restrict__ cf,
+                                          float* __restrict__ ys, const f2 (&A2)[2], f2 (&h)[2], float& sumd,
+                                          int lane, int l, int b, int c, int n0, bool on, int t, int te) {
+  using G = Geo<L>;
+  constexpr int CH = G::CH, NP = G::NP, U = G::U, TT = Tile<L>::TT;
+#pragma unroll 4
+  for (int i = 0; i < TT; i += U) {
+    float yv[U];
+    // (t is a multiple of the tile)
+    if (!END && (TT % kCk == 0 ? i : t + i) % kCk == 0 && p.states && on && t + i < te) {
+      const size_t s = ((size_t)b * ((p.T + kCk - 1) / kCk) + (t + i) / kCk) * p.D + c;
+      *reinterpret_cast<float4*>(p.states + s * p.N + n0) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const float2 d = dd[(i + j) * CH];
+      f2 B0, B1;
+      load_bc(bf + (i + j) * NP, B0, B1);
+      const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
+      h[0] = fma2(ex2v(mul2(A2[0], d2)), h[0], mul2(du2, B0));
+      h[1] = fma2(ex2v(mul2(A2[1], d2)), h[1], mul2(du2, B1));
+      if (END) {
+        sumd += d.x;
+      } else {
+        f2 C0, C1;
+        load_bc(cf + (i + j) * NP, C0, C1);
+        const f2 y2 = fma2(h[1], C1, mul2(h[0], C0));
+        yv[j] = lo(y2) + hi(y2);
+      }
+    }
+    if (!END) {
+      int j = 0;
+      reduce_scatter<U, L / 2, 1>(yv, lane, j);
+      if (l % (L / U) == 0) ys[(i + j) * G::YS] = yv[0];
+    }
+  }
+}
 
 // One block: 128/L channels of one sequence over one segment of its tokens.
 // END: only the segment's effect on the state (its end value from a zero
 // start and the sum of delta), which the blocks of the later segments fold
 // into the state they start from.
 template <typename IO, int L, bool END>
-__global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
   using G = Geo<L>;
   using X = Tile<L>;
   constexpr int CH = G::CH, NP = G::NP, U = G::U, TT = X::TT, EV = X::EV, BN = X::BN;
   extern __shared__ __align__(16) char raw[];
-  Smem<L>& sm = *reinterpret_cast<Smem<L>*>(raw);
+  using S = Smem<IO, L>;
+  S& sm = *reinterpret_cast<S*>(raw);
   const int tid = threadIdx.x;
   const int g = blockIdx.x / p.nct, ct = blockIdx.x % p.nct;
   const int b = blockIdx.y, seg = blockIdx.z;
@@ -56,18 +100,42 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
       Pack<IO, EV> dt;
       Pack<IO, 4> b[BN], c[BN];
     };
+    // this thread's elements of the next tile to load
+    const IO* pu = (const IO*)p.u + p.ru.at(b, t0 + i) + c;
+    const IO* pdt = (const IO*)p.dt + p.rdt.at(b, t0 + i) + c;
+    const IO* pz = p.z ? (const IO*)p.z + p.rz.at(b, t0 + i) + c : nullptr;
+    const IO *pb[BN], *pc[BN];
+    int tb[BN], nb[BN];
+#pragma unroll
+    for (int j = 0; j < BN; ++j) {
+      const int v = et + j * NE, n0 = v % L * 4;
+      tb[j] = t0 + v / L;
+      nb[j] = v < TT * L ? p.N - n0 : 0;
+      pb[j] = (const IO*)p.Bm + p.rb.at(b, tb[j]) + g * p.N + n0;
+      pc[j] = (const IO*)p.Cm + p.rc.at(b, tb[j]) + g * p.N + n0;
+    }
+    float bias[EV], Ds[EV];
+#pragma unroll
+    for (int e = 0; e < EV; ++e) {
+      bias[e] = p.dtb && e < nc ? p.dtb[c + e] : 0.f;
+      Ds[e] = !END && p.Dskip && e < nc ? p.Dskip[c + e] : 0.f;
+    }
     auto load = [&](int k, Next& x) {
-      const int t = t0 + k * TT + i;
-      const int n = t < te ? nc : 0;
-      x.dt.load((const IO*)p.dt + p.rdt.at(b, t) + c, n, p.vec);
-      x.a.u.load((const IO*)p.u + p.ru.at(b, t) + c, n, p.vec);
-      if (!END && p.z) x.a.z.load((const IO*)p.z + p.rz.at(b, t) + c, n, p.vec);
+      const int n = t0 + k * TT + i < te ? nc : 0;
+      x.dt.load(pdt, n, p.vec);
+      x.a.u.load(pu, n, p.vec);
+      if (!END && p.z) x.a.z.load(pz, n, p.vec);
+      pdt += TT * p.rdt.ld;
+      pu += TT * p.ru.ld;
+      pz += TT * p.rz.ld;
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
-        const int v = et + j * NE, tb = t0 + k * TT + v / L, n0 = v % L * 4;
-        const int nb = v < TT * L && tb < te ? p.N - n0 : 0;
-        x.b[j].load((const IO*)p.Bm + p.rb.at(b, tb) + g * p.N + n0, nb, p.vecbc);
-        if (!END) x.c[j].load((const IO*)p.Cm + p.rc.at(b, tb) + g * p.N + n0, nb, p.vecbc);
+        const int m = tb[j] < te ? nb[j] : 0;
+        x.b[j].load(pb[j], m, p.vecbc);
+        if (!END) x.c[j].load(pc[j], m, p.vecbc);
+        tb[j] += TT;
+        pb[j] += TT * p.rb.ld;
+        pc[j] += TT * p.rc.ld;
       }
     };
     auto prepare = [&](int k, const Next& x) {
@@ -75,22 +143,19 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
       float2* dd = &sm.dd[k & 1][i * CH + cl];
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
-        float dl = 0.f;
-        if (live && e < nc) {
-          dl = x.dt.get(e) + (p.dtb ? p.dtb[c + e] : 0.f);
-          if (p.softplus) dl = softplus(dl);
-        }
+        float dl = x.dt.get(e) + bias[e];
+        if (p.softplus) dl = softplus(dl);
+        // (a channel that is not there has u = 0 and takes nothing up; what its
+        // state decays by does not matter)
+        dl = live ? dl : 0.f;
         dd[e] = make_float2(dl, dl * x.a.u.get(e));
       }
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
         const int v = et + j * NE;
         if (v < TT * L) {
-          *reinterpret_cast<float4*>(&sm.bf[k & 1][v * 4]) =
-              make_float4(x.b[j].get(0), x.b[j].get(1), x.b[j].get(2), x.b[j].get(3));
-          if (!END)
-            *reinterpret_cast<float4*>(&sm.cf[k & 1][v * 4]) =
-                make_float4(x.c[j].get(0), x.c[j].get(1), x.c[j].get(2), x.c[j].get(3));
+          x.b[j].put(&sm.bf[k & 1][v * 4]);
+          if (!END) x.c[j].put(&sm.cf[k & 1][v * 4]);
         }
       }
     };
@@ -98,13 +163,13 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
       const int t = t0 + k * TT + i;
       if (!p.y || t >= te) return;
       float o[EV];
+      load_f<EV>(&sm.ys[k & 1][i * G::YS + cl], o);
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
-        o[e] = sm.ys[k & 1][i * G::YS + cl + e];
-        if (p.Dskip && e < nc) o[e] = fmaf(p.Dskip[c + e], x.u.get(e), o[e]);
+        o[e] = fmaf(Ds[e], x.u.get(e), o[e]);
         if (p.z) {
           const float z = x.z.get(e);
-          o[e] *= z * sigmoid(z);
+          o[e] *= z * sigm(z);
         }
       }
       store_n<IO, EV>((IO*)p.y + ((size_t)b * p.T + t) * p.D + c, o, nc, p.vec);
@@ -171,38 +236,11 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
   __syncthreads();
   for (int k = 0; k < ntile; ++k) {
     const float2* dd = sm.dd[k & 1] + cl;
-    const float* bf = sm.bf[k & 1] + n0;
-    const float* cf = sm.cf[k & 1] + n0;
+    const IO* bf = sm.bf[k & 1] + n0;
+    const IO* cf = sm.cf[k & 1] + n0;
     float* ys = sm.ys[k & 1] + cl;
     const int t = t0 + k * TT;
-#pragma unroll 2
-    for (int i = 0; i < TT; i += U) {
-      float yv[U];
-      if (!END && p.states && on && (t + i) % kCk == 0 && t + i < te) {
-        const size_t s = ((size_t)b * ((p.T + kCk - 1) / kCk) + (t + i) / kCk) * p.D + c;
-        *reinterpret_cast<float4*>(p.states + s * p.N + n0) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
-      }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const float2 d = dd[(i + j) * CH];
-        const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(bf + (i + j) * NP);
-        const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
-        h[0] = fma2(ex2v(mul2(A2[0], d2)), h[0], mul2(du2, B4.x));
-        h[1] = fma2(ex2v(mul2(A2[1], d2)), h[1], mul2(du2, B4.y));
-        if (END) {
-          sumd += d.x;
-        } else {
-          const ulonglong2 C4 = *reinterpret_cast<const ulonglong2*>(cf + (i + j) * NP);
-          const f2 y2 = fma2(h[1], C4.y, mul2(h[0], C4.x));
-          yv[j] = lo(y2) + hi(y2);
-        }
-      }
-      if (!END) {
-        int j = 0;
-        reduce_scatter<U, L / 2, 1>(yv, lane, j);
-        if (l % (L / U) == 0) ys[(i + j) * G::YS] = yv[0];
-      }
-    }
+    scan_tile<IO, L, END>(p, dd, bf, cf, ys, A2, h, sumd, lane, l, b, c, n0, on, t, te);
     __syncthreads();
   }
   const float4 hv = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
@@ -217,7 +255,7 @@ __global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
 
 template <typename IO, int L>
 cudaError_t go(const ScanParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(Smem<L>);
+  const size_t smem = sizeof(Smem<IO, L>);
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
@@ -282,7 +320,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p, float* sta
     if (p.Dskip) y = fmaf(p.Dskip[c], u, y);
     if (p.z) {
       const float z = to_f(((const IO*)p.z)[p.rz.at(b, 0) + c]);
-      y *= z * sigmoid(z);
+      y *= z * scan::sigm(z);
     }
     ((IO*)p.y)[bc] = from_f<IO>(y);
   }
