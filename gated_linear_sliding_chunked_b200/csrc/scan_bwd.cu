@@ -25,8 +25,9 @@ constexpr int kWarps = NS / 32;
 template <typename IO, int L>
 struct alignas(16) Smem {
   static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP;
-  float2 q[2][TB * CH];  // delta, delta u
-  float qe[2][TB * CH];  // e
+  static constexpr int DS = CH + 2;  // row of q and qe, off the banks of the row before
+  float2 q[2][TB * DS];  // delta, delta u
+  float qe[2][TB * DS];  // e
   IO bf[2][TB * NP], cf[2][TB * NP];
   float gB[2][TB * Geo<L>::YS], gA[2][TB * Geo<L>::YS], yc[2][TB * Geo<L>::YS];
   float red[2][kWarps][TB][2 * NP];  // dB, dC over a warp's channels
@@ -41,7 +42,7 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
                                           float* red, const f2 (&A2)[2], f2 (&gr)[2], f2& dt0,
                                           f2& dt1, int lane, int l) {
   using G = Geo<L>;
-  constexpr int CH = G::CH, NP = G::NP, U = G::U, YS = G::YS;
+  constexpr int NP = G::NP, U = G::U, YS = G::YS, DS = Smem<IO, L>::DS;
   // forward over the tile: the state after every token, h[i + 1]
   f2 h[TB + 1][2];
   h[0][0] = pk(h0.x, h0.y);
@@ -52,7 +53,7 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int m = i + j;
-      const float2 x = q[m * CH];
+      const float2 x = q[m * DS];
       f2 B0, B1;
       load_bc(bf + m * NP, B0, B1);
       const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y);
@@ -81,12 +82,12 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
 #pragma unroll
     for (int j = U - 1; j >= 0; --j) {
       const int m = i + j;
-      const float2 x = q[m * CH];
+      const float2 x = q[m * DS];
       f2 B0, B1;
       load_bc(bf + m * NP, B0, B1);
       f2 C0, C1;
       load_bc(cf + m * NP, C0, C1);
-      const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y), e2 = pk(qe[m * CH], qe[m * CH]);
+      const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y), e2 = pk(qe[m * DS], qe[m * DS]);
       gr[0] = fma2(e2, C0, gr[0]);
       gr[1] = fma2(e2, C1, gr[1]);
       const f2 dB0 = mul2(gr[0], du2), dB1 = mul2(gr[1], du2);
@@ -130,7 +131,7 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
 template <typename IO, int L, bool END>
 __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams p) {
   using G = Geo<L>;
-  constexpr int CH = G::CH, NP = G::NP, U = G::U, YS = G::YS;
+  constexpr int CH = G::CH, NP = G::NP, YS = G::YS;
   constexpr int EV = TB * CH / NE > 1 ? (TB * CH / NE < 8 ? TB * CH / NE : 8) : 2;  // channels of an elementwise thread
   constexpr int ROWT = CH / EV;                                 // threads of a token
   constexpr int PASS = (TB * ROWT + NE - 1) / NE;               // tokens of a thread
@@ -218,32 +219,41 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
         const int i = i0 + s * IS;
         if (i >= TB) continue;
         const bool live = tt + i < te;
+        // behind the sequence's end the loads left zeros: e = u = 0, and delta is
+        // made 0 (a channel that is not there only needs e = u = 0)
+        Tok& x = tok[s];
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
-          // behind the sequence's end the loads left zeros: e = u = 0, and delta is
-          // made 0 (a channel that is not there only needs e = u = 0)
-          float sg = 1.f, dzf = 0.f, dl = nx[s].dt.get(e) + bias[e];
-          if (p.softplus) {
-            float x;
-            const float pre = dl;
-            dl = softplus_parts(pre, x);
-            sg = rcp(1.f + x) * (pre >= 0.f ? 1.f : x);
+          x.delta[e] = nx[s].dt.get(e) + bias[e];
+          x.sg[e] = 1.f;
+          x.e[e] = nx[s].dy.get(e);
+          x.dzf[e] = 0.f;
+          x.u[e] = END ? 0.f : nx[s].u.get(e);
+        }
+        if (p.softplus) {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) {
+            float y;
+            const float pre = x.delta[e];
+            x.delta[e] = softplus_parts(pre, y);
+            x.sg[e] = rcp(1.f + y) * (pre >= 0.f ? 1.f : y);
           }
-          dl = live ? dl : 0.f;
-          float ee = nx[s].dy.get(e);
-          if (p.z) {
+        }
+        if (p.z) {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) {
             const float z = nx[s].z.get(e), sz = sigm(z), zs = z * sz;
-            dzf = ee * fmaf(-zs, sz, sz + zs);
-            ee *= zs;
+            x.dzf[e] = x.e[e] * fmaf(-zs, sz, sz + zs);
+            x.e[e] *= zs;
           }
-          const float u = END ? 0.f : nx[s].u.get(e), du = dl * u;
-          tok[s].delta[e] = dl;
-          tok[s].e[e] = ee;
-          tok[s].u[e] = u;
-          tok[s].sg[e] = sg;
-          tok[s].dzf[e] = dzf;
-          sm.q[k & 1][i * CH + cl + e] = make_float2(dl, du);
-          sm.qe[k & 1][i * CH + cl + e] = ee;
+        }
+#pragma unroll
+        for (int e = 0; e < EV; ++e) x.delta[e] = live ? x.delta[e] : 0.f;
+#pragma unroll
+        for (int e = 0; e < EV; e += 2) {
+          *reinterpret_cast<float4*>(&sm.q[k & 1][i * S::DS + cl + e]) =
+              make_float4(x.delta[e], x.delta[e] * x.u[e], x.delta[e + 1], x.delta[e + 1] * x.u[e + 1]);
+          *reinterpret_cast<float2*>(&sm.qe[k & 1][i * S::DS + cl + e]) = make_float2(x.e[e], x.e[e + 1]);
         }
       }
 #pragma unroll
@@ -389,7 +399,7 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
     if constexpr (END) {
 #pragma unroll 4
       for (int i = TB - 1; i >= 0; --i) {
-        const float d = q[i * CH].x, e = qe[i * CH];
+        const float d = q[i * S::DS].x, e = qe[i * S::DS];
         const f2 d2 = pk(d, d), e2 = pk(e, e);
         f2 C0, C1;
         load_bc(cf + i * NP, C0, C1);

@@ -12,46 +12,57 @@ struct Tile {
   static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP;
   static constexpr int TT = L >= 4 ? 32 : 8 * L;
   static constexpr int EV = TT * CH / NE;                    // elements of a thread: neighbours in a row
+  static constexpr int DS = CH + 2;                          // row of dd, off the banks of the row before
   static constexpr int BN = TT * L > NE ? TT * L / NE : 1;   // its 4-element vectors of B and of C
 };
 
 template <typename IO, int L>
 struct alignas(16) Smem {
   using X = Tile<L>;
-  float2 dd[2][X::TT * X::CH];  // delta, delta * u
+  float2 dd[2][X::TT * X::DS];  // delta, delta * u
   IO bf[2][X::TT * X::NP], cf[2][X::TT * X::NP];
   float ys[2][X::TT * Geo<L>::YS];
 };
 
-// The scan warps' walk over one tile.  (The tile's inputs and its results do
-// not overlap; told so, the compiler loads the next tokens' operands before
-// it has stored the last ones' sums.)
+// The scan warps' walk over one tile, U tokens at a time.  The decays and
+// inputs of the next U tokens are formed before the state passes through
+// these, and the whole tile is one run of instructions, so that the loads and
+// exponentials of the former fill the waits of the latter.
 template <typename IO, int L, bool END>
-__device__ __forceinline__ void scan_tile(const ScanParams& p, const float2* __restrict__ dd,
-                                          const IO* __restrict__ bf, const IO* __restrict__ cf,
-                                          float* __restrict__ ys, const f2 (&A2)[2], f2 (&h)[2], float& sumd,
-                                          int lane, int l, int b, int c, int n0, bool on, int t, int te) {
+__device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const IO* __restrict__ bf,
+                                          const IO* __restrict__ cf, float* __restrict__ ys, const f2 (&A2)[2],
+                                          f2 (&h)[2], float& sumd, int lane, int l, float* states, size_t ck_step,
+                                          int ck_left) {
   using G = Geo<L>;
-  constexpr int CH = G::CH, NP = G::NP, U = G::U, TT = Tile<L>::TT;
-#pragma unroll 4
-  for (int i = 0; i < TT; i += U) {
-    float yv[U];
-    // (t is a multiple of the tile)
-    if (!END && (TT % kCk == 0 ? i : t + i) % kCk == 0 && p.states && on && t + i < te) {
-      const size_t s = ((size_t)b * ((p.T + kCk - 1) / kCk) + (t + i) / kCk) * p.D + c;
-      *reinterpret_cast<float4*>(p.states + s * p.N + n0) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
-    }
+  constexpr int NP = G::NP, U = G::U, TT = Tile<L>::TT, NG = TT / U;
+  f2 a[2][U][2], x[2][U][2];
+  auto form = [&](int i, f2 (&a)[U][2], f2 (&x)[U][2]) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const float2 d = dd[(i + j) * CH];
+      const float2 d = dd[(i + j) * Tile<L>::DS];
       f2 B0, B1;
       load_bc(bf + (i + j) * NP, B0, B1);
       const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
-      h[0] = fma2(ex2v(mul2(A2[0], d2)), h[0], mul2(du2, B0));
-      h[1] = fma2(ex2v(mul2(A2[1], d2)), h[1], mul2(du2, B1));
-      if (END) {
-        sumd += d.x;
-      } else {
+      a[j][0] = ex2v(mul2(A2[0], d2));
+      a[j][1] = ex2v(mul2(A2[1], d2));
+      x[j][0] = mul2(du2, B0);
+      x[j][1] = mul2(du2, B1);
+      if (END) sumd += d.x;
+    }
+  };
+  form(0, a[0], x[0]);
+#pragma unroll
+  for (int q = 0; q < NG; ++q) {
+    const int i = q * U;
+    if (q + 1 < NG) form(i + U, a[(q + 1) & 1], x[(q + 1) & 1]);
+    if (!END && i % kCk == 0 && i < ck_left)  // the state before every 16th token
+      *reinterpret_cast<float4*>(states + i / kCk * ck_step) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
+    float yv[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      h[0] = fma2(a[q & 1][j][0], h[0], x[q & 1][j][0]);
+      h[1] = fma2(a[q & 1][j][1], h[1], x[q & 1][j][1]);
+      if (!END) {
         f2 C0, C1;
         load_bc(cf + (i + j) * NP, C0, C1);
         const f2 y2 = fma2(h[1], C1, mul2(h[0], C0));
@@ -74,7 +85,7 @@ template <typename IO, int L, bool END>
 __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
   using G = Geo<L>;
   using X = Tile<L>;
-  constexpr int CH = G::CH, NP = G::NP, U = G::U, TT = X::TT, EV = X::EV, BN = X::BN;
+  constexpr int CH = G::CH, TT = X::TT, EV = X::EV, BN = X::BN, DS = X::DS;
   extern __shared__ __align__(16) char raw[];
   using S = Smem<IO, L>;
   S& sm = *reinterpret_cast<S*>(raw);
@@ -140,16 +151,22 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
     };
     auto prepare = [&](int k, const Next& x) {
       const bool live = t0 + k * TT + i < te;
-      float2* dd = &sm.dd[k & 1][i * CH + cl];
+      float2* dd = &sm.dd[k & 1][i * DS + cl];
+      float dl[EV];
 #pragma unroll
-      for (int e = 0; e < EV; ++e) {
-        float dl = x.dt.get(e) + bias[e];
-        if (p.softplus) dl = softplus(dl);
-        // (a channel that is not there has u = 0 and takes nothing up; what its
-        // state decays by does not matter)
-        dl = live ? dl : 0.f;
-        dd[e] = make_float2(dl, dl * x.a.u.get(e));
+      for (int e = 0; e < EV; ++e) dl[e] = x.dt.get(e) + bias[e];
+      if (p.softplus) {
+#pragma unroll
+        for (int e = 0; e < EV; ++e) dl[e] = softplus(dl[e]);
       }
+      // (a channel that is not there has u = 0 and takes nothing up; what its
+      // state decays by does not matter)
+#pragma unroll
+      for (int e = 0; e < EV; ++e) dl[e] = live ? dl[e] : 0.f;
+#pragma unroll
+      for (int e = 0; e < EV; e += 2)
+        *reinterpret_cast<float4*>(dd + e) =
+            make_float4(dl[e], dl[e] * x.a.u.get(e), dl[e + 1], dl[e + 1] * x.a.u.get(e + 1));
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
         const int v = et + j * NE;
@@ -165,9 +182,10 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
       float o[EV];
       load_f<EV>(&sm.ys[k & 1][i * G::YS + cl], o);
 #pragma unroll
-      for (int e = 0; e < EV; ++e) {
-        o[e] = fmaf(Ds[e], x.u.get(e), o[e]);
-        if (p.z) {
+      for (int e = 0; e < EV; ++e) o[e] = fmaf(Ds[e], x.u.get(e), o[e]);
+      if (p.z) {
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
           const float z = x.z.get(e);
           o[e] *= z * sigm(z);
         }
@@ -239,8 +257,12 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
     const IO* bf = sm.bf[k & 1] + n0;
     const IO* cf = sm.cf[k & 1] + n0;
     float* ys = sm.ys[k & 1] + cl;
+    // (a tile of 8 tokens starts at a 16th one every other time)
     const int t = t0 + k * TT;
-    scan_tile<IO, L, END>(p, dd, bf, cf, ys, A2, h, sumd, lane, l, b, c, n0, on, t, te);
+    const bool ck = p.states && on && t % kCk == 0;
+    scan_tile<IO, L, END>(dd, bf, cf, ys, A2, h, sumd, lane, l,
+                          p.states + (((size_t)b * ((p.T + kCk - 1) / kCk) + t / kCk) * p.D + c) * p.N + n0,
+                          (size_t)p.D * p.N, ck ? te - t : 0);
     __syncthreads();
   }
   const float4 hv = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
