@@ -31,89 +31,122 @@ struct alignas(16) Smem {
   IO bf[2][TB * NP], cf[2][TB * NP];
   float gB[2][TB * Geo<L>::YS], gA[2][TB * Geo<L>::YS], yc[2][TB * Geo<L>::YS];
   float red[2][kWarps][TB][2 * NP];  // dB, dC over a warp's channels
+  float4 ck[2][NS];  // the state before the tile, as the scan threads hold it
 };
 
-// The scan warps' walk over one tile, forward and back.
+// The scan warps' walk over one tile, forward and back.  Sums over lanes take
+// an exchange's latency a stage, and a shared memory store waits for its
+// value while the loads behind it wait for the store; so a token's operands
+// are loaded, and the next token's arithmetic done, before its sums over the
+// channels are formed and stored.
 template <typename IO, int L>
-__device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const float2* q,
-                                          const float* qe, const IO* bf,
-                                          const IO* cf, float* gB,
-                                          float* gA, float* yc,
-                                          float* red, const f2 (&A2)[2], f2 (&gr)[2], f2& dt0,
-                                          f2& dt1, int lane, int l) {
+__device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const float2* q, const float* qe,
+                                          const IO* bf, const IO* cf, float* gB, float* gA, float* yc, float* red,
+                                          f2 (&A2)[2], f2 (&gr)[2], f2 (&dA)[2], int lane, int l) {
   using G = Geo<L>;
   constexpr int NP = G::NP, U = G::U, YS = G::YS, DS = Smem<IO, L>::DS;
-  // forward over the tile: the state after every token, h[i + 1]
+  // ---- forward: the state after every token, h[i + 1]
   f2 h[TB + 1][2];
   h[0][0] = pk(h0.x, h0.y);
   h[0][1] = pk(h0.z, h0.w);
+  {
+    f2 a[2][U][2], x[2][U][2];
+    auto form = [&](int i, f2 (&a)[U][2], f2 (&x)[U][2]) {
 #pragma unroll
-  for (int i = 0; i < TB; i += U) {
-    float yv[U];
+      for (int j = 0; j < U; ++j) {
+        const float2 d = q[(i + j) * DS];
+        f2 B0, B1;
+        load_bc(bf + (i + j) * NP, B0, B1);
+        const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
+        a[j][0] = ex2v(mul2(A2[0], d2));
+        a[j][1] = ex2v(mul2(A2[1], d2));
+        x[j][0] = mul2(du2, B0);
+        x[j][1] = mul2(du2, B1);
+      }
+    };
+    form(0, a[0], x[0]);
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int m = i + j;
-      const float2 x = q[m * DS];
-      f2 B0, B1;
-      load_bc(bf + m * NP, B0, B1);
-      const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y);
-      h[m + 1][0] = fma2(ex2v(mul2(A2[0], d2)), h[m][0], mul2(du2, B0));
-      h[m + 1][1] = fma2(ex2v(mul2(A2[1], d2)), h[m][1], mul2(du2, B1));
+    for (int k = 0; k < TB / U; ++k) {
+      const int i = k * U;
+      if (i + U < TB) form(i + U, a[(k + 1) & 1], x[(k + 1) & 1]);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        h[i + j + 1][0] = fma2(a[k & 1][j][0], h[i + j][0], x[k & 1][j][0]);
+        h[i + j + 1][1] = fma2(a[k & 1][j][1], h[i + j][1], x[k & 1][j][1]);
+      }
       if (want_y) {
-        f2 C0, C1;
-      load_bc(cf + m * NP, C0, C1);
-        const f2 y2 = fma2(h[m + 1][1], C1, mul2(h[m + 1][0], C0));
-        yv[j] = lo(y2) + hi(y2);
+        float yv[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          f2 C0, C1;
+          load_bc(cf + (i + j) * NP, C0, C1);
+          const f2 y2 = fma2(h[i + j + 1][1], C1, mul2(h[i + j + 1][0], C0));
+          yv[j] = lo(y2) + hi(y2);
+        }
+        int j = 0;
+        reduce_scatter<U, L / 2, 1>(yv, lane, j);
+        if (l % (L / U) == 0) yc[(i + j) * YS] = yv[0];
       }
     }
-    if (want_y) {
-      int j = 0;
-      reduce_scatter<U, L / 2, 1>(yv, lane, j);
-      if (l % (L / U) == 0) yc[(i + j) * YS] = yv[0];
-    }
   }
-  // and back; a is taken again, which costs less than keeping it (and the
+  // ---- and back.  a is taken again, which costs less than keeping it (and the
   // compiler is kept from keeping it: 64 more registers would be spilled)
-  f2 R2[2] = {A2[0], A2[1]};
-  asm volatile("" : "+l"(R2[0]), "+l"(R2[1]));
+  asm volatile("" : "+l"(A2[0]), "+l"(A2[1]));
+  struct Op {
+    float2 d;
+    float e;
+    f2 B0, B1, C0, C1;
+  };
+  auto load = [&](int m, Op& o) {
+    o.d = q[m * DS];
+    o.e = qe[m * DS];
+    load_bc(bf + m * NP, o.B0, o.B1);
+    load_bc(cf + m * NP, o.C0, o.C1);
+  };
+  // dB and dC of token m: over the warp's channels, then to the block's table
+  auto sum_bc = [&](int m, float (&v)[8]) {
+    int base = 0;
+    reduce_scatter<8, 16, L>(v, lane, base);
+    // what is left of the 8: 1 for L <= 4 (equal in the lanes that differ
+    // below bit 2 and from L up), 2 for L = 8, 4 for L = 16
+    constexpr int LEFT = L <= 4 ? 1 : L / 4;
+    if (L >= 4 || (lane & 3 & ~(L - 1)) == 0) {
+#pragma unroll
+      for (int y = 0; y < LEFT; ++y) {
+        const int z = base + y;
+        red[m * 2 * NP + (z >> 2) * NP + (z & 3)] = v[y];
+      }
+    }
+  };
+  Op op[2];
+  float v[2][8];
+  load(TB - 1, op[(TB - 1) & 1]);
 #pragma unroll
   for (int i = TB - U; i >= 0; i -= U) {
     float vB[U], vA[U];
 #pragma unroll
     for (int j = U - 1; j >= 0; --j) {
       const int m = i + j;
-      const float2 x = q[m * DS];
-      f2 B0, B1;
-      load_bc(bf + m * NP, B0, B1);
-      f2 C0, C1;
-      load_bc(cf + m * NP, C0, C1);
-      const f2 d2 = pk(x.x, x.x), du2 = pk(x.y, x.y), e2 = pk(qe[m * DS], qe[m * DS]);
-      gr[0] = fma2(e2, C0, gr[0]);
-      gr[1] = fma2(e2, C1, gr[1]);
+      if (m > 0) load(m - 1, op[(m - 1) & 1]);
+      const Op& o = op[m & 1];
+      const f2 d2 = pk(o.d.x, o.d.x), du2 = pk(o.d.y, o.d.y), e2 = pk(o.e, o.e);
+      gr[0] = fma2(e2, o.C0, gr[0]);
+      gr[1] = fma2(e2, o.C1, gr[1]);
       const f2 dB0 = mul2(gr[0], du2), dB1 = mul2(gr[1], du2);
       const f2 dC0 = mul2(h[m + 1][0], e2), dC1 = mul2(h[m + 1][1], e2);
-      const f2 sB = fma2(gr[1], B1, mul2(gr[0], B0));
-      gr[0] = mul2(gr[0], ex2v(mul2(R2[0], d2)));
-      gr[1] = mul2(gr[1], ex2v(mul2(R2[1], d2)));
+      const f2 sB = fma2(gr[1], o.B1, mul2(gr[0], o.B0));
+      gr[0] = mul2(gr[0], ex2v(mul2(A2[0], d2)));
+      gr[1] = mul2(gr[1], ex2v(mul2(A2[1], d2)));
       const f2 gp0 = mul2(gr[0], h[m][0]), gp1 = mul2(gr[1], h[m][1]);
       const f2 sA = fma2(gp1, A2[1], mul2(gp0, A2[0]));
-      dt0 = fma2(gp0, d2, dt0);
-      dt1 = fma2(gp1, d2, dt1);
+      dA[0] = fma2(gp0, d2, dA[0]);
+      dA[1] = fma2(gp1, d2, dA[1]);
       vB[j] = lo(sB) + hi(sB);
       vA[j] = lo(sA) + hi(sA);
-      float v[8] = {lo(dB0), hi(dB0), lo(dB1), hi(dB1), lo(dC0), hi(dC0), lo(dC1), hi(dC1)};
-      int base = 0;
-      reduce_scatter<8, 16, L>(v, lane, base);
-      // what is left of the 8: 1 for L <= 4 (equal in the lanes that differ
-      // below bit 2 and from L up), 2 for L = 8, 4 for L = 16
-      constexpr int LEFT = L <= 4 ? 1 : L / 4;
-      if (L >= 4 || (lane & 3 & ~(L - 1)) == 0) {
-#pragma unroll
-        for (int y = 0; y < LEFT; ++y) {
-          const int z = base + y;
-          red[m * 2 * NP + (z >> 2) * NP + (z & 3)] = v[y];
-        }
-      }
+      float (&w)[8] = v[m & 1];
+      w[0] = lo(dB0); w[1] = hi(dB0); w[2] = lo(dB1); w[3] = hi(dB1);
+      w[4] = lo(dC0); w[5] = hi(dC0); w[6] = lo(dC1); w[7] = hi(dC1);
+      if (m + 1 < TB) sum_bc(m + 1, v[(m + 1) & 1]);
     }
     int j = 0;
     reduce_scatter<U, L / 2, 1>(vB, lane, j);
@@ -124,6 +157,7 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
       gA[(i + j) * YS] = vA[0];
     }
   }
+  sum_bc(0, v[0]);
 }
 
 // END: only the gradient that the segment hands to the one before it when
@@ -188,6 +222,11 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
       pb[j] = (const IO*)p.Bm + (p.rb.at(b, 0) + g * p.N + n0) + (int64_t)(tl + v / L) * p.rb.ld;
       pc[j] = (const IO*)p.Cm + (p.rc.at(b, 0) + g * p.N + n0) + (int64_t)(tl + v / L) * p.rc.ld;
     }
+    // a saved state: 4 of them, those of the scan thread of the same number
+    float4 ck = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool ck_on = !END && c0 + et / L < cmax && et % L * 4 < p.N;
+    const size_t nck = (p.T + kCk - 1) / kCk;
+    const float* pck = p.states + ((b * nck + tl / kCk) * p.D + c0 + et / L) * p.N + et % L * 4;
     auto load = [&](int k) {
       const int tt = t0 + (ntile - 1 - k) * TB;
 #pragma unroll
@@ -211,9 +250,12 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
         pc[j] -= TB * p.rc.ld;
         pb[j] -= TB * p.rb.ld;
       }
+      if (ck_on) ck = __ldg(reinterpret_cast<const float4*>(pck));
+      pck -= (size_t)p.D * p.N;
     };
     auto prepare = [&](int k, Tok (&tok)[PASS]) {
       const int tt = t0 + (ntile - 1 - k) * TB;
+      if (!END) sm.ck[k & 1][et] = ck;
 #pragma unroll
       for (int s = 0; s < PASS; ++s) {
         const int i = i0 + s * IS;
@@ -360,15 +402,9 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
   const int cl = tid / L, l = tid % L, c = c0 + cl;
   const int n0 = 4 * l;
   const bool on = c < cmax && n0 < p.N;
-  const int nck = (p.T + kCk - 1) / kCk;
   const size_t sidx = ((size_t)b * p.D + c) * p.N + n0;
   const size_t sstep = (size_t)p.B * p.D * p.N;
-  const float* ckp = p.states + ((size_t)b * nck * p.D + c) * p.N + n0;
-  f2 A2[2] = {0, 0}, gr[2] = {0, 0}, dA[2] = {0, 0}, dAc[2] = {0, 0};
-  float4 ck = make_float4(0.f, 0.f, 0.f, 0.f);  // the state before the tile, loaded a tile ahead
-  auto load_ck = [&](int k) {
-    if (on) ck = __ldg(reinterpret_cast<const float4*>(ckp + (size_t)(t0 / kCk + ntile - 1 - k) * p.D * p.N));
-  };
+  f2 A2[2] = {0, 0}, gr[2] = {0, 0}, dA[2] = {0, 0}, dAt[2] = {0, 0};
   if (on) {
     const float4 a = *reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0);
     A2[0] = pk(a.x * kLog2e, a.y * kLog2e);
@@ -385,7 +421,6 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
         gr[0] = fma2(ex2v(mul2(A2[0], pk(d, d))), gr[0], pk(x.x, x.y));
         gr[1] = fma2(ex2v(mul2(A2[1], pk(d, d))), gr[1], pk(x.z, x.w));
       }
-      if (ntile > 0) load_ck(0);
     }
   }
   float sumd = 0.f;
@@ -408,17 +443,16 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
         sumd += d;
       }
     } else {
-      f2 dt0 = 0, dt1 = 0;  // dA of the tile
-      const float4 h0 = ck;
-      if (k + 1 < ntile) load_ck(k + 1);
-      walk_tile<IO, L>(p.dz != nullptr, h0, q, qe, bf, cf, sm.gB[w] + cl, sm.gA[w] + cl, sm.yc[w] + cl,
-                   &sm.red[w][warp][0][0] + n0, A2, gr, dt0, dt1, lane, l);
-      // dA over thousands of tiles: the sum carries the rounding of each addition on
+      walk_tile<IO, L>(p.dz != nullptr, sm.ck[w][tid], q, qe, bf, cf, sm.gB[w] + cl, sm.gA[w] + cl, sm.yc[w] + cl,
+                       &sm.red[w][warp][0][0] + n0, A2, gr, dAt, lane, l);
+      // dA over 16 tiles at a time: thousands of tokens added to one sum would
+      // cost it bits
+      if (k % 16 == 15) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const f2 y = add2(x ? dt1 : dt0, dAc[x]), s = add2(dA[x], y);
-        dAc[x] = add2(y, mul2(pk(-1.f, -1.f), add2(s, mul2(pk(-1.f, -1.f), dA[x]))));
-        dA[x] = s;
+        for (int x = 0; x < 2; ++x) {
+          dA[x] = add2(dA[x], dAt[x]);
+          dAt[x] = 0;
+        }
       }
     }
     __syncthreads();
@@ -429,6 +463,8 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
     if (c < cmax && l == 0) p.segD[((size_t)seg * p.B + b) * p.D + c] = sumd;
     return;
   }
+  dA[0] = add2(dA[0], dAt[0]);
+  dA[1] = add2(dA[1], dAt[1]);
   if (p.dh0 && on && seg == 0) *reinterpret_cast<float4*>(p.dh0 + sidx) = gv;
   if (on)
     *reinterpret_cast<float4*>(part + (size_t)c * p.N + n0) =
