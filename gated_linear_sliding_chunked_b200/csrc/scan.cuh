@@ -1,16 +1,17 @@
 // Shared parts of the selective state space scan kernels.
 //
-// Layout of the work: a channel's N states lie across L = ceil(N/4) lanes
-// (rounded up to a power of two) of a warp, 4 states a lane, and the four scan
-// warps of a block hold 128/L neighbouring channels of one sequence, with the
-// state in registers.  The tokens are walked in tiles.  Four more warps do
-// what is elementwise in (token, channel): while the scan warps walk a tile,
-// they finish the outputs of the tile before and prepare the steps (softplus),
-// inputs and gates of the tile behind, whose global loads they issued a tile
-// earlier.  One block-wide barrier a tile hands the shared memory buffers over.
-// Without the split the scan warps would wait out the loads, the softplus and
-// the stores of every tile, with too few warps on an SM to hide it: a layer
-// has only (sequences x channels x N/4)/32 of them.
+// Layout of the work: a channel's states lie across lanes of a warp, 4 states of
+// a channel to a thread in the forward, 2 neighbouring states of 2 neighbouring
+// channels in the backward; the four scan warps of a block hold NS * 4 / N
+// channels (N rounded up to a power of two) of one sequence.  The tokens are
+// walked in tiles.  Four more warps do what is elementwise in (token,
+// channel): while the scan warps walk a tile, they finish the outputs of the
+// tile before and prepare the steps (softplus), inputs and gates of the tile
+// behind, whose global loads they issued a tile earlier.  One block-wide
+// barrier a tile hands the shared memory buffers over.  Without the split the
+// scan warps would wait out the loads, the softplus and the stores of every
+// tile, with too few warps on an SM to hide it: a layer has only (sequences x
+// channels x N/4)/32 of them.
 //
 // One exp per (token, channel, state) cannot be done without: 16 a cycle and
 // SM, which outweighs the tokens' bytes.
@@ -107,9 +108,8 @@ __device__ __forceinline__ f2 ex2v(f2 x) { return pk(ex2(lo(x)), ex2(hi(x))); }
 // sigma(x).  log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3, by the series
 // s + s^3/3 + .. + s^15/15 (the rest is below 2^-29 of it): accurate relative
 // to the result also where e is small, which is where steps live.
-__device__ __forceinline__ float softplus_parts(float x, float& e) {
-  e = ex2(-kLog2e * fabsf(x));
-  const float s = e * rcp(2.f + e), q = s * s;
+__device__ __forceinline__ float softplus_of(float x, float s) {
+  const float q = s * s;
   float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
   p = fmaf(q, p, 1.f / 11.f);
   p = fmaf(q, p, 1.f / 9.f);
@@ -120,8 +120,14 @@ __device__ __forceinline__ float softplus_parts(float x, float& e) {
   return fmaxf(x, 0.f) + fmaf(t * q, p, t);
 }
 __device__ __forceinline__ float softplus(float x) {
-  float e;
-  return softplus_parts(x, e);
+  const float e = ex2(-kLog2e * fabsf(x));
+  return softplus_of(x, e * rcp(2.f + e));
+}
+// with sigma(x), both quotients from one reciprocal
+__device__ __forceinline__ float softplus(float x, float& sg) {
+  const float e = ex2(-kLog2e * fabsf(x)), a = 1.f + e, b = 2.f + e, r = rcp(a * b);
+  sg = b * r * (x >= 0.f ? 1.f : e);
+  return softplus_of(x, e * a * r);
 }
 
 // V consecutive elements of a row as they are in memory
@@ -141,25 +147,27 @@ struct Pack {
     if constexpr (W == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   }
-  // in 16-, 8- or 4-byte accesses when vec (the row allows it), else element
-  // by element; n of the V elements exist (all or none of them when vec)
+  // n of the V elements exist; the rest becomes zero.  In 16-, 8- or 4-byte
+  // accesses when vec: the row allows it and n is V or none.  (Written out
+  // under both conditions: a value kept where there is nothing to load would be
+  // selected after the load, which then waits for memory there and then.)
   __device__ __forceinline__ void load(const IO* p, int n, bool vec) {
     if (vec) {
-      if (n <= 0) {
-        zero();
-        return;
-      }
-      if constexpr (W % 4 == 0) {
+      if (n > 0) {
+        if constexpr (W % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < W; i += 4) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
-          w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+          for (int i = 0; i < W; i += 4) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+            w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+          }
+        } else if constexpr (W % 2 == 0) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+          w[0] = x.x; w[1] = x.y;
+        } else {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
         }
-      } else if constexpr (W % 2 == 0) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-        w[0] = x.x; w[1] = x.y;
       } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        zero();
       }
     } else {
       zero();
@@ -172,23 +180,6 @@ struct Pack {
     }
   }
 };
-
-// 4 elements of B or C as the scan warps read them from shared memory, as pairs
-// of floats.  They stay in the I/O type there: what a warp's shared memory
-// loads return to registers, 128 bytes a cycle and SM however many lanes read
-// the same words, is what the scan runs out of first.
-template <typename IO>
-__device__ __forceinline__ void load_bc(const IO* p, f2& x, f2& y) {
-  if constexpr (sizeof(IO) == 4) {
-    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
-    x = v.x;
-    y = v.y;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    x = pk(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
-    y = pk(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
-  }
-}
 
 // V floats from shared memory (16- or 8-byte aligned as V allows)
 template <int V>
@@ -255,28 +246,20 @@ __device__ __forceinline__ void reduce_scatter(float (&v)[SZ], int lane, int& ba
   }
 }
 
-template <int L>
-struct Geo {
-  static constexpr int CH = NS / L;         // channels of a block
-  static constexpr int NP = 4 * L;          // states, padded
-  static constexpr int U = L < 4 ? L : 4;   // tokens whose lane sums are formed together
-  static constexpr int PAD = 32 / L < 4 ? 4 : 32 / L;
-  static constexpr int YS = CH + PAD;       // row of a [tokens][channels] fp32 tile
-};
-
 // Floats from one partial row of the parameter gradients to the next: rows
 // are written in vectors of 4
 __host__ __device__ inline size_t part_ld(int D, int N) { return ((size_t)D * (N + 2) + 3) / 4 * 4; }
 
-inline int lanes_of(int N) {
-  int l = 1;
-  while (4 * l < N) l *= 2;
-  return l;
+// N rounded up to a power of two, at least 4
+inline int states_of(int N) {
+  int n = 4;
+  while (n < N) n *= 2;
+  return n;
 }
 
 }  // namespace scan
 
-cudaError_t launch_scan_fwd(const scan::ScanParams& p, int L, bool bf, cudaStream_t s);
-cudaError_t launch_scan_bwd(const scan::ScanParams& p, int L, bool bf, cudaStream_t s);
+cudaError_t launch_scan_fwd(const scan::ScanParams& p, bool bf, cudaStream_t s);
+cudaError_t launch_scan_bwd(const scan::ScanParams& p, bool bf, cudaStream_t s);
 
 }  // namespace lz

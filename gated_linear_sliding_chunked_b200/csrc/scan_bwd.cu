@@ -19,19 +19,68 @@ namespace lz {
 namespace scan {
 namespace {
 
+// A thread holds 2 channels x 2 states: pairs of channels are what the packed
+// arithmetic works on, and the sums over channels start within the thread.  (4
+// states of one channel to a thread took 28 instructions a token for those
+// sums against 14, and moves to repeat each step and input in a pair of
+// registers: 1745 us against 1677 us at 2 x 8192 tokens, 4096 channels, 16
+// states.)  L: lanes of a channel pair.
+template <int L>
+struct Geo {
+  static constexpr int CH = 2 * NS / L;     // channels of a block
+  static constexpr int NP = 2 * L;          // states, padded
+  static constexpr int U = L < 8 ? L / 2 : 4;  // tokens whose lane sums are formed together
+  // a [tokens][channels] fp32 tile: rows off the banks of the rows written with them
+  static constexpr int YS = CH + (L == 4 ? 16 : L == 8 ? 8 : 4);
+  static constexpr int DS = CH / 2 + 1;     // row of a [tokens][channel pairs] tile of 4 words
+};
+
+// 2 elements of B or C as the scan warps read them from shared memory, each
+// twice in a register pair.  They stay in the I/O type there: what a warp's
+// shared memory loads return to registers, 128 bytes a cycle and SM however
+// many lanes read the same words, is what the scan runs out of first.
+template <typename IO>
+__device__ __forceinline__ void load_bc(const IO* p, f2& x, f2& y) {
+  float a, b;
+  if constexpr (sizeof(IO) == 4) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    a = v.x;
+    b = v.y;
+  } else {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    a = __uint_as_float(v << 16);
+    b = __uint_as_float(v & 0xffff0000u);
+  }
+  x = pk(a, a);
+  y = pk(b, b);
+}
+
+// A thread's 2 channels x 2 states of an array [.., D][N] (p: its first): s[i]
+// is state i of both channels.
+__device__ __forceinline__ void load_state(const float* p, int N, bool on0, bool on1, f2 (&s)[2]) {
+  float2 a = make_float2(0.f, 0.f), b = a;
+  if (on0) a = *reinterpret_cast<const float2*>(p);
+  if (on1) b = *reinterpret_cast<const float2*>(p + N);
+  s[0] = pk(a.x, b.x);
+  s[1] = pk(a.y, b.y);
+}
+__device__ __forceinline__ void store_state(float* p, int N, bool on0, bool on1, const f2 (&s)[2]) {
+  if (on0) *reinterpret_cast<float2*>(p) = make_float2(lo(s[0]), lo(s[1]));
+  if (on1) *reinterpret_cast<float2*>(p + N) = make_float2(hi(s[0]), hi(s[1]));
+}
+
 constexpr int TB = kCk;  // tokens of a tile
 constexpr int kWarps = NS / 32;
 
 template <typename IO, int L>
 struct alignas(16) Smem {
-  static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP;
-  static constexpr int DS = CH + 2;  // row of q and qe, off the banks of the row before
-  float2 q[2][TB * DS];  // delta, delta u
-  float qe[2][TB * DS];  // e
+  static constexpr int NP = Geo<L>::NP;
+  float4 q[2][TB * Geo<L>::DS];       // of a channel pair: delta, delta; delta u, delta u
+  float2 qe[2][TB * Geo<L>::DS];      // e, e
   IO bf[2][TB * NP], cf[2][TB * NP];
   float gB[2][TB * Geo<L>::YS], gA[2][TB * Geo<L>::YS], yc[2][TB * Geo<L>::YS];
   float red[2][kWarps][TB][2 * NP];  // dB, dC over a warp's channels
-  float4 ck[2][NS];  // the state before the tile, as the scan threads hold it
+  ulonglong2 ck[2][NS];  // the state before the tile, as the scan threads hold it
 };
 
 // The scan warps' walk over one tile, forward and back.  Sums over lanes take
@@ -40,28 +89,27 @@ struct alignas(16) Smem {
 // are loaded, and the next token's arithmetic done, before its sums over the
 // channels are formed and stored.
 template <typename IO, int L>
-__device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const float2* q, const float* qe,
+__device__ __forceinline__ void walk_tile(bool want_y, const ulonglong2 h0, const float4* q, const float2* qe,
                                           const IO* bf, const IO* cf, float* gB, float* gA, float* yc, float* red,
                                           f2 (&A2)[2], f2 (&gr)[2], f2 (&dA)[2], int lane, int l) {
   using G = Geo<L>;
-  constexpr int NP = G::NP, U = G::U, YS = G::YS, DS = Smem<IO, L>::DS;
+  constexpr int NP = G::NP, U = G::U, YS = G::YS, DS = G::DS;
   // ---- forward: the state after every token, h[i + 1]
   f2 h[TB + 1][2];
-  h[0][0] = pk(h0.x, h0.y);
-  h[0][1] = pk(h0.z, h0.w);
+  h[0][0] = h0.x;
+  h[0][1] = h0.y;
   {
     f2 a[2][U][2], x[2][U][2];
     auto form = [&](int i, f2 (&a)[U][2], f2 (&x)[U][2]) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const float2 d = q[(i + j) * DS];
+        const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&q[(i + j) * DS]);
         f2 B0, B1;
         load_bc(bf + (i + j) * NP, B0, B1);
-        const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
-        a[j][0] = ex2v(mul2(A2[0], d2));
-        a[j][1] = ex2v(mul2(A2[1], d2));
-        x[j][0] = mul2(du2, B0);
-        x[j][1] = mul2(du2, B1);
+        a[j][0] = ex2v(mul2(A2[0], d.x));
+        a[j][1] = ex2v(mul2(A2[1], d.x));
+        x[j][0] = mul2(d.y, B0);
+        x[j][1] = mul2(d.y, B1);
       }
     };
     form(0, a[0], x[0]);
@@ -75,17 +123,18 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
         h[i + j + 1][1] = fma2(a[k & 1][j][1], h[i + j][1], x[k & 1][j][1]);
       }
       if (want_y) {
-        float yv[U];
+        float yv[2 * U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
           f2 C0, C1;
           load_bc(cf + (i + j) * NP, C0, C1);
           const f2 y2 = fma2(h[i + j + 1][1], C1, mul2(h[i + j + 1][0], C0));
-          yv[j] = lo(y2) + hi(y2);
+          yv[2 * j] = lo(y2);
+          yv[2 * j + 1] = hi(y2);
         }
         int j = 0;
-        reduce_scatter<U, L / 2, 1>(yv, lane, j);
-        if (l % (L / U) == 0) yc[(i + j) * YS] = yv[0];
+        reduce_scatter<2 * U, L / 2, 1>(yv, lane, j);
+        if (l % (L / (2 * U)) == 0) yc[(i + (j >> 1)) * YS + (j & 1)] = yv[0];
       }
     }
   }
@@ -93,43 +142,42 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
   // compiler is kept from keeping it: 64 more registers would be spilled)
   asm volatile("" : "+l"(A2[0]), "+l"(A2[1]));
   struct Op {
-    float2 d;
-    float e;
-    f2 B0, B1, C0, C1;
+    ulonglong2 d;
+    f2 e, B0, B1, C0, C1;
   };
   auto load = [&](int m, Op& o) {
-    o.d = q[m * DS];
-    o.e = qe[m * DS];
+    o.d = *reinterpret_cast<const ulonglong2*>(&q[m * DS]);
+    o.e = *reinterpret_cast<const f2*>(&qe[m * DS]);
     load_bc(bf + m * NP, o.B0, o.B1);
     load_bc(cf + m * NP, o.C0, o.C1);
   };
   // dB and dC of token m: over the warp's channels, then to the block's table
-  auto sum_bc = [&](int m, float (&v)[8]) {
+  auto sum_bc = [&](int m, float (&v)[4]) {
     int base = 0;
-    reduce_scatter<8, 16, L>(v, lane, base);
-    // what is left of the 8: 1 for L <= 4 (equal in the lanes that differ
-    // below bit 2 and from L up), 2 for L = 8, 4 for L = 16
-    constexpr int LEFT = L <= 4 ? 1 : L / 4;
-    if (L >= 4 || (lane & 3 & ~(L - 1)) == 0) {
+    reduce_scatter<4, 16, L>(v, lane, base);
+    // what is left of the 4: 1 for L <= 8 (equal in the lanes that differ in a
+    // bit below 8 and not below L), 2 for L = 16, 4 for L = 32
+    constexpr int LEFT = L <= 8 ? 1 : L / 8;
+    if ((lane & 7 & ~(L - 1)) == 0) {
 #pragma unroll
       for (int y = 0; y < LEFT; ++y) {
         const int z = base + y;
-        red[m * 2 * NP + (z >> 2) * NP + (z & 3)] = v[y];
+        red[m * 2 * NP + (z >> 1) * NP + (z & 1)] = v[y];
       }
     }
   };
   Op op[2];
-  float v[2][8];
+  float v[2][4];
   load(TB - 1, op[(TB - 1) & 1]);
 #pragma unroll
   for (int i = TB - U; i >= 0; i -= U) {
-    float vB[U], vA[U];
+    float vB[2 * U], vA[2 * U];
 #pragma unroll
     for (int j = U - 1; j >= 0; --j) {
       const int m = i + j;
       if (m > 0) load(m - 1, op[(m - 1) & 1]);
       const Op& o = op[m & 1];
-      const f2 d2 = pk(o.d.x, o.d.x), du2 = pk(o.d.y, o.d.y), e2 = pk(o.e, o.e);
+      const f2 d2 = o.d.x, du2 = o.d.y, e2 = o.e;
       gr[0] = fma2(e2, o.C0, gr[0]);
       gr[1] = fma2(e2, o.C1, gr[1]);
       const f2 dB0 = mul2(gr[0], du2), dB1 = mul2(gr[1], du2);
@@ -141,20 +189,24 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
       const f2 sA = fma2(gp1, A2[1], mul2(gp0, A2[0]));
       dA[0] = fma2(gp0, d2, dA[0]);
       dA[1] = fma2(gp1, d2, dA[1]);
-      vB[j] = lo(sB) + hi(sB);
-      vA[j] = lo(sA) + hi(sA);
-      float (&w)[8] = v[m & 1];
-      w[0] = lo(dB0); w[1] = hi(dB0); w[2] = lo(dB1); w[3] = hi(dB1);
-      w[4] = lo(dC0); w[5] = hi(dC0); w[6] = lo(dC1); w[7] = hi(dC1);
+      vB[2 * j] = lo(sB);
+      vB[2 * j + 1] = hi(sB);
+      vA[2 * j] = lo(sA);
+      vA[2 * j + 1] = hi(sA);
+      float (&w)[4] = v[m & 1];  // over the thread's two channels
+      w[0] = lo(dB0) + hi(dB0);
+      w[1] = lo(dB1) + hi(dB1);
+      w[2] = lo(dC0) + hi(dC0);
+      w[3] = lo(dC1) + hi(dC1);
       if (m + 1 < TB) sum_bc(m + 1, v[(m + 1) & 1]);
     }
     int j = 0;
-    reduce_scatter<U, L / 2, 1>(vB, lane, j);
+    reduce_scatter<2 * U, L / 2, 1>(vB, lane, j);
     j = 0;
-    reduce_scatter<U, L / 2, 1>(vA, lane, j);
-    if (l % (L / U) == 0) {
-      gB[(i + j) * YS] = vB[0];
-      gA[(i + j) * YS] = vA[0];
+    reduce_scatter<2 * U, L / 2, 1>(vA, lane, j);
+    if (l % (L / (2 * U)) == 0) {
+      gB[(i + (j >> 1)) * YS + (j & 1)] = vB[0];
+      gA[(i + (j >> 1)) * YS + (j & 1)] = vA[0];
     }
   }
   sum_bc(0, v[0]);
@@ -163,13 +215,13 @@ __device__ __forceinline__ void walk_tile(bool want_y, const float4 h0, const fl
 // END: only the gradient that the segment hands to the one before it when
 // none comes from behind (the state gradient before its first token).
 template <typename IO, int L, bool END>
-__global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(NT, L >= 8 ? 2 : 1) scan_bwd_kernel(ScanParams p) {
   using G = Geo<L>;
   constexpr int CH = G::CH, NP = G::NP, YS = G::YS;
   constexpr int EV = TB * CH / NE > 1 ? (TB * CH / NE < 8 ? TB * CH / NE : 8) : 2;  // channels of an elementwise thread
   constexpr int ROWT = CH / EV;                                 // threads of a token
   constexpr int PASS = (TB * ROWT + NE - 1) / NE;               // tokens of a thread
-  constexpr int BN = TB * L > NE ? TB * L / NE : 1;             // its 4-element vectors of B and of C
+  constexpr int BV = TB * NP / 4, BN = BV > NE ? BV / NE : 1;   // 4-element vectors of B and of C, a thread's
   extern __shared__ __align__(16) char raw[];
   using S = Smem<IO, L>;
   S& sm = *reinterpret_cast<S*>(raw);
@@ -198,7 +250,7 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
     };
     Next nx[PASS];
     Pack<IO, 4> nb[BN], ncv[BN];
-    Tok cur[PASS], last[PASS];
+    Tok tok[2][PASS];
     float Ds[EV], bias[EV], sD[EV], sT[EV];
 #pragma unroll
     for (int e = 0; e < EV; ++e) {
@@ -206,80 +258,84 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
       bias[e] = p.dtb && e < nc ? p.dtb[c + e] : 0.f;
       sD[e] = sT[e] = 0.f;
     }
-    // this thread's elements of the next tile to load (from the last tile down)
+    // Pointers to this thread's elements: of the next tile to load, and of the
+    // next tile of outputs, from the last tile down.
     const int tl = t0 + (ntile - 1) * TB;
-    const Rows rdy{p.D, (int64_t)p.T * p.D};
+    const int64_t tok0 = (int64_t)b * p.T + tl + i0;  // row of a contiguous array
     const IO* pu = (const IO*)p.u + (p.ru.at(b, 0) + c) + (int64_t)(tl + i0) * p.ru.ld;
     const IO* pdt = (const IO*)p.dt + (p.rdt.at(b, 0) + c) + (int64_t)(tl + i0) * p.rdt.ld;
-    const IO* pdy = (const IO*)p.dy + (rdy.at(b, 0) + c) + (int64_t)(tl + i0) * rdy.ld;
-    const IO* pz = p.z ? (const IO*)p.z + (p.rz.at(b, 0) + c) + (int64_t)(tl + i0) * p.rz.ld : nullptr;
+    const IO* pdy = (const IO*)p.dy + tok0 * p.D + c;
+    const IO* pz = (const IO*)p.z + (p.rz.at(b, 0) + c) + (int64_t)(tl + i0) * p.rz.ld;
     const IO *pb[BN], *pc[BN];
     int nbn[BN];
 #pragma unroll
     for (int j = 0; j < BN; ++j) {
-      const int v = et + j * NE, n0 = v % L * 4;
-      nbn[j] = v < TB * L ? p.N - n0 : 0;
-      pb[j] = (const IO*)p.Bm + (p.rb.at(b, 0) + g * p.N + n0) + (int64_t)(tl + v / L) * p.rb.ld;
-      pc[j] = (const IO*)p.Cm + (p.rc.at(b, 0) + g * p.N + n0) + (int64_t)(tl + v / L) * p.rc.ld;
+      const int v = et + j * NE, n0 = v % (L / 2) * 4;
+      nbn[j] = v < BV ? p.N - n0 : 0;
+      pb[j] = (const IO*)p.Bm + (p.rb.at(b, 0) + g * p.N + n0) + (int64_t)(tl + v / (L / 2)) * p.rb.ld;
+      pc[j] = (const IO*)p.Cm + (p.rc.at(b, 0) + g * p.N + n0) + (int64_t)(tl + v / (L / 2)) * p.rc.ld;
     }
     // a saved state: 4 of them, those of the scan thread of the same number
-    float4 ck = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool ck_on = !END && c0 + et / L < cmax && et % L * 4 < p.N;
+    f2 ck[2] = {0, 0};
+    const int ckc = c0 + et / L * 2, ckn = et % L * 2;
+    const bool ck0 = !END && ckc < cmax && ckn < p.N, ck1 = !END && ckc + 1 < cmax && ckn < p.N;
     const size_t nck = (p.T + kCk - 1) / kCk;
-    const float* pck = p.states + ((b * nck + tl / kCk) * p.D + c0 + et / L) * p.N + et % L * 4;
+    const float* pck = p.states + ((b * nck + tl / kCk) * p.D + ckc) * p.N + ckn;
+    int64_t out = tok0 * p.D + c;
+    // dB, dC: vectors of 4 of a token's [2][N], added over the warps
+    constexpr int SV = TB * L, SN = SV > NE ? SV / NE : 1;
+    const int sn = et % (L / 2) * 4, sm_ = et % L / (L / 2), si = et / L;
+    const bool son = et < SV && sn < p.N;
+    const int64_t srow = (int64_t)p.G * 2 * p.N;
+    float* pbc = p.bc + (((int64_t)ct * p.B + b) * p.T + tl + si) * srow + (int64_t)(g * 2 + sm_) * p.N + sn;
+
+    // Only tile 0 of the walk, the sequence's last, can have tokens behind the
+    // end.
     auto load = [&](int k) {
-      const int tt = t0 + (ntile - 1 - k) * TB;
 #pragma unroll
       for (int s = 0; s < PASS; ++s) {
-        const int i = i0 + s * IS, t = tt + i;
-        const int n = i < TB && t < te ? nc : 0;
+        const int i = i0 + s * IS;
+        const int n = i < TB && (k > 0 || tl + i < te) ? nc : 0;
         nx[s].dt.load(pdt + s * IS * p.rdt.ld, n, p.vec);
-        nx[s].dy.load(pdy + s * IS * rdy.ld, n, p.vec);
+        nx[s].dy.load(pdy + (int64_t)s * IS * p.D, n, p.vec);
         if (p.z) nx[s].z.load(pz + s * IS * p.rz.ld, n, p.vec);
         if (!END) nx[s].u.load(pu + s * IS * p.ru.ld, n, p.vec);
       }
       pdt -= TB * p.rdt.ld;
-      pdy -= TB * rdy.ld;
+      pdy -= (int64_t)TB * p.D;
       pz -= TB * p.rz.ld;
       pu -= TB * p.ru.ld;
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
-        const int n = tt + (et + j * NE) / L < te ? nbn[j] : 0;
+        const int n = k > 0 || tl + (et + j * NE) / (L / 2) < te ? nbn[j] : 0;
         ncv[j].load(pc[j], n, p.vecbc);
         if (!END) nb[j].load(pb[j], n, p.vecbc);
         pc[j] -= TB * p.rc.ld;
         pb[j] -= TB * p.rb.ld;
       }
-      if (ck_on) ck = __ldg(reinterpret_cast<const float4*>(pck));
-      pck -= (size_t)p.D * p.N;
+      if (!END) load_state(pck, p.N, ck0, ck1, ck);
+      pck -= (int64_t)p.D * p.N;
     };
     auto prepare = [&](int k, Tok (&tok)[PASS]) {
-      const int tt = t0 + (ntile - 1 - k) * TB;
-      if (!END) sm.ck[k & 1][et] = ck;
+      if (!END) sm.ck[k & 1][et] = make_ulonglong2(ck[0], ck[1]);
 #pragma unroll
       for (int s = 0; s < PASS; ++s) {
         const int i = i0 + s * IS;
         if (i >= TB) continue;
-        const bool live = tt + i < te;
-        // behind the sequence's end the loads left zeros: e = u = 0, and delta is
-        // made 0 (a channel that is not there only needs e = u = 0)
+        const bool live = k > 0 || tl + i < te;
         Tok& x = tok[s];
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
           x.delta[e] = nx[s].dt.get(e) + bias[e];
-          x.sg[e] = 1.f;
           x.e[e] = nx[s].dy.get(e);
-          x.dzf[e] = 0.f;
           x.u[e] = END ? 0.f : nx[s].u.get(e);
         }
         if (p.softplus) {
 #pragma unroll
-          for (int e = 0; e < EV; ++e) {
-            float y;
-            const float pre = x.delta[e];
-            x.delta[e] = softplus_parts(pre, y);
-            x.sg[e] = rcp(1.f + y) * (pre >= 0.f ? 1.f : y);
-          }
+          for (int e = 0; e < EV; ++e) x.delta[e] = softplus(x.delta[e], x.sg[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) x.sg[e] = 1.f;
         }
         if (p.z) {
 #pragma unroll
@@ -289,60 +345,67 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
             x.e[e] *= zs;
           }
         }
+        // behind the sequence's end e = u = 0, and delta is made 0 (a channel
+        // that is not there only needs e = u = 0)
 #pragma unroll
         for (int e = 0; e < EV; ++e) x.delta[e] = live ? x.delta[e] : 0.f;
 #pragma unroll
         for (int e = 0; e < EV; e += 2) {
-          *reinterpret_cast<float4*>(&sm.q[k & 1][i * S::DS + cl + e]) =
-              make_float4(x.delta[e], x.delta[e] * x.u[e], x.delta[e + 1], x.delta[e + 1] * x.u[e + 1]);
-          *reinterpret_cast<float2*>(&sm.qe[k & 1][i * S::DS + cl + e]) = make_float2(x.e[e], x.e[e + 1]);
+          const int at = i * G::DS + (cl + e) / 2;
+          sm.q[k & 1][at] = make_float4(x.delta[e], x.delta[e + 1], x.delta[e] * x.u[e], x.delta[e + 1] * x.u[e + 1]);
+          sm.qe[k & 1][at] = make_float2(x.e[e], x.e[e + 1]);
         }
       }
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
         const int v = et + j * NE;
-        if (v < TB * L) {
+        if (v < BV) {
           ncv[j].put(&sm.cf[k & 1][v * 4]);
           if (!END) nb[j].put(&sm.bf[k & 1][v * 4]);
         }
       }
     };
     auto finish = [&](int k, const Tok (&tok)[PASS]) {
-      const int tt = t0 + (ntile - 1 - k) * TB, w = k & 1;
+      const int w = k & 1;
 #pragma unroll
       for (int s = 0; s < PASS; ++s) {
-        const int i = i0 + s * IS, t = tt + i;
-        if (i >= TB || t >= te) continue;
+        const int i = i0 + s * IS;
+        if (i >= TB || !(k > 0 || tl + i < te)) continue;
         float du[EV], dd[EV], dz[EV], gB[EV], gA[EV], yc[EV];
         load_f<EV>(&sm.gB[w][i * YS + cl], gB);
         load_f<EV>(&sm.gA[w][i * YS + cl], gA);
-        if (p.dz) load_f<EV>(&sm.yc[w][i * YS + cl], yc);
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
           du[e] = fmaf(tok[s].delta[e], gB[e], Ds[e] * tok[s].e[e]);
           dd[e] = fmaf(tok[s].u[e], gB[e], kLn2 * gA[e]) * tok[s].sg[e];
           sD[e] = fmaf(tok[s].e[e], tok[s].u[e], sD[e]);
           sT[e] += dd[e];
-          if (p.dz) dz[e] = tok[s].dzf[e] * fmaf(Ds[e], tok[s].u[e], yc[e]);
         }
-        const size_t at = ((size_t)b * p.T + t) * p.D + c;
+        const int64_t at = out + (int64_t)s * IS * p.D;
         store_n<IO, EV>((IO*)p.du + at, du, nc, p.vec);
         store_n<IO, EV>((IO*)p.ddt + at, dd, nc, p.vec);
-        if (p.dz) store_n<IO, EV>((IO*)p.dz + at, dz, nc, p.vec);
+        if (p.dz) {
+          load_f<EV>(&sm.yc[w][i * YS + cl], yc);
+#pragma unroll
+          for (int e = 0; e < EV; ++e) dz[e] = tok[s].dzf[e] * fmaf(Ds[e], tok[s].u[e], yc[e]);
+          store_n<IO, EV>((IO*)p.dz + at, dz, nc, p.vec);
+        }
       }
-      for (int v = et; v < TB * 2 * L; v += NE) {
-        const int i = v / (2 * L), n = v % L * 4, m = v % (2 * L) / L;
-        if (tt + i < te && n < p.N) {
+      out -= (int64_t)TB * p.D;
+#pragma unroll
+      for (int j = 0; j < SN; ++j) {
+        const int i = si + j * (NE / L);
+        if (son && (k > 0 || tl + i < te)) {
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int x = 0; x < kWarps; ++x) {
-            const float4 r = *reinterpret_cast<const float4*>(&sm.red[w][x][i][m * NP + n]);
+            const float4 r = *reinterpret_cast<const float4*>(&sm.red[w][x][i][sm_ * NP + sn]);
             s.x += r.x; s.y += r.y; s.z += r.z; s.w += r.w;
           }
-          *reinterpret_cast<float4*>(
-              &p.bc[(((((size_t)ct * p.B + b) * p.T + tt + i) * p.G + g) * 2 + m) * p.N + n]) = s;
+          *reinterpret_cast<float4*>(pbc + j * (NE / L) * srow) = s;
         }
       }
+      pbc -= TB * srow;
     };
     if (!END) {
       // behind the sequence's end: zeros
@@ -357,21 +420,27 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
     }
     if (ntile > 0) {
       load(0);
-      prepare(0, cur);
+      prepare(0, tok[0]);
       if (ntile > 1) load(1);
     }
     __syncthreads();
-    for (int k = 0; k < ntile; ++k) {
-      // outputs of tile k - 1 first: its registers then take tile k + 1
-      if (!END && k > 0) finish(k - 1, last);
-#pragma unroll
-      for (int s = 0; s < PASS; ++s) last[s] = cur[s];
-      if (k + 1 < ntile) prepare(k + 1, cur);
+    // tile k - 1's outputs first: its registers then take tile k + 1
+    auto step = [&](int k, Tok (&x)[PASS]) {
+      if constexpr (!END)
+        if (k > 0) finish(k - 1, x);
+      if (k + 1 < ntile) prepare(k + 1, x);
       if (k + 2 < ntile) load(k + 2);
       __syncthreads();
+    };
+    for (int k = 0; k < ntile; k += 2) {
+      step(k, tok[1]);
+      if (k + 1 < ntile) step(k + 1, tok[0]);
     }
     if constexpr (!END) {
-      if (ntile > 0) finish(ntile - 1, last);
+      if (ntile > 0) {
+        if (ntile & 1) finish(ntile - 1, tok[0]);
+        else finish(ntile - 1, tok[1]);
+      }
       // sums of e u and ddt over the block's token rows, in order
       float* s1 = &sm.red[0][0][0][0];
       float* s2 = &sm.gB[0][0];
@@ -399,48 +468,42 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
 
   // ---- scan warps
   const int lane = tid % 32, warp = tid / 32;
-  const int cl = tid / L, l = tid % L, c = c0 + cl;
-  const int n0 = 4 * l;
-  const bool on = c < cmax && n0 < p.N;
+  const int cl = tid / L * 2, l = tid % L, c = c0 + cl;  // this thread's first channel and its lane
+  const int n0 = 2 * l;
+  const bool on0 = c < cmax && n0 < p.N, on1 = c + 1 < cmax && n0 < p.N;
   const size_t sidx = ((size_t)b * p.D + c) * p.N + n0;
   const size_t sstep = (size_t)p.B * p.D * p.N;
-  f2 A2[2] = {0, 0}, gr[2] = {0, 0}, dA[2] = {0, 0}, dAt[2] = {0, 0};
-  if (on) {
-    const float4 a = *reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0);
-    A2[0] = pk(a.x * kLog2e, a.y * kLog2e);
-    A2[1] = pk(a.z * kLog2e, a.w * kLog2e);
-    if (!END) {
-      if (p.dhT) {
-        const float4 x = *reinterpret_cast<const float4*>(p.dhT + sidx);
-        gr[0] = pk(x.x, x.y);
-        gr[1] = pk(x.z, x.w);
-      }
-      for (int s = p.nseg - 1; s > seg; --s) {
-        const float4 x = *reinterpret_cast<const float4*>(p.segE + s * sstep + sidx);
-        const float d = p.segD[((size_t)s * p.B + b) * p.D + c];
-        gr[0] = fma2(ex2v(mul2(A2[0], pk(d, d))), gr[0], pk(x.x, x.y));
-        gr[1] = fma2(ex2v(mul2(A2[1], pk(d, d))), gr[1], pk(x.z, x.w));
-      }
+  f2 A2[2], gr[2] = {0, 0}, dA[2] = {0, 0}, dAt[2] = {0, 0}, sumd = 0;
+  load_state(p.A + (size_t)c * p.N + n0, p.N, on0, on1, A2);
+  A2[0] = mul2(A2[0], pk(kLog2e, kLog2e));
+  A2[1] = mul2(A2[1], pk(kLog2e, kLog2e));
+  if (!END) {
+    if (p.dhT) load_state(p.dhT + sidx, p.N, on0, on1, gr);
+    for (int s = p.nseg - 1; s > seg; --s) {
+      f2 x[2];
+      load_state(p.segE + s * sstep + sidx, p.N, on0, on1, x);
+      const float* sd = p.segD + ((size_t)s * p.B + b) * p.D + c;
+      const f2 d = pk(on0 ? sd[0] : 0.f, on1 ? sd[1] : 0.f);
+      gr[0] = fma2(ex2v(mul2(A2[0], d)), gr[0], x[0]);
+      gr[1] = fma2(ex2v(mul2(A2[1], d)), gr[1], x[1]);
     }
   }
-  float sumd = 0.f;
   __syncthreads();
   for (int k = 0; k < ntile; ++k) {
     const int w = k & 1;
-    const float2* q = sm.q[w] + cl;
-    const float* qe = sm.qe[w] + cl;
+    const float4* q = sm.q[w] + cl / 2;
+    const float2* qe = sm.qe[w] + cl / 2;
     const IO* bf = sm.bf[w] + n0;
     const IO* cf = sm.cf[w] + n0;
     if constexpr (END) {
-#pragma unroll 4
+#pragma unroll
       for (int i = TB - 1; i >= 0; --i) {
-        const float d = q[i * S::DS].x, e = qe[i * S::DS];
-        const f2 d2 = pk(d, d), e2 = pk(e, e);
+        const f2 d = *reinterpret_cast<const f2*>(&q[i * G::DS]), e = *reinterpret_cast<const f2*>(&qe[i * G::DS]);
         f2 C0, C1;
         load_bc(cf + i * NP, C0, C1);
-        gr[0] = mul2(fma2(e2, C0, gr[0]), ex2v(mul2(A2[0], d2)));
-        gr[1] = mul2(fma2(e2, C1, gr[1]), ex2v(mul2(A2[1], d2)));
-        sumd += d;
+        gr[0] = mul2(fma2(e, C0, gr[0]), ex2v(mul2(A2[0], d)));
+        gr[1] = mul2(fma2(e, C1, gr[1]), ex2v(mul2(A2[1], d)));
+        sumd = add2(sumd, d);
       }
     } else {
       walk_tile<IO, L>(p.dz != nullptr, sm.ck[w][tid], q, qe, bf, cf, sm.gB[w] + cl, sm.gA[w] + cl, sm.yc[w] + cl,
@@ -457,18 +520,17 @@ __global__ void __launch_bounds__(NT, L >= 4 ? 2 : 1) scan_bwd_kernel(ScanParams
     }
     __syncthreads();
   }
-  const float4 gv = make_float4(lo(gr[0]), hi(gr[0]), lo(gr[1]), hi(gr[1]));
   if (END) {
-    if (on) *reinterpret_cast<float4*>(p.segE + seg * sstep + sidx) = gv;
-    if (c < cmax && l == 0) p.segD[((size_t)seg * p.B + b) * p.D + c] = sumd;
+    store_state(p.segE + seg * sstep + sidx, p.N, on0, on1, gr);
+    float* sd = p.segD + ((size_t)seg * p.B + b) * p.D + c;
+    if (l == 0 && on0) sd[0] = lo(sumd);
+    if (l == 0 && on1) sd[1] = hi(sumd);
     return;
   }
   dA[0] = add2(dA[0], dAt[0]);
   dA[1] = add2(dA[1], dAt[1]);
-  if (p.dh0 && on && seg == 0) *reinterpret_cast<float4*>(p.dh0 + sidx) = gv;
-  if (on)
-    *reinterpret_cast<float4*>(part + (size_t)c * p.N + n0) =
-        make_float4(lo(dA[0]), hi(dA[0]), lo(dA[1]), hi(dA[1]));
+  if (p.dh0 && seg == 0) store_state(p.dh0 + sidx, p.N, on0, on1, gr);
+  store_state(part + (size_t)c * p.N + n0, p.N, on0, on1, dA);
 }
 
 // dB, dC of a token: the channel tiles' shares added in order.  One thread per
@@ -523,17 +585,17 @@ cudaError_t go(const ScanParams& p, cudaStream_t s) {
 }  // namespace
 }  // namespace scan
 
-cudaError_t launch_scan_bwd(const scan::ScanParams& p0, int L, bool bf, cudaStream_t s) {
+cudaError_t launch_scan_bwd(const scan::ScanParams& p0, bool bf, cudaStream_t s) {
   scan::ScanParams p = p0;
   // gradients are contiguous: vectors of 4 need whole rows of them
   const size_t es = bf ? 2 : 4;
   p.vec = p.vec && rows_vec(p.dy, Rows{p.D, 0}, (int)(16 / es), es);
-  switch (L) {
-    case 1: return bf ? scan::go<bf16, 1>(p, s) : scan::go<float, 1>(p, s);
+  switch (scan::states_of(p.N) / 2) {
     case 2: return bf ? scan::go<bf16, 2>(p, s) : scan::go<float, 2>(p, s);
     case 4: return bf ? scan::go<bf16, 4>(p, s) : scan::go<float, 4>(p, s);
     case 8: return bf ? scan::go<bf16, 8>(p, s) : scan::go<float, 8>(p, s);
     case 16: return bf ? scan::go<bf16, 16>(p, s) : scan::go<float, 16>(p, s);
+    case 32: return bf ? scan::go<bf16, 32>(p, s) : scan::go<float, 32>(p, s);
   }
   return cudaErrorInvalidValue;
 }

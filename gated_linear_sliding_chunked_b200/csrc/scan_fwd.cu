@@ -5,6 +5,33 @@ namespace lz {
 namespace scan {
 namespace {
 
+// L: lanes of a channel, 4 states a lane
+template <int L>
+struct Geo {
+  static constexpr int CH = NS / L;         // channels of a block
+  static constexpr int NP = 4 * L;          // states, padded
+  static constexpr int U = L < 4 ? L : 4;   // tokens whose lane sums are formed together
+  static constexpr int PAD = 32 / L < 4 ? 4 : 32 / L;
+  static constexpr int YS = CH + PAD;       // row of a [tokens][channels] fp32 tile
+};
+
+// 4 elements of B or C as the scan warps read them from shared memory, as pairs
+// of floats.  They stay in the I/O type there: what a warp's shared memory
+// loads return to registers, 128 bytes a cycle and SM however many lanes read
+// the same words, is what the scan runs out of first.
+template <typename IO>
+__device__ __forceinline__ void load_bc(const IO* p, f2& x, f2& y) {
+  if constexpr (sizeof(IO) == 4) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    x = v.x;
+    y = v.y;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    x = pk(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    y = pk(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  }
+}
+
 // Tile: 8 elements of (token, channel) for each elementwise thread, as long as
 // that is at most 32 tokens.
 template <int L>
@@ -369,13 +396,15 @@ cudaError_t go_step(const ScanParams& p, float* state, cudaStream_t s) {
   }                                                          \
   return cudaErrorInvalidValue;
 
-cudaError_t launch_scan_fwd(const scan::ScanParams& p, int L, bool bf, cudaStream_t s) {
+cudaError_t launch_scan_fwd(const scan::ScanParams& p, bool bf, cudaStream_t s) {
+  const int L = scan::states_of(p.N) / 4;
 #define LZ_CALL(IO, LL) scan::go<IO, LL>(p, s)
   LZ_LANES(LZ_CALL)
 #undef LZ_CALL
 }
 
-static cudaError_t launch_scan_step(const scan::ScanParams& p, float* state, int L, bool bf, cudaStream_t s) {
+static cudaError_t launch_scan_step(const scan::ScanParams& p, float* state, bool bf, cudaStream_t s) {
+  const int L = scan::states_of(p.N) / 4;
 #define LZ_CALL(IO, LL) scan::go_step<IO, LL>(p, state, s)
   LZ_LANES(LZ_CALL)
 #undef LZ_CALL
@@ -413,7 +442,7 @@ lz_status check_scan(const char* fn, const lz_scan_dims* d) {
 // on; kFull blocks are taken as a full device.
 constexpr int kFull = 148;
 void plan(const lz_scan_dims* d, int* nct, int* seg, int* nseg) {
-  const int L = scan::lanes_of(d->N), CH = scan::NS / L;
+  const int CH = scan::NS * 4 / scan::states_of(d->N);
   const int per = d->D / d->G;
   *nct = (per + CH - 1) / CH;
   const int64_t base = (int64_t)*nct * d->G * d->B;
@@ -507,7 +536,7 @@ extern "C" lz_status lz_scan_fwd(const lz_scan_dims* d, const void* u, const voi
   p.h0 = h0; p.lens = lens; p.y = y; p.hT = hT; p.states = states;
   p.segE = (float*)((char*)ws + w.segE);
   p.segD = (float*)((char*)ws + w.segD);
-  return layer_done(launch_scan_fwd(p, scan::lanes_of(d->N), d->io == LZ_BF16, (cudaStream_t)stream), fn);
+  return layer_done(launch_scan_fwd(p, d->io == LZ_BF16, (cudaStream_t)stream), fn);
 }
 
 extern "C" lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const void* dt, const float* A,
@@ -537,7 +566,6 @@ extern "C" lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const voi
   if (ws_bytes < w.total)
     return layer_fail(LZ_ERR_INVALID_ARG, "%s: workspace too small (%zu bytes, need %zu)", fn, ws_bytes, w.total);
   ScanParams p = params_of(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias);
-  const int L = scan::lanes_of(d->N);
   const bool bf = d->io == LZ_BF16;
   cudaStream_t s = (cudaStream_t)stream;
   p.h0 = h0; p.lens = lens;
@@ -547,12 +575,12 @@ extern "C" lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const voi
   p.states = const_cast<float*>(states);
   if (!states && data) {
     p.states = (float*)((char*)ws + w.states);
-    e = launch_scan_fwd(p, L, bf, s);
+    e = launch_scan_fwd(p, bf, s);
   }
   p.dy = dy; p.dhT = dhT; p.du = du; p.ddt = ddt; p.dz = dz; p.dh0 = dh0; p.dB = dB; p.dC = dC;
   p.part = (float*)((char*)ws + w.part);
   p.bc = (float*)((char*)ws + w.bc);
-  if (e == cudaSuccess && d->B > 0) e = launch_scan_bwd(p, L, bf, s);
+  if (e == cudaSuccess && d->B > 0) e = launch_scan_bwd(p, bf, s);
   if (e == cudaSuccess)
     e = launch_sum_rows({p.part, d->B * p.nseg, scan::part_ld(d->D, d->N), dA, (size_t)d->D * d->N, dDskip,
                          (size_t)d->D, ddt_bias, (size_t)d->D},
@@ -577,6 +605,5 @@ extern "C" lz_status lz_scan_step(const lz_scan_dims* d, float* state, const voi
   one.T = 1;
   ScanParams p = params_of(&one, u, dt, A, Bm, Cm, Dskip, z, dt_bias);
   p.y = y;
-  return layer_done(
-      launch_scan_step(p, state, scan::lanes_of(d->N), d->io == LZ_BF16, (cudaStream_t)stream), fn);
+  return layer_done(launch_scan_step(p, state, d->io == LZ_BF16, (cudaStream_t)stream), fn);
 }
