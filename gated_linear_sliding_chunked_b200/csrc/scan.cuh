@@ -2,10 +2,9 @@
 //
 // Layout of the work: a channel's states lie across lanes of a warp, 4 states of
 // a channel to a thread in the forward, 2 neighbouring states of 2 neighbouring
-// channels in the backward; the four scan warps of a block hold NS * 4 / N
-// channels (N rounded up to a power of two) of one sequence.  The tokens are
-// walked in tiles.  Four more warps do what is elementwise in (token,
-// channel): while the scan warps walk a tile, they finish the outputs of the
+// channels in the backward; the W scan warps of a block hold 128 W / N channels
+// (N rounded up to a power of two) of one sequence.  The tokens are walked in
+// tiles.  W more warps do what is elementwise in (token, channel): while the scan warps walk a tile, they finish the outputs of the
 // tile before and prepare the steps (softplus), inputs and gates of the tile
 // behind, whose global loads they issued a tile earlier.  One block-wide
 // barrier a tile hands the shared memory buffers over.  Without the split the
@@ -22,15 +21,13 @@
 namespace lz {
 namespace scan {
 
-constexpr int NS = 128;      // scan threads of a block
-constexpr int NE = 128;      // elementwise threads
-constexpr int NT = NS + NE;
 constexpr int kCk = 16;      // tokens between two saved states
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct ScanParams {
   int B, T, D, G, N, softplus;
+  int W;         // scan warps of a block (4 or 7), and elementwise warps
   int nct;       // channel tiles of a group
   int seg, nseg; // tokens of a segment, segments
   bool vec, vecbc;  // rows of 16-byte vectors: u, dt, z, dy and outputs; of 4 elements: B, C
@@ -245,6 +242,9 @@ __device__ __forceinline__ void reduce_scatter(float (&v)[SZ], int lane, int& ba
     }
   }
 }
+
+// Row of a [tokens][CH] fp32 tile: CH or a little more, of which x is left over 32 banks
+constexpr int row_of(int CH, int x) { return CH + (x - CH % 32 + 32) % 32; }
 
 // Floats from one partial row of the parameter gradients to the next: rows
 // are written in vectors of 4

@@ -25,13 +25,13 @@ namespace {
 // sums against 14, and moves to repeat each step and input in a pair of
 // registers: 1745 us against 1677 us at 2 x 8192 tokens, 4096 channels, 16
 // states.)  L: lanes of a channel pair.
-template <int L>
+template <int L, int W>
 struct Geo {
+  static constexpr int NS = 32 * W, NE = 32 * W;  // scan threads, elementwise threads
   static constexpr int CH = 2 * NS / L;     // channels of a block
   static constexpr int NP = 2 * L;          // states, padded
   static constexpr int U = L < 8 ? L / 2 : 4;  // tokens whose lane sums are formed together
-  // a [tokens][channels] fp32 tile: rows off the banks of the rows written with them
-  static constexpr int YS = CH + (L == 4 ? 16 : L == 8 ? 8 : 4);
+  static constexpr int YS = row_of(CH, L == 4 ? 16 : L == 8 ? 8 : 4);
   static constexpr int DS = CH / 2 + 1;     // row of a [tokens][channel pairs] tile of 4 words
 };
 
@@ -70,17 +70,17 @@ __device__ __forceinline__ void store_state(float* p, int N, bool on0, bool on1,
 }
 
 constexpr int TB = kCk;  // tokens of a tile
-constexpr int kWarps = NS / 32;
 
-template <typename IO, int L>
+template <typename IO, int L, int W>
 struct alignas(16) Smem {
-  static constexpr int NP = Geo<L>::NP;
-  float4 q[2][TB * Geo<L>::DS];       // of a channel pair: delta, delta; delta u, delta u
-  float2 qe[2][TB * Geo<L>::DS];      // e, e
+  using G = Geo<L, W>;
+  static constexpr int NP = G::NP;
+  float4 q[2][TB * G::DS];       // of a channel pair: delta, delta; delta u, delta u
+  float2 qe[2][TB * G::DS];      // e, e
   IO bf[2][TB * NP], cf[2][TB * NP];
-  float gB[2][TB * Geo<L>::YS], gA[2][TB * Geo<L>::YS], yc[2][TB * Geo<L>::YS];
-  float red[2][kWarps][TB][2 * NP];  // dB, dC over a warp's channels
-  ulonglong2 ck[2][NS];  // the state before the tile, as the scan threads hold it
+  float gB[2][TB * G::YS], gA[2][TB * G::YS], yc[2][TB * G::YS];
+  float red[2][W][TB][2 * NP];  // dB, dC over a warp's channels
+  ulonglong2 ck[2][G::NS];  // the state before the tile, as the scan threads hold it
 };
 
 // The scan warps' walk over one tile, forward and back.  Sums over lanes take
@@ -88,11 +88,11 @@ struct alignas(16) Smem {
 // value while the loads behind it wait for the store; so a token's operands
 // are loaded, and the next token's arithmetic done, before its sums over the
 // channels are formed and stored.
-template <typename IO, int L>
+template <typename IO, int L, int W>
 __device__ __forceinline__ void walk_tile(bool want_y, const ulonglong2 h0, const float4* q, const float2* qe,
                                           const IO* bf, const IO* cf, float* gB, float* gA, float* yc, float* red,
                                           f2 (&A2)[2], f2 (&gr)[2], f2 (&dA)[2], int lane, int l) {
-  using G = Geo<L>;
+  using G = Geo<L, W>;
   constexpr int NP = G::NP, U = G::U, YS = G::YS, DS = G::DS;
   // ---- forward: the state after every token, h[i + 1]
   f2 h[TB + 1][2];
@@ -214,16 +214,17 @@ __device__ __forceinline__ void walk_tile(bool want_y, const ulonglong2 h0, cons
 
 // END: only the gradient that the segment hands to the one before it when
 // none comes from behind (the state gradient before its first token).
-template <typename IO, int L, bool END>
-__global__ void __launch_bounds__(NT, L >= 8 ? 2 : 1) scan_bwd_kernel(ScanParams p) {
-  using G = Geo<L>;
+template <typename IO, int L, int W, bool END>
+__global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_kernel(ScanParams p) {
+  using G = Geo<L, W>;
   constexpr int CH = G::CH, NP = G::NP, YS = G::YS;
+  constexpr int NS = G::NS, NE = G::NE;
   constexpr int EV = TB * CH / NE > 1 ? (TB * CH / NE < 8 ? TB * CH / NE : 8) : 2;  // channels of an elementwise thread
   constexpr int ROWT = CH / EV;                                 // threads of a token
   constexpr int PASS = (TB * ROWT + NE - 1) / NE;               // tokens of a thread
-  constexpr int BV = TB * NP / 4, BN = BV > NE ? BV / NE : 1;   // 4-element vectors of B and of C, a thread's
+  constexpr int BV = TB * NP / 4, BN = (BV + NE - 1) / NE;   // 4-element vectors of B and of C, a thread's
   extern __shared__ __align__(16) char raw[];
-  using S = Smem<IO, L>;
+  using S = Smem<IO, L, W>;
   S& sm = *reinterpret_cast<S*>(raw);
   const int tid = threadIdx.x;
   const int g = blockIdx.x / p.nct, ct = blockIdx.x % p.nct;
@@ -283,9 +284,8 @@ __global__ void __launch_bounds__(NT, L >= 8 ? 2 : 1) scan_bwd_kernel(ScanParams
     const float* pck = p.states + ((b * nck + tl / kCk) * p.D + ckc) * p.N + ckn;
     int64_t out = tok0 * p.D + c;
     // dB, dC: vectors of 4 of a token's [2][N], added over the warps
-    constexpr int SV = TB * L, SN = SV > NE ? SV / NE : 1;
+    constexpr int SV = TB * L, SN = (SV + NE - 1) / NE;
     const int sn = et % (L / 2) * 4, sm_ = et % L / (L / 2), si = et / L;
-    const bool son = et < SV && sn < p.N;
     const int64_t srow = (int64_t)p.G * 2 * p.N;
     float* pbc = p.bc + (((int64_t)ct * p.B + b) * p.T + tl + si) * srow + (int64_t)(g * 2 + sm_) * p.N + sn;
 
@@ -395,10 +395,10 @@ __global__ void __launch_bounds__(NT, L >= 8 ? 2 : 1) scan_bwd_kernel(ScanParams
 #pragma unroll
       for (int j = 0; j < SN; ++j) {
         const int i = si + j * (NE / L);
-        if (son && (k > 0 || tl + i < te)) {
+        if (et + j * NE < SV && sn < p.N && (k > 0 || tl + i < te)) {
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int x = 0; x < kWarps; ++x) {
+          for (int x = 0; x < W; ++x) {
             const float4 r = *reinterpret_cast<const float4*>(&sm.red[w][x][i][sm_ * NP + sn]);
             s.x += r.x; s.y += r.y; s.z += r.z; s.w += r.w;
           }
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(NT, L >= 8 ? 2 : 1) scan_bwd_kernel(ScanParams
       // sums of e u and ddt over the block's token rows, in order
       float* s1 = &sm.red[0][0][0][0];
       float* s2 = &sm.gB[0][0];
-      static_assert(IS * CH <= 2 * kWarps * TB * 2 * NP && IS * CH <= 2 * TB * YS, "room for the sums");
+      static_assert(IS * CH <= 2 * W * TB * 2 * NP && IS * CH <= 2 * TB * YS, "room for the sums");
       asm volatile("bar.sync 1, %0;" ::"n"(NE) : "memory");
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(NT, L >= 8 ? 2 : 1) scan_bwd_kernel(ScanParams
         sumd = add2(sumd, d);
       }
     } else {
-      walk_tile<IO, L>(p.dz != nullptr, sm.ck[w][tid], q, qe, bf, cf, sm.gB[w] + cl, sm.gA[w] + cl, sm.yc[w] + cl,
+      walk_tile<IO, L, W>(p.dz != nullptr, sm.ck[w][tid], q, qe, bf, cf, sm.gB[w] + cl, sm.gA[w] + cl, sm.yc[w] + cl,
                        &sm.red[w][warp][0][0] + n0, A2, gr, dAt, lane, l);
       // dA over 16 tiles at a time: thousands of tokens added to one sum would
       // cost it bits
@@ -554,25 +554,25 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(ScanParams p) {
   out[((size_t)b * p.T * p.G + tg) * p.N + n] = from_f<IO>(s);
 }
 
-template <typename IO, int L>
+template <typename IO, int L, int W>
 cudaError_t go(const ScanParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(Smem<IO, L>);
+  const size_t smem = sizeof(Smem<IO, L, W>);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, W, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   if (p.nseg > 1) {
     ScopedTiming tm("scan_bwd_ends", s);
-    scan_bwd_kernel<IO, L, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), NT, smem, s>>>(p);
+    scan_bwd_kernel<IO, L, W, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), 64 * W, smem, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   {
     ScopedTiming tm("scan_bwd", s);
-    scan_bwd_kernel<IO, L, false><<<dim3(p.G * p.nct, p.B, p.nseg), NT, smem, s>>>(p);
+    scan_bwd_kernel<IO, L, W, false><<<dim3(p.G * p.nct, p.B, p.nseg), 64 * W, smem, s>>>(p);
   }
   e = cudaGetLastError();
   const size_t n = (size_t)p.B * p.T * p.G * 2 * p.N;
@@ -580,6 +580,18 @@ cudaError_t go(const ScanParams& p, cudaStream_t s) {
   ScopedTiming tm("scan_bc_sum", s);
   scan_bc_kernel<IO><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+template <typename IO>
+cudaError_t go_any(const ScanParams& p, cudaStream_t s) {
+  switch (states_of(p.N)) {
+    case 4: return go<IO, 2, 4>(p, s);
+    case 8: return go<IO, 4, 4>(p, s);
+    case 16: return p.W == 7 ? go<IO, 8, 7>(p, s) : go<IO, 8, 4>(p, s);
+    case 32: return p.W == 7 ? go<IO, 16, 7>(p, s) : go<IO, 16, 4>(p, s);
+    case 64: return p.W == 7 ? go<IO, 32, 7>(p, s) : go<IO, 32, 4>(p, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -590,14 +602,7 @@ cudaError_t launch_scan_bwd(const scan::ScanParams& p0, bool bf, cudaStream_t s)
   // gradients are contiguous: vectors of 4 need whole rows of them
   const size_t es = bf ? 2 : 4;
   p.vec = p.vec && rows_vec(p.dy, Rows{p.D, 0}, (int)(16 / es), es);
-  switch (scan::states_of(p.N) / 2) {
-    case 2: return bf ? scan::go<bf16, 2>(p, s) : scan::go<float, 2>(p, s);
-    case 4: return bf ? scan::go<bf16, 4>(p, s) : scan::go<float, 4>(p, s);
-    case 8: return bf ? scan::go<bf16, 8>(p, s) : scan::go<float, 8>(p, s);
-    case 16: return bf ? scan::go<bf16, 16>(p, s) : scan::go<float, 16>(p, s);
-    case 32: return bf ? scan::go<bf16, 32>(p, s) : scan::go<float, 32>(p, s);
-  }
-  return cudaErrorInvalidValue;
+  return bf ? scan::go_any<bf16>(p, s) : scan::go_any<float>(p, s);
 }
 
 }  // namespace lz

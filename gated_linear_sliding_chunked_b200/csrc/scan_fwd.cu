@@ -5,14 +5,14 @@ namespace lz {
 namespace scan {
 namespace {
 
-// L: lanes of a channel, 4 states a lane
-template <int L>
+// L: lanes of a channel, 4 states a lane; W: scan warps of a block
+template <int L, int W>
 struct Geo {
+  static constexpr int NS = 32 * W, NE = 32 * W;  // scan threads, elementwise threads
   static constexpr int CH = NS / L;         // channels of a block
   static constexpr int NP = 4 * L;          // states, padded
   static constexpr int U = L < 4 ? L : 4;   // tokens whose lane sums are formed together
-  static constexpr int PAD = 32 / L < 4 ? 4 : 32 / L;
-  static constexpr int YS = CH + PAD;       // row of a [tokens][channels] fp32 tile
+  static constexpr int YS = row_of(CH, L == 2 ? 16 : L == 4 ? 8 : 4);
 };
 
 // 4 elements of B or C as the scan warps read them from shared memory, as pairs
@@ -34,39 +34,41 @@ __device__ __forceinline__ void load_bc(const IO* p, f2& x, f2& y) {
 
 // Tile: 8 elements of (token, channel) for each elementwise thread, as long as
 // that is at most 32 tokens.
-template <int L>
+template <int L, int W>
 struct Tile {
-  static constexpr int CH = Geo<L>::CH, NP = Geo<L>::NP;
+  using G = Geo<L, W>;
   static constexpr int TT = L >= 4 ? 32 : 8 * L;
-  static constexpr int EV = TT * CH / NE;                    // elements of a thread: neighbours in a row
-  static constexpr int DS = CH + 2;                          // row of dd, off the banks of the row before
-  static constexpr int BN = TT * L > NE ? TT * L / NE : 1;   // its 4-element vectors of B and of C
+  static constexpr int EV = TT * G::CH / G::NE;              // elements of a thread: neighbours in a row
+  static constexpr int DS = G::CH + 2;                       // row of dd, off the banks of the row before
+  static constexpr int BV = TT * L;                          // 4-element vectors of B, and of C
+  static constexpr int BN = (BV + G::NE - 1) / G::NE;        // those of a thread
 };
 
-template <typename IO, int L>
+template <typename IO, int L, int W>
 struct alignas(16) Smem {
-  using X = Tile<L>;
+  using X = Tile<L, W>;
+  using G = Geo<L, W>;
   float2 dd[2][X::TT * X::DS];  // delta, delta * u
-  IO bf[2][X::TT * X::NP], cf[2][X::TT * X::NP];
-  float ys[2][X::TT * Geo<L>::YS];
+  IO bf[2][X::TT * G::NP], cf[2][X::TT * G::NP];
+  float ys[2][X::TT * G::YS];
 };
 
 // The scan warps' walk over one tile, U tokens at a time.  The decays and
 // inputs of the next U tokens are formed before the state passes through
 // these, and the whole tile is one run of instructions, so that the loads and
 // exponentials of the former fill the waits of the latter.
-template <typename IO, int L, bool END>
+template <typename IO, int L, int W, bool END>
 __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const IO* __restrict__ bf,
                                           const IO* __restrict__ cf, float* __restrict__ ys, const f2 (&A2)[2],
                                           f2 (&h)[2], float& sumd, int lane, int l, float* states, size_t ck_step,
                                           int ck_left) {
-  using G = Geo<L>;
-  constexpr int NP = G::NP, U = G::U, TT = Tile<L>::TT, NG = TT / U;
+  using G = Geo<L, W>;
+  constexpr int NP = G::NP, U = G::U, TT = Tile<L, W>::TT, NG = TT / U;
   f2 a[2][U][2], x[2][U][2];
   auto form = [&](int i, f2 (&a)[U][2], f2 (&x)[U][2]) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const float2 d = dd[(i + j) * Tile<L>::DS];
+      const float2 d = dd[(i + j) * Tile<L, W>::DS];
       f2 B0, B1;
       load_bc(bf + (i + j) * NP, B0, B1);
       const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
@@ -104,17 +106,18 @@ __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const I
   }
 }
 
-// One block: 128/L channels of one sequence over one segment of its tokens.
+// One block: 32 W / L channels of one sequence over one segment of its tokens.
 // END: only the segment's effect on the state (its end value from a zero
 // start and the sum of delta), which the blocks of the later segments fold
 // into the state they start from.
-template <typename IO, int L, bool END>
-__global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
-  using G = Geo<L>;
-  using X = Tile<L>;
+template <typename IO, int L, int W, bool END>
+__global__ void __launch_bounds__(64 * W, W > 4 ? 1 : 2) scan_fwd_kernel(ScanParams p) {
+  using G = Geo<L, W>;
+  using X = Tile<L, W>;
   constexpr int CH = G::CH, TT = X::TT, EV = X::EV, BN = X::BN, DS = X::DS;
+  constexpr int NS = G::NS, NE = G::NE;
   extern __shared__ __align__(16) char raw[];
-  using S = Smem<IO, L>;
+  using S = Smem<IO, L, W>;
   S& sm = *reinterpret_cast<S*>(raw);
   const int tid = threadIdx.x;
   const int g = blockIdx.x / p.nct, ct = blockIdx.x % p.nct;
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
     for (int j = 0; j < BN; ++j) {
       const int v = et + j * NE, n0 = v % L * 4;
       tb[j] = t0 + v / L;
-      nb[j] = v < TT * L ? p.N - n0 : 0;
+      nb[j] = v < X::BV ? p.N - n0 : 0;
       pb[j] = (const IO*)p.Bm + p.rb.at(b, tb[j]) + g * p.N + n0;
       pc[j] = (const IO*)p.Cm + p.rc.at(b, tb[j]) + g * p.N + n0;
     }
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
         const int v = et + j * NE;
-        if (v < TT * L) {
+        if (v < X::BV) {
           x.b[j].put(&sm.bf[k & 1][v * 4]);
           if (!END) x.c[j].put(&sm.cf[k & 1][v * 4]);
         }
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
     // (a tile of 8 tokens starts at a 16th one every other time)
     const int t = t0 + k * TT;
     const bool ck = p.states && on && t % kCk == 0;
-    scan_tile<IO, L, END>(dd, bf, cf, ys, A2, h, sumd, lane, l,
+    scan_tile<IO, L, W, END>(dd, bf, cf, ys, A2, h, sumd, lane, l,
                           p.states + (((size_t)b * ((p.T + kCk - 1) / kCk) + t / kCk) * p.D + c) * p.N + n0,
                           (size_t)p.D * p.N, ck ? te - t : 0);
     __syncthreads();
@@ -302,24 +305,36 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
   }
 }
 
-template <typename IO, int L>
+template <typename IO, int L, int W>
 cudaError_t go(const ScanParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(Smem<IO, L>);
+  const size_t smem = sizeof(Smem<IO, L, W>);
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, W, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   if (p.nseg > 1) {
     ScopedTiming tm("scan_fwd_ends", s);
-    scan_fwd_kernel<IO, L, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), NT, smem, s>>>(p);
+    scan_fwd_kernel<IO, L, W, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), 64 * W, smem, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   ScopedTiming tm("scan_fwd", s);
-  scan_fwd_kernel<IO, L, false><<<dim3(p.G * p.nct, p.B, p.nseg), NT, smem, s>>>(p);
+  scan_fwd_kernel<IO, L, W, false><<<dim3(p.G * p.nct, p.B, p.nseg), 64 * W, smem, s>>>(p);
   return cudaGetLastError();
+}
+
+template <typename IO>
+cudaError_t go_any(const ScanParams& p, cudaStream_t s) {
+  switch (states_of(p.N)) {
+    case 4: return go<IO, 1, 4>(p, s);
+    case 8: return go<IO, 2, 4>(p, s);
+    case 16: return p.W == 7 ? go<IO, 4, 7>(p, s) : go<IO, 4, 4>(p, s);
+    case 32: return p.W == 7 ? go<IO, 8, 7>(p, s) : go<IO, 8, 4>(p, s);
+    case 64: return p.W == 7 ? go<IO, 16, 7>(p, s) : go<IO, 16, 4>(p, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 // ---- single tokens --------------------------------------------------------
@@ -386,28 +401,20 @@ cudaError_t go_step(const ScanParams& p, float* state, cudaStream_t s) {
 }  // namespace
 }  // namespace scan
 
-#define LZ_LANES(CALL)                                       \
-  switch (L) {                                               \
-    case 1: return bf ? CALL(bf16, 1) : CALL(float, 1);      \
-    case 2: return bf ? CALL(bf16, 2) : CALL(float, 2);      \
-    case 4: return bf ? CALL(bf16, 4) : CALL(float, 4);      \
-    case 8: return bf ? CALL(bf16, 8) : CALL(float, 8);      \
-    case 16: return bf ? CALL(bf16, 16) : CALL(float, 16);   \
-  }                                                          \
-  return cudaErrorInvalidValue;
-
 cudaError_t launch_scan_fwd(const scan::ScanParams& p, bool bf, cudaStream_t s) {
-  const int L = scan::states_of(p.N) / 4;
-#define LZ_CALL(IO, LL) scan::go<IO, LL>(p, s)
-  LZ_LANES(LZ_CALL)
-#undef LZ_CALL
+  return bf ? scan::go_any<bf16>(p, s) : scan::go_any<float>(p, s);
 }
 
-static cudaError_t launch_scan_step(const scan::ScanParams& p, float* state, bool bf, cudaStream_t s) {
-  const int L = scan::states_of(p.N) / 4;
-#define LZ_CALL(IO, LL) scan::go_step<IO, LL>(p, state, s)
-  LZ_LANES(LZ_CALL)
-#undef LZ_CALL
+template <typename IO>
+static cudaError_t launch_scan_step(const scan::ScanParams& p, float* state, cudaStream_t s) {
+  switch (scan::states_of(p.N)) {
+    case 4: return scan::go_step<IO, 1>(p, state, s);
+    case 8: return scan::go_step<IO, 2>(p, state, s);
+    case 16: return scan::go_step<IO, 4>(p, state, s);
+    case 32: return scan::go_step<IO, 8>(p, state, s);
+    case 64: return scan::go_step<IO, 16>(p, state, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 // ---- host -----------------------------------------------------------------
@@ -436,22 +443,31 @@ lz_status check_scan(const char* fn, const lz_scan_dims* d) {
   return LZ_OK;
 }
 
-// Channel tiles, and the segments that a sequence is cut into when there are
-// too few channels and sequences to fill the device.  A segmented call runs
-// the recurrence twice (ends, then outputs), so it pays from three segments
-// on; kFull blocks are taken as a full device.
-constexpr int kFull = 148;
-void plan(const lz_scan_dims* d, int* nct, int* seg, int* nseg) {
-  const int CH = scan::NS * 4 / scan::states_of(d->N);
-  const int per = d->D / d->G;
-  *nct = (per + CH - 1) / CH;
-  const int64_t base = (int64_t)*nct * d->G * d->B;
+// Scan warps of a block, channel tiles, and the segments that a sequence is cut
+// into when there are too few channels and sequences to fill the device.
+//
+// Segments: a segmented call runs the recurrence twice (ends, then outputs), so
+// it pays from three segments on.  Warps: a block of 7 + 7 warps has an SM to
+// itself, blocks of 4 + 4 share one by twos; the kind is taken that leaves the
+// fewest scan warps on the busiest of kSMs SMs.  (At 2 sequences of 4096
+// channels with 16 states: 148 blocks of 7 against 256 of 4, two of which
+// meet on most SMs: 7 warps against 8.)
+constexpr int kSMs = 148;
+void plan(const lz_scan_dims* d, int* W, int* nct, int* seg, int* nseg) {
+  const int N = scan::states_of(d->N), per = d->D / d->G;
+  const int64_t gb = (int64_t)d->G * d->B;
+  auto tiles = [&](int w) { return (per + 128 * w / N - 1) / (128 * w / N); };
+  auto busiest = [&](int w) { return (tiles(w) * gb + kSMs - 1) / kSMs * w; };
+  const int64_t base = tiles(4) * gb;
   int n = 1;
-  if (base > 0 && base * 3 <= kFull * 2) n = (int)std::min<int64_t>(32, kFull * 4 / base);
+  if (base > 0 && base * 3 <= kSMs * 2) n = (int)std::min<int64_t>(32, kSMs * 4 / base);
+  *W = N >= 16 && n == 1 && busiest(7) < busiest(4) ? 7 : 4;
+  *nct = tiles(*W);
   int len = ((d->T + n - 1) / n + 31) / 32 * 32;
   len = std::max(len, 64);
-  *seg = len;
-  *nseg = std::max(1, (d->T + len - 1) / len);
+  // a sequence that is not cut is one segment, however short
+  *seg = n > 1 ? len : std::max(1, (d->T + 31) / 32 * 32);
+  *nseg = std::max(1, (d->T + *seg - 1) / *seg);
 }
 
 size_t state_bytes(const lz_scan_dims* d) {
@@ -462,8 +478,8 @@ struct Ws {
   size_t segE, segD, part, bc, states, total;
 };
 Ws ws_of(const lz_scan_dims* d, bool bwd) {
-  int nct, seg, nseg;
-  plan(d, &nct, &seg, &nseg);
+  int W, nct, seg, nseg;
+  plan(d, &W, &nct, &seg, &nseg);
   const size_t bd = (size_t)d->B * d->D;
   Ws w{};
   size_t o = 0;
@@ -483,7 +499,7 @@ ScanParams params_of(const lz_scan_dims* d, const void* u, const void* dt, const
                      const void* Cm, const float* Dskip, const void* z, const float* dtb) {
   ScanParams p{};
   p.B = d->B; p.T = d->T; p.D = d->D; p.G = d->G; p.N = d->N; p.softplus = d->softplus;
-  plan(d, &p.nct, &p.seg, &p.nseg);
+  plan(d, &p.W, &p.nct, &p.seg, &p.nseg);
   const int bcw = d->G * d->N;
   p.ru = rows_of(d->u, d->T, d->D);
   p.rdt = rows_of(d->dt, d->T, d->D);
@@ -605,5 +621,6 @@ extern "C" lz_status lz_scan_step(const lz_scan_dims* d, float* state, const voi
   one.T = 1;
   ScanParams p = params_of(&one, u, dt, A, Bm, Cm, Dskip, z, dt_bias);
   p.y = y;
-  return layer_done(launch_scan_step(p, state, d->io == LZ_BF16, (cudaStream_t)stream), fn);
+  cudaStream_t s = (cudaStream_t)stream;
+  return layer_done(d->io == LZ_BF16 ? launch_scan_step<bf16>(p, state, s) : launch_scan_step<float>(p, state, s), fn);
 }

@@ -87,6 +87,12 @@ CASES = [  # dtype, B, T, D, G, N, z, h0, skip, lens, strided, softplus
     (F, 1, 513, 132, 1, 4, True, True, True, [512], False, True),
     (F, 1, 2, 300, 2, 16, True, True, True, [-3], False, True),
     (F, 4, 33, 3000, 1, 16, True, True, True, [99, 33, 32, 31], False, True),
+    # as many channels as blocks of seven scan warps are taken for
+    (BF, 2, 35, 4096, 1, 16, True, True, True, [35, 18], False, True),
+    (F, 2, 17, 4090, 2, 16, True, False, True, None, False, True),
+    (BF, 2, 33, 2040, 1, 32, False, True, True, None, True, True),
+    (F, 2, 20, 1020, 2, 52, True, True, True, [20, 3], False, True),
+    (BF, 2, 18, 1024, 1, 64, True, False, True, None, False, True),
 ]
 
 
