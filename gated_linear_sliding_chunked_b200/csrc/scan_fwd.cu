@@ -79,6 +79,13 @@ __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const I
       if (END) sumd += d.x;
     }
   };
+  // C h of U tokens: summed over the lanes a step later
+  float yv[2][U];
+  auto sum_y = [&](int i, float (&v)[U]) {
+    int j = 0;
+    reduce_scatter<U, L / 2, 1>(v, lane, j);
+    if (l % (L / U) == 0) ys[(i + j) * G::YS] = v[0];
+  };
   form(0, a[0], x[0]);
 #pragma unroll
   for (int q = 0; q < NG; ++q) {
@@ -86,7 +93,6 @@ __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const I
     if (q + 1 < NG) form(i + U, a[(q + 1) & 1], x[(q + 1) & 1]);
     if (!END && i % kCk == 0 && i < ck_left)  // the state before every 16th token
       *reinterpret_cast<float4*>(states + i / kCk * ck_step) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
-    float yv[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       h[0] = fma2(a[q & 1][j][0], h[0], x[q & 1][j][0]);
@@ -95,15 +101,12 @@ __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const I
         f2 C0, C1;
         load_bc(cf + (i + j) * NP, C0, C1);
         const f2 y2 = fma2(h[1], C1, mul2(h[0], C0));
-        yv[j] = lo(y2) + hi(y2);
+        yv[q & 1][j] = lo(y2) + hi(y2);
       }
     }
-    if (!END) {
-      int j = 0;
-      reduce_scatter<U, L / 2, 1>(yv, lane, j);
-      if (l % (L / U) == 0) ys[(i + j) * G::YS] = yv[0];
-    }
+    if (!END && q > 0) sum_y(i - U, yv[(q + 1) & 1]);
   }
+  if (!END) sum_y(TT - U, yv[(NG - 1) & 1]);
 }
 
 // One block: 32 W / L channels of one sequence over one segment of its tokens.
