@@ -4,17 +4,18 @@
 // A row of D features stays in registers between its two norms: every input
 // is read once and every output written once, a few operations an element, so
 // HBM bandwidth bounds it (forward up to 5 values an element, backward up to
-// 8).  A thread holds 16 elements; up to 512 elements a row belongs to one
-// warp (no block-wide synchronisation), longer rows to a block.  Blocks walk
-// the rows with a stride, so that the backward's parameter gradients stay in
-// registers and leave as one partial per block.
+// 8).  A thread holds E = 16 (backward of up to 4096 features: 8) elements; up
+// to 512 elements a row belongs to one warp (no block-wide synchronisation),
+// longer rows to a block.  Blocks walk the rows with a stride: the next row's
+// loads are in flight while this one is worked on, and the backward's
+// parameter gradients stay in registers and leave as one partial per block.
 #include "layer.cuh"
 
 namespace lz {
 namespace {
 
-constexpr int E = 16;         // elements of a thread
-constexpr int kMaxD = 16384;  // 1024 threads
+constexpr int kMaxD = 16384;  // 16 elements a thread, 1024 threads
+constexpr int kWarpD = 512;   // rows of a warp: 16 elements a lane
 constexpr int kRowWarps = 4;  // rows of a block of one-warp rows
 
 // How the sums over a group of features are formed: the group is the whole
@@ -57,7 +58,7 @@ __device__ __forceinline__ float team_sum(float v, float* red) {
 }
 
 // Per-vector partial sums ps[k] -> the sum over each vector's group
-template <int VW, bool WARP, int MODE>
+template <int E, int VW, bool WARP, int MODE>
 __device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int lane, int team, float* red,
                                           float* sm) {
   constexpr int NV = E / VW;
@@ -107,7 +108,7 @@ __device__ __forceinline__ size_t o_at(const NormParams& p, const Rows& so, int 
   return (((size_t)b * p.G + g) * p.T + t) * dv + (c - g * dv);
 }
 
-template <typename IO, int VW, bool WARP, int MODE, int MAXT>
+template <typename IO, int E, int VW, bool WARP, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
   extern __shared__ float sm[];
   __shared__ float red[32];
@@ -117,36 +118,47 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
   const int nvec = p.D / VW;
   const int64_t row0 = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
   const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
-  for (int64_t row = row0; row < p.rows; row += step) {
-    const int b = (int)(row / p.T), t = (int)(row % p.T);
-    float x[E];
+  struct In {
+    Raw<IO, VW> o[NV], z[NV], r[NV];
+  };
+  auto fetch = [&](int64_t row, In& in) {
+    const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = k * team + lane;
-      if (v < nvec) {
-        load_vec<VW>((const IO*)p.o + o_at(p, p.so, b, t, v * VW), x + k * VW);
-      } else {
+      const int v = k * team + lane, c = v * VW;
+      const bool on = v < nvec;
+      in.o[k].load_if((const IO*)p.o + o_at(p, p.so, b, t, c), on);
+      if (p.z) in.z[k].load_if((const IO*)p.z + p.sz.at(b, t) + c, on);
+      if (p.r) in.r[k].load_if((const IO*)p.r + p.sr.at(b, t) + c, on);
+    }
+  };
+  In nx;
+  if (row0 < p.rows) fetch(row0, nx);
+  for (int64_t row = row0; row < p.rows; row += step) {
+    const In in = nx;
+    if (row + step < p.rows) fetch(row + step, nx);
+    float x[E], ps[NV];
 #pragma unroll
-        for (int e = 0; e < VW; ++e) x[k * VW + e] = 0.f;
+    for (int k = 0; k < NV; ++k) {
+      ps[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        x[k * VW + e] = in.o[k].get(e);
+        ps[k] = fmaf(x[k * VW + e], x[k * VW + e], ps[k]);
       }
     }
     if (p.w) {
-      float ps[NV];
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        ps[k] = 0.f;
-#pragma unroll
-        for (int e = 0; e < VW; ++e) ps[k] = fmaf(x[k * VW + e], x[k * VW + e], ps[k]);
-      }
-      group_sum<VW, WARP, MODE>(p, ps, lane, team, red, sm);
+      group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red, sm);
       const float ig = (float)p.G / (float)p.D;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const float rs = rsqrtf(ps[k] * ig + p.eps);
         const int v = k * team + lane;
         if (v < nvec) {
+          float w[VW];
+          load_floats<VW>(p.w + v * VW, w);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) x[k * VW + e] *= rs * p.w[v * VW + e];
+          for (int e = 0; e < VW; ++e) x[k * VW + e] *= rs * w[e];
         }
       }
     }
@@ -158,20 +170,21 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
         const int c = v * VW;
         float* xv = x + k * VW;
         if (p.z) {
-          float z[VW];
-          load_vec<VW>((const IO*)p.z + p.sz.at(b, t) + c, z);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) xv[e] *= z[e] * sigmoid(z[e]);
+          for (int e = 0; e < VW; ++e) {
+            const float z = in.z[k].get(e);
+            xv[e] *= z * sigmoid(z);
+          }
         }
         if (p.s) {
+          float s[VW];
+          load_floats<VW>(p.s + c, s);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) xv[e] *= p.s[c + e];
+          for (int e = 0; e < VW; ++e) xv[e] *= s[e];
         }
         if (p.r) {
-          float r[VW];
-          load_vec<VW>((const IO*)p.r + p.sr.at(b, t) + c, r);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) xv[e] += r[e];
+          for (int e = 0; e < VW; ++e) xv[e] += in.r[k].get(e);
         }
         store_vec<VW>((IO*)p.out + (size_t)row * p.D + c, xv);
         // the second norm is that of the stored stream, so that the backward
@@ -190,8 +203,10 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
         const int v = k * team + lane;
         if (v < nvec) {
           float* xv = x + k * VW;
+          float w[VW];
+          load_floats<VW>(p.w2 + v * VW, w);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) xv[e] *= rs * p.w2[v * VW + e];
+          for (int e = 0; e < VW; ++e) xv[e] *= rs * w[e];
           store_vec<VW>((IO*)p.n + (size_t)row * p.D + v * VW, xv);
         }
       }
@@ -204,7 +219,7 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
 // and with mh = o rs, core = mh w, f = e s:
 //   ds = sum e core silu(z)     dz = f core silu'(z)     dw = sum f silu(z) mh
 //   do = rs (k - mh mean_group(k mh)),  k = f silu(z) w
-template <typename IO, int VW, bool WARP, int MODE, int MAXT>
+template <typename IO, int E, int VW, bool WARP, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
   extern __shared__ float sm[];
   __shared__ float red[32];
@@ -219,61 +234,81 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
   float dw[E], ds[E], dw2[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = ds[i] = dw2[i] = 0.f;
-  for (int64_t row = row0; row < p.rows; row += step) {
-    const int b = (int)(row / p.T), t = (int)(row % p.T);
-    float e[E], x[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) e[i] = x[i] = 0.f;
-    if (p.dn) {
-      float ss = 0.f, qx = 0.f;
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int v = k * team + lane;
-        if (v < nvec) {
-          load_vec<VW>((const IO*)p.out + (size_t)row * p.D + v * VW, x + k * VW);
-          load_vec<VW>((const IO*)p.dn + (size_t)row * p.D + v * VW, e + k * VW);
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            const int i = k * VW + j;
-            ss = fmaf(x[i], x[i], ss);
-            qx = fmaf(e[i] * p.w2[v * VW + j], x[i], qx);
-          }
-        }
-      }
-      const float rs = rsqrtf(team_sum<WARP>(ss, red) * id + p.eps);
-      const float m = team_sum<WARP>(qx, red) * id * rs * rs;
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int v = k * team + lane;
-        if (v < nvec) {
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            const int i = k * VW + j;
-            dw2[i] = fmaf(e[i] * rs, x[i], dw2[i]);
-            e[i] = rs * (e[i] * p.w2[v * VW + j] - x[i] * m);
-          }
-        }
-      }
-    }
-    float ps[NV], rs[NV];
+  struct In {
+    Raw<IO, VW> o[NV], z[NV], out[NV], dout[NV], dn[NV];
+  };
+  auto fetch = [&](int64_t row, In& in) {
+    const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
+    const size_t at = (size_t)row * p.D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = k * team + lane;
+      const int v = k * team + lane, c = v * VW;
+      const bool on = v < nvec;
+      if (p.dn) {
+        in.out[k].load_if((const IO*)p.out + at + c, on);
+        in.dn[k].load_if((const IO*)p.dn + at + c, on);
+      }
+      in.o[k].load_if((const IO*)p.o + o_at(p, p.so, b, t, c), on);
+      if (p.dout) in.dout[k].load_if((const IO*)p.dout + at + c, on);
+      if (p.z) in.z[k].load_if((const IO*)p.z + p.sz.at(b, t) + c, on);
+    }
+  };
+  In nx;
+  if (row0 < p.rows) fetch(row0, nx);
+  for (int64_t row = row0; row < p.rows; row += step) {
+    const In in = nx;
+    if (row + step < p.rows) fetch(row + step, nx);
+    float e[E], x[E], ps[NV], rs[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
       ps[k] = 0.f;
-      if (v < nvec) {
-        load_vec<VW>((const IO*)p.o + o_at(p, p.so, b, t, v * VW), x + k * VW);
 #pragma unroll
-        for (int j = 0; j < VW; ++j) ps[k] = fmaf(x[k * VW + j], x[k * VW + j], ps[k]);
-        if (p.dout) {
-          float g[VW];
-          load_vec<VW>((const IO*)p.dout + (size_t)row * p.D + v * VW, g);
-#pragma unroll
-          for (int j = 0; j < VW; ++j) e[k * VW + j] += g[j];
-        }
-        if (p.dr) store_vec<VW>((IO*)p.dr + (size_t)row * p.D + v * VW, e + k * VW);
+      for (int j = 0; j < VW; ++j) {
+        x[k * VW + j] = in.o[k].get(j);
+        ps[k] = fmaf(x[k * VW + j], x[k * VW + j], ps[k]);
+        e[k * VW + j] = p.dout ? in.dout[k].get(j) : 0.f;
       }
     }
-    if (p.w) group_sum<VW, WARP, MODE>(p, ps, lane, team, red, sm);
+    if (p.dn) {
+      float ss = 0.f, qx = 0.f;
+      float w2[E];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = k * team + lane;
+        if (v < nvec) {
+          load_floats<VW>(p.w2 + v * VW, w2 + k * VW);
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            const float xo = in.out[k].get(j);
+            ss = fmaf(xo, xo, ss);
+            qx = fmaf(in.dn[k].get(j) * w2[k * VW + j], xo, qx);
+          }
+        }
+      }
+      const float r2 = rsqrtf(team_sum<WARP>(ss, red) * id + p.eps);
+      const float m = team_sum<WARP>(qx, red) * id * r2 * r2;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = k * team + lane;
+        if (v < nvec) {
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            const int i = k * VW + j;
+            const float xo = in.out[k].get(j), dn = in.dn[k].get(j);
+            dw2[i] = fmaf(dn * r2, xo, dw2[i]);
+            e[i] += r2 * (dn * w2[i] - xo * m);
+          }
+        }
+      }
+    }
+    if (p.dr) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = k * team + lane;
+        if (v < nvec) store_vec<VW>((IO*)p.dr + (size_t)row * p.D + v * VW, e + k * VW);
+      }
+    }
+    if (p.w) group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red, sm);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = k * team + lane;
@@ -281,31 +316,43 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
       ps[k] = 0.f;
       if (v < nvec) {
         const int c = v * VW;
-        float z[VW], dz[VW];
-        if (p.z) load_vec<VW>((const IO*)p.z + p.sz.at(b, t) + c, z);
+        float dz[VW], wv[VW], sv[VW];
+#pragma unroll
+        for (int j = 0; j < VW; ++j) wv[j] = sv[j] = 1.f;
+        if (p.w) load_floats<VW>(p.w + c, wv);
+        if (p.s) load_floats<VW>(p.s + c, sv);
+        if (p.z) {
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            const int i = k * VW + j;
+            x[i] *= rs[k];  // mh
+            const float core = x[i] * wv[j], f = e[i] * sv[j];
+            const float z = in.z[k].get(j), sg = sigmoid(z), si = z * sg;
+            dz[j] = f * core * fmaf(-si, sg, sg + si);
+            ds[i] = fmaf(e[i] * core, si, ds[i]);
+            e[i] = f * si;
+          }
+          if (p.dz) store_vec<VW>((IO*)p.dz + (size_t)row * p.D + c, dz);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            const int i = k * VW + j;
+            x[i] *= rs[k];
+            ds[i] = fmaf(e[i], x[i] * wv[j], ds[i]);
+            e[i] *= sv[j];
+          }
+        }
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
           const int i = k * VW + j;
-          const float wv = p.w ? p.w[c + j] : 1.f, sv = p.s ? p.s[c + j] : 1.f;
-          x[i] *= rs[k];  // mh
-          const float core = x[i] * wv;
-          float f = e[i] * sv;
-          if (p.z) {
-            const float sg = sigmoid(z[j]), si = z[j] * sg;
-            dz[j] = f * core * (sg + si * (1.f - sg));
-            ds[i] = fmaf(e[i] * core, si, ds[i]);
-            f *= si;
-          } else {
-            ds[i] = fmaf(e[i], core, ds[i]);
-          }
-          dw[i] = fmaf(f, x[i], dw[i]);
-          e[i] = f * wv;  // the gradient at mh
+          dw[i] = fmaf(e[i], x[i], dw[i]);
+          e[i] *= wv[j];  // the gradient at mh
           ps[k] = fmaf(e[i], x[i], ps[k]);
         }
-        if (p.dz) store_vec<VW>((IO*)p.dz + (size_t)row * p.D + c, dz);
       }
     }
-    if (p.w) group_sum<VW, WARP, MODE>(p, ps, lane, team, red, sm);
+    if (p.w) group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red, sm);
+    const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = k * team + lane;
@@ -360,7 +407,8 @@ struct Shape {
   size_t smem;  // of the group sums
 };
 
-Shape shape_of(const lz_norm_dims* d, bool vec) {
+// E: elements of a thread
+Shape shape_of(const lz_norm_dims* d, bool vec, int E) {
   Shape s;
   s.vec = vec;
   s.vw = vec ? (int)(16 / esize(d->io)) : 1;
@@ -368,7 +416,7 @@ Shape shape_of(const lz_norm_dims* d, bool vec) {
   const int gd = d->D / d->G;
   const int gv = gd % s.vw == 0 ? gd / s.vw : 0;
   s.mode = d->G == 1 ? GROUP_ROW : (gv >= 1 && gv <= 32 && (gv & (gv - 1)) == 0) ? GROUP_LANES : GROUP_SMEM;
-  s.warp = d->D <= 32 * E && s.mode != GROUP_SMEM;
+  s.warp = d->D <= kWarpD && s.mode != GROUP_SMEM;
   s.threads = s.warp ? kRowWarps * 32 : (nvec * s.vw + E - 1) / E;
   s.threads = (s.threads + 31) / 32 * 32;
   s.smem = s.mode == GROUP_SMEM ? (size_t)(nvec + d->G) * sizeof(float) : 0;
@@ -385,13 +433,13 @@ int grid_rows(Kern k, int64_t rows, int threads, size_t smem, int rows_per_block
   return (int)std::max<int64_t>(1, std::min<int64_t>(want, wave));
 }
 
-template <typename IO, int VW, bool WARP, int MODE>
+template <typename IO, int E, int VW, bool WARP, int MODE>
 cudaError_t go_fwd(const NormParams& p, const Shape& sh, cudaStream_t s) {
   constexpr int kT = WARP ? kRowWarps * 32 : 512;
   // rows of more than 8192 features need blocks of up to 1024 threads
-  auto k = norm_fwd_kernel<IO, VW, WARP, MODE, kT>;
-  if constexpr (!WARP) {
-    if (sh.threads > kT) k = norm_fwd_kernel<IO, VW, WARP, MODE, 1024>;
+  auto k = norm_fwd_kernel<IO, E, VW, WARP, MODE, kT>;
+  if constexpr (!WARP && E == 16) {
+    if (sh.threads > kT) k = norm_fwd_kernel<IO, E, VW, WARP, MODE, 1024>;
   }
   if (sh.smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
@@ -407,13 +455,13 @@ cudaError_t go_fwd(const NormParams& p, const Shape& sh, cudaStream_t s) {
 constexpr int kMaxBlocks = 148 * 8;
 int bwd_part_rows(int64_t rows) { return (int)std::min<int64_t>(std::max<int64_t>(rows, 1), kMaxBlocks); }
 
-template <typename IO, int VW, bool WARP, int MODE>
+template <typename IO, int E, int VW, bool WARP, int MODE>
 cudaError_t go_bwd(const NormParams& p, const Shape& sh, int* blocks, cudaStream_t s) {
   constexpr int kT = WARP ? kRowWarps * 32 : 512;
   // rows of more than 8192 features need blocks of up to 1024 threads
-  auto k = norm_bwd_kernel<IO, VW, WARP, MODE, kT>;
-  if constexpr (!WARP) {
-    if (sh.threads > kT) k = norm_bwd_kernel<IO, VW, WARP, MODE, 1024>;
+  auto k = norm_bwd_kernel<IO, E, VW, WARP, MODE, kT>;
+  if constexpr (!WARP && E == 16) {
+    if (sh.threads > kT) k = norm_bwd_kernel<IO, E, VW, WARP, MODE, 1024>;
   }
   const size_t smem = WARP ? std::max(sh.smem, (size_t)kRowWarps * p.D * sizeof(float)) : sh.smem;
   if (smem > 48 * 1024) {
@@ -455,6 +503,8 @@ lz_status check_norm(const char* fn, const lz_norm_dims* d) {
     return layer_fail(LZ_ERR_INVALID_ARG, "%s: heads must be 0 or 1 (got %d)", fn, d->heads);
   if (!(d->eps > 0.f && d->eps < 3.0e38f))
     return layer_fail(LZ_ERR_INVALID_ARG, "%s: eps must be finite and > 0", fn);
+  if ((int64_t)d->B * d->T >= (int64_t(1) << 31))
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: B * T must be below 2^31", fn);
   if (!rows_ok(d->o) || !rows_ok(d->z) || !rows_ok(d->r))
     return layer_fail(LZ_ERR_INVALID_ARG, "%s: bad row strides", fn);
   return LZ_OK;
@@ -499,9 +549,9 @@ extern "C" lz_status lz_block_norm_fwd(const lz_norm_dims* d, const void* o, con
   p.sz = rows_of(d->z, d->T, d->D);
   p.sr = rows_of(d->r, d->T, d->D);
   p.o = o; p.w = w; p.z = z; p.s = s; p.r = r; p.w2 = w2; p.out = out; p.n = n;
-  const Shape sh = shape_of(d, norm_vec(d, p));
+  const Shape sh = shape_of(d, norm_vec(d, p), 16);
   cudaError_t e = cudaSuccess;
-#define LZ_CALL(IO, VW, WARP, MODE) go_fwd<IO, VW, WARP, MODE>(p, sh, (cudaStream_t)stream)
+#define LZ_CALL(IO, VW, WARP, MODE) go_fwd<IO, 16, VW, WARP, MODE>(p, sh, (cudaStream_t)stream)
   LZ_NORM_DISPATCH(LZ_CALL);
 #undef LZ_CALL
   return layer_done(e, fn);
@@ -536,10 +586,15 @@ extern "C" lz_status lz_block_norm_bwd(const lz_norm_dims* d, const void* o, con
   p.sz = rows_of(d->z, d->T, d->D);
   p.o = o; p.w = w; p.z = z; p.s = s; p.w2 = w2; p.out = const_cast<void*>(out);
   p.dout = dout; p.dn = dn; p.d_o = dOo; p.dz = dz; p.dr = dr; p.part = (float*)ws;
-  const Shape sh = shape_of(d, norm_vec(d, p));
+  // 8 elements a thread leave room for the next row's loads beside the
+  // parameter gradients, up to the 512 threads that 128 registers allow
+  const bool narrow = d->D > kWarpD && d->D <= 4096;
+  const Shape sh = shape_of(d, norm_vec(d, p), narrow ? 8 : 16);
   cudaError_t e = cudaSuccess;
   int blocks = 0;
-#define LZ_CALL(IO, VW, WARP, MODE) go_bwd<IO, VW, WARP, MODE>(p, sh, &blocks, (cudaStream_t)stream)
+#define LZ_CALL(IO, VW, WARP, MODE)                                                          \
+  (narrow && !sh.warp ? go_bwd<IO, 8, VW, false, MODE>(p, sh, &blocks, (cudaStream_t)stream) \
+                      : go_bwd<IO, 16, VW, WARP, MODE>(p, sh, &blocks, (cudaStream_t)stream))
   LZ_NORM_DISPATCH(LZ_CALL);
 #undef LZ_CALL
   if (e == cudaSuccess && (dw || ds || dw2))

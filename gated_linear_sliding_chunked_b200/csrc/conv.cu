@@ -14,7 +14,7 @@ namespace {
 constexpr int NT = 128;
 
 struct ConvParams {
-  int B, T, D, silu, run;  // run: tokens of a thread
+  int B, T, D, silu, run;  // run: tokens of a thread, a multiple of RT
   Rows x;
   const void* px;
   const float* w;
@@ -25,103 +25,145 @@ struct ConvParams {
   void* xT;
 };
 
+constexpr int RT = 8;  // tokens whose loads are in flight at once
+
 // x at token t of sequence b; the history where t < 0
 template <typename IO, int K, int VW>
-__device__ __forceinline__ void load_x(const ConvParams& p, int b, int t, int c, float* v) {
-  if (t >= 0) {
-    load_vec<VW>((const IO*)p.px + p.x.at(b, t) + c, v);
-  } else if (p.x0) {
-    load_vec<VW>((const IO*)p.x0 + ((size_t)b * (K - 1) + (t + K - 1)) * p.D + c, v);
+__device__ __forceinline__ void load_x(const ConvParams& p, int b, int t, int c, Raw<IO, VW>& v) {
+  if (t >= 0) v.load((const IO*)p.px + p.x.at(b, t) + c);
+  else if (p.x0) v.load((const IO*)p.x0 + ((size_t)b * (K - 1) + (t + K - 1)) * p.D + c);
+  else v.zero();
+}
+
+// Taps and biases of VW neighbouring channels: w[e * K + j]
+template <int K, int VW>
+__device__ __forceinline__ void load_taps(const ConvParams& p, int c, float* w, float* bias) {
+  load_floats<K * VW>(p.w + (size_t)c * K, w);
+  if (p.bias) {
+    load_floats<VW>(p.bias + c, bias);
   } else {
 #pragma unroll
-    for (int e = 0; e < VW; ++e) v[e] = 0.f;
+    for (int e = 0; e < VW; ++e) bias[e] = 0.f;
   }
 }
 
 template <typename IO, int K, int VW>
 __global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvParams p) {
   const int nvec = p.D / VW;
-  const int nrun = (p.T + p.run - 1) / p.run;
-  const size_t idx = (size_t)blockIdx.x * NT + threadIdx.x;
+  const int nrun = max(1, (p.T + p.run - 1) / p.run);
+  const unsigned idx = blockIdx.x * NT + threadIdx.x;
   const int b = blockIdx.y;
-  const int c = (int)(idx % nvec) * VW;
-  const int run = (int)(idx / nvec);
-  if (run >= (nrun > 0 ? nrun : 1)) return;
+  const int run = (int)(idx / (unsigned)nvec);
+  const int c = (int)(idx - (unsigned)run * nvec) * VW;
+  if (run >= nrun) return;
   const int L = seq_len(p.lens, b, p.T);
   if (run == 0 && p.xT) {
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
-      float v[VW];
+      Raw<IO, VW> v;
       load_x<IO, K, VW>(p, b, L - (K - 1) + j, c, v);
-      store_vec<VW>((IO*)p.xT + ((size_t)b * (K - 1) + j) * p.D + c, v);
+      v.put((IO*)p.xT + ((size_t)b * (K - 1) + j) * p.D + c);
     }
   }
   const int t0 = run * p.run, t1 = min(p.T, t0 + p.run), te = min(t1, L);
-  float w[K][VW], bias[VW], h[K][VW];
-#pragma unroll
-  for (int e = 0; e < VW; ++e) {
-#pragma unroll
-    for (int j = 0; j < K; ++j) w[j][e] = p.w[(size_t)(c + e) * K + j];
-    bias[e] = p.bias ? p.bias[c + e] : 0.f;
-  }
-  IO* y = (IO*)p.y + ((size_t)b * p.T) * p.D + c;
+  IO* y = (IO*)p.y + ((size_t)b * p.T + t0) * p.D + c;
+  const IO* x = (const IO*)p.px + p.x.at(b, t0) + c;
+  float w[K * VW], bias[VW], h[K > 1 ? K - 1 : 1][VW];
   if (t0 < te) {
+    Raw<IO, VW> v[RT], g[K > 1 ? K - 1 : 1];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) load_x<IO, K, VW>(p, b, t0 - (K - 1) + j, c, h[j]);
-#pragma unroll 4
-    for (int t = t0; t < te; ++t) {
-      load_vec<VW>((const IO*)p.px + p.x.at(b, t) + c, h[K - 1]);
-      float o[VW];
+    for (int j = 0; j < K - 1; ++j) load_x<IO, K, VW>(p, b, t0 - (K - 1) + j, c, g[j]);
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        float a = bias[e];
+    for (int i = 0; i < RT; ++i) v[i].load_if(x + i * p.x.ld, t0 + i < te);
+    load_taps<K, VW>(p, c, w, bias);
 #pragma unroll
-        for (int j = 0; j < K; ++j) a = fmaf(w[j][e], h[j][e], a);
-        o[e] = p.silu ? a * sigmoid(a) : a;
+    for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) h[j][e] = h[j + 1][e];
+      for (int e = 0; e < VW; ++e) h[j][e] = g[j].get(e);
+    for (int t = t0;;) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float o[VW];
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          const float xe = v[i].get(e);
+          float a = fmaf(w[e * K + K - 1], xe, bias[e]);
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) a = fmaf(w[e * K + j], h[j][e], a);
+#pragma unroll
+          for (int j = 0; j + 1 < K - 1; ++j) h[j][e] = h[j + 1][e];
+          if (K > 1) h[K - 2 < 0 ? 0 : K - 2][e] = xe;
+          o[e] = a;
+        }
+        if (p.silu) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) o[e] *= sigmoid(o[e]);
+        }
+        if (t + i < te) store_vec<VW>(y + (size_t)i * p.D, o);
       }
-      store_vec<VW>(y + (size_t)t * p.D, o);
+      t += RT;
+      if (t >= te) break;
+      x += RT * p.x.ld;
+      y += (size_t)RT * p.D;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) v[i].load_if(x + i * p.x.ld, t + i < te);
     }
   }
-  float zero[VW];
-#pragma unroll
-  for (int e = 0; e < VW; ++e) zero[e] = 0.f;
-  for (int t = max(t0, te); t < t1; ++t) store_vec<VW>(y + (size_t)t * p.D, zero);
+  if (te < t1) {  // behind the sequence's end: zeros
+    Raw<IO, VW> z;
+    z.zero();
+    IO* yz = (IO*)p.y + ((size_t)b * p.T) * p.D + c;
+    for (int t = max(t0, te); t < t1; ++t) z.put(yz + (size_t)t * p.D);
+  }
 }
 
 template <typename IO, int K, int VW>
 __global__ void __launch_bounds__(NT) conv_step_kernel(ConvParams p, void* hist) {
-  const int nvec = p.D / VW;
-  const size_t idx = (size_t)blockIdx.x * NT + threadIdx.x;
-  const int c = (int)(idx % nvec) * VW;
-  const int b = (int)(idx / nvec);
-  if (b >= p.B) return;
-  float h[K][VW];
-  IO* hp = (IO*)hist + (size_t)b * (K - 1) * p.D + c;
-  load_vec<VW>((const IO*)p.px + p.x.at(b, 0) + c, h[K - 1]);
+  const int c = (blockIdx.x * NT + threadIdx.x) * VW;
+  if (c >= p.D) return;
+  float w[K * VW], bias[VW];
+  load_taps<K, VW>(p, c, w, bias);
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    Raw<IO, VW> h[K];
+    IO* hp = (IO*)hist + (size_t)b * (K - 1) * p.D + c;
+    h[K - 1].load((const IO*)p.px + p.x.at(b, 0) + c);
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) load_vec<VW>(hp + (size_t)j * p.D, h[j]);
+    for (int j = 0; j < K - 1; ++j) {
+      // (plain loads: the history is written below)
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) store_vec<VW>(hp + (size_t)j * p.D, h[j + 1]);
-  float o[VW];
+      for (int i = 0; i < Raw<IO, VW>::W; ++i) h[j].w[i] = 0;
+      Raw<IO, VW>& r = h[j];
+      const IO* q = hp + (size_t)j * p.D;
+      if constexpr (VW == 1) {
+        if constexpr (sizeof(IO) == 2) r.w[0] = *reinterpret_cast<const unsigned short*>(q);
+        else r.w[0] = *reinterpret_cast<const uint32_t*>(q);
+      } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(q);
+        r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+      }
+    }
 #pragma unroll
-  for (int e = 0; e < VW; ++e) {
-    float a = p.bias ? p.bias[c + e] : 0.f;
+    for (int j = 0; j < K - 1; ++j) h[j + 1].put(hp + (size_t)j * p.D);
+    float o[VW];
 #pragma unroll
-    for (int j = 0; j < K; ++j) a = fmaf(p.w[(size_t)(c + e) * K + j], h[j][e], a);
-    o[e] = p.silu ? a * sigmoid(a) : a;
+    for (int e = 0; e < VW; ++e) {
+      float a = fmaf(w[e * K + K - 1], h[K - 1].get(e), bias[e]);
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) a = fmaf(w[e * K + j], h[j].get(e), a);
+      o[e] = p.silu ? a * sigmoid(a) : a;
+    }
+    store_vec<VW>((IO*)p.y + (size_t)b * p.D + c, o);
   }
-  store_vec<VW>((IO*)p.y + (size_t)b * p.D + c, o);
 }
 
 // ---- backward -------------------------------------------------------------
 // dp_t = dy_t act'(p_t) needs the inputs up to K-1 tokens back, dx_t =
 // sum_j w_j dp_{t+K-1-j} the dp up to K-1 tokens ahead: a run of tokens
-// [t0, t1) forms dp for [t0, t1 + K-1) with both windows in registers.  A warp
-// holds 32 channel vectors, the block's warps neighbouring runs; the parameter
-// gradients stay in registers over the run and are added across the warps in
-// shared memory, one partial per block, which launch_sum_rows adds up.
+// [t0, t1) forms dp for [t0, t1 + K-1) with both windows in registers, RT
+// tokens at a time.  A warp holds 32 channel vectors, the block's warps
+// neighbouring runs; the parameter gradients stay in registers over the run
+// and are added across the warps in shared memory, one partial per block,
+// which launch_sum_rows adds up.
 constexpr int kWarps = 4;
 
 struct ConvBwdParams {
@@ -136,6 +178,7 @@ struct ConvBwdParams {
 template <typename IO, int K, int VW>
 __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) {
   __shared__ float red[kWarps][32 * VW];
+  constexpr int KW = K > 1 ? K - 1 : 1;
   const ConvParams& p = q.f;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int b = blockIdx.z;
@@ -143,80 +186,86 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) 
   const bool on = c < p.D;
   const int L = seq_len(p.lens, b, p.T);
   const int t0 = (blockIdx.y * kWarps + warp) * p.run, t1 = min(p.T, t0 + p.run);
-  const bool first = t0 == 0;
-  float w[K][VW], bias[VW], xw[K][VW], dpw[K][VW], dw[K][VW], db[VW];
+  const bool first = t0 == 0 && q.dx0;
+  float w[K * VW], bias[VW], xw[KW][VW], dpw[KW][VW], dw[K][VW], db[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      w[j][e] = on ? p.w[(size_t)(c + e) * K + j] : 0.f;
-      dw[j][e] = 0.f;
-      dpw[j][e] = 0.f;
-    }
-    bias[e] = on && p.bias ? p.bias[c + e] : 0.f;
     db[e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j][e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < KW; ++j) dpw[j][e] = xw[j][e] = 0.f;
   }
-  if (on && (t0 < t1 || (first && q.dx0))) {
+  if (on && (t0 < t1 || first)) {
+    load_taps<K, VW>(p, c, w, bias);
     IO* dx = (IO*)q.dx + (size_t)b * p.T * p.D + c;
     if (t0 < L) {
+      Raw<IO, VW> g[KW];
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) load_x<IO, K, VW>(p, b, t0 - (K - 1) + j, c, xw[j]);
+      for (int j = 0; j < K - 1; ++j) load_x<IO, K, VW>(p, b, t0 - (K - 1) + j, c, g[j]);
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) xw[j][e] = g[j].get(e);
     }
     // s walks the tokens whose dp is formed; dx of token s - (K-1) is then complete
-#pragma unroll 4
-    for (int s = t0; s < t1 + K - 1; ++s) {
-      if (s < L) {
-        float dyv[VW];
-        load_vec<VW>((const IO*)p.px + p.x.at(b, s) + c, xw[K - 1]);
-        load_vec<VW>((const IO*)q.dy + ((size_t)b * p.T + s) * p.D + c, dyv);
+    for (int s0 = t0; s0 < t1 + K - 1; s0 += RT) {
+      Raw<IO, VW> xv[RT], dyv[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int s = s0 + i;
+        const bool live = s < t1 + K - 1 && s < L;
+        xv[i].load_if((const IO*)p.px + p.x.at(b, s) + c, live);
+        dyv[i].load_if((const IO*)q.dy + ((size_t)b * p.T + s) * p.D + c, live);
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int s = s0 + i, t = s - (K - 1);
+        float dp[VW], o[VW];
 #pragma unroll
         for (int e = 0; e < VW; ++e) {
-          float dp = dyv[e];
+          const float xe = xv[i].get(e);
+          float a = fmaf(w[e * K + K - 1], xe, bias[e]);
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) a = fmaf(w[e * K + j], xw[j][e], a);
+          // (dy is zero behind the end, and with it dp)
+          float g = dyv[i].get(e);
           if (p.silu) {
-            float a = bias[e];
-#pragma unroll
-            for (int j = 0; j < K; ++j) a = fmaf(w[j][e], xw[j][e], a);
-            const float sg = sigmoid(a);
-            dp *= sg * (1.f + a * (1.f - sg));
+            const float sg = sigmoid(a), as = a * sg;
+            g *= fmaf(-as, sg, sg + as);
           }
-          dpw[K - 1][e] = dp;
-          if (s < t1) {
-            db[e] += dp;
+          dp[e] = g;
+          const float own = s < t1 ? g : 0.f;  // tokens of the next run are its own
+          db[e] += own;
+          dw[K - 1][e] = fmaf(own, xe, dw[K - 1][e]);
 #pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][e] = fmaf(dp, xw[j][e], dw[j][e]);
+          for (int j = 0; j < K - 1; ++j) dw[j][e] = fmaf(own, xw[j][e], dw[j][e]);
+          // dx_t = sum_j w_j dp_{s-j}
+          o[e] = w[e * K] * g;
+#pragma unroll
+          for (int j = 1; j < K; ++j) o[e] = fmaf(w[e * K + j], dpw[K - 1 - j][e], o[e]);
+#pragma unroll
+          for (int j = 0; j + 1 < K - 1; ++j) {
+            xw[j][e] = xw[j + 1][e];
+            dpw[j][e] = dpw[j + 1][e];
           }
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) xw[j][e] = xw[j + 1][e];
+          if (K > 1) {
+            xw[KW - 1][e] = xe;
+            dpw[KW - 1][e] = g;
+          }
         }
-      } else {
+        if (t < t1 && (t >= t0 || first)) {
+          const int jT = t - (L - (K - 1));  // token t is row jT of the final history
+          if (q.dxT && jT >= 0 && t < L) {
+            float g[VW];
+            load_vec<VW>((const IO*)q.dxT + ((size_t)b * (K - 1) + jT) * p.D + c, g);
 #pragma unroll
-        for (int e = 0; e < VW; ++e) dpw[K - 1][e] = 0.f;
+            for (int e = 0; e < VW; ++e) o[e] += g[e];
+          }
+          if (t >= 0) store_vec<VW>(dx + (size_t)t * p.D, o);
+          else store_vec<VW>((IO*)q.dx0 + ((size_t)b * (K - 1) + t + K - 1) * p.D + c, o);
+        }
       }
-      const int t = s - (K - 1);
-      if (t >= t0 || (first && q.dx0)) {
-        float o[VW];
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          o[e] = 0.f;
-#pragma unroll
-          for (int j = 0; j < K; ++j) o[e] = fmaf(w[j][e], dpw[K - 1 - j][e], o[e]);
-        }
-        const int jT = t - (L - (K - 1));  // token t is row jT of the final history
-        if (q.dxT && jT >= 0 && t < L) {
-          float g[VW];
-          load_vec<VW>((const IO*)q.dxT + ((size_t)b * (K - 1) + jT) * p.D + c, g);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) o[e] += g[e];
-        }
-        if (t >= 0)
-          store_vec<VW>(dx + (size_t)t * p.D, o);
-        else
-          store_vec<VW>((IO*)q.dx0 + ((size_t)b * (K - 1) + t + K - 1) * p.D + c, o);
-      }
-#pragma unroll
-      for (int e = 0; e < VW; ++e)
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) dpw[j][e] = dpw[j + 1][e];
     }
   }
   // ---- the block's partial of dw, dbias: warps added in order
@@ -255,7 +304,7 @@ lz_status check_conv(const char* fn, const lz_conv_dims* d) {
   if (!rows_ok(d->x)) return layer_fail(LZ_ERR_INVALID_ARG, "%s: bad row strides", fn);
   if (d->B > 65535) return layer_fail(LZ_ERR_UNSUPPORTED, "%s: B must be <= 65535 (got %d)", fn, d->B);
   // keeps grid dimensions and 32-bit token indices in range
-  if (d->T > (1 << 23) || (double)d->T * d->D > (double)(1ll << 36))
+  if (d->T > (1 << 23) || (double)d->T * d->D > (double)(1ll << 34))
     return layer_fail(LZ_ERR_UNSUPPORTED, "%s: problem too large (T %d, D %d)", fn, d->T, d->D);
   return LZ_OK;
 }
@@ -297,9 +346,11 @@ struct StepParams {
 template <typename IO, int K, int VW>
 struct StepLaunch {
   static cudaError_t go(const StepParams& q, cudaStream_t s) {
-    const size_t n = (size_t)q.p.B * (q.p.D / VW);
+    const int gx = (q.p.D / VW + NT - 1) / NT;
+    // a thread keeps its taps over several sequences once the device is full
+    const int gy = std::max(1, std::min(q.p.B, 148 * 8 / gx));
     ScopedTiming tm("conv_step", s);
-    conv_step_kernel<IO, K, VW><<<(unsigned)((n + NT - 1) / NT), NT, 0, s>>>(q.p, q.hist);
+    conv_step_kernel<IO, K, VW><<<dim3(gx, gy), NT, 0, s>>>(q.p, q.hist);
     return cudaGetLastError();
   }
 };
@@ -352,12 +403,12 @@ extern "C" lz_status lz_conv_fwd(const lz_conv_dims* d, const void* x, const flo
                        {x0, "x0", false, 16}, {lens, "lens", false, 8}, {y, "y", data, 16}, {xT, "xT", false, 16}});
   if (st == LZ_OK) st = check_distinct(fn, {y, xT}, {x, x0});
   if (st != LZ_OK) return st;
-  ConvParams p{d->B, d->T, d->D, d->silu, 16, rows_of(d->x, d->T, d->D), x, w, bias, x0, lens, y, xT};
+  ConvParams p{d->B, d->T, d->D, d->silu, RT, rows_of(d->x, d->T, d->D), x, w, bias, x0, lens, y, xT};
   const bool vec = conv_vec(d, x, p.x);
-  // runs of 16 tokens re-read 3/16 of the input from L2; with few of them
-  // (short prompts) runs of 4 put four times the threads on the machine
-  const size_t threads = (size_t)d->B * ((d->T + 15) / 16) * (d->D / (vec ? 16 / esize(d->io) : 1));
-  if (threads < 148 * 1024) p.run = 4;
+  // long runs re-read less of the input (K - 1 tokens each, from L2); with few
+  // of them runs of RT tokens put more threads on the machine
+  const size_t vecs = d->D / (vec ? 16 / esize(d->io) : 1);
+  while (p.run < 4 * RT && (size_t)d->B * ((d->T + 2 * p.run - 1) / (2 * p.run)) * vecs >= 148 * 2048) p.run *= 2;
   return layer_done(dispatch_k<FwdLaunch>(p, d->K, d->io == LZ_BF16, vec, (cudaStream_t)stream), fn);
 }
 
@@ -403,7 +454,7 @@ extern "C" lz_status lz_conv_step(const lz_conv_dims* d, void* hist, const void*
                        {bias, "bias", false, 16}, {y, "y", true, 16}});
   if (st == LZ_OK) st = check_distinct(fn, {hist, y}, {x});
   if (st != LZ_OK) return st;
-  StepParams q{{d->B, 1, d->D, d->silu, 1, rows_of(d->x, 1, d->D), x, w, bias, nullptr, nullptr, y, nullptr}, hist};
+  StepParams q{{d->B, 1, d->D, d->silu, RT, rows_of(d->x, 1, d->D), x, w, bias, nullptr, nullptr, y, nullptr}, hist};
   return layer_done(
       dispatch_k<StepLaunch>(q, d->K, d->io == LZ_BF16, conv_vec(d, x, q.p.x), (cudaStream_t)stream), fn);
 }

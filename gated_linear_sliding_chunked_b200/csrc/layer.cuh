@@ -76,8 +76,83 @@ __device__ __forceinline__ void store_vec(bf16* p, const float* x) {
   }
 }
 
-// sigma(x): exp's overflow for very negative x gives 1 / inf = 0, the limit
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// sigma(x) (1 / inf = 0 where exp(-x) overflows)
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+
+// V consecutive elements of a row as they are in memory (V * sizeof(IO) bytes:
+// a multiple of 4; V = 1: one element)
+template <typename IO, int V>
+struct Raw {
+  static constexpr int W = (V * (int)sizeof(IO) + 3) / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const IO* p) {
+    if constexpr (V * sizeof(IO) == 2) {
+      w[0] = *reinterpret_cast<const unsigned short*>(p);
+    } else if constexpr (W % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+        w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+      }
+    } else if constexpr (W % 2 == 0) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = x.x; w[1] = x.y;
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    }
+  }
+  // (written out under both conditions: a value kept where there is nothing to
+  // load would be selected after the load, which then waits for memory there)
+  __device__ __forceinline__ void load_if(const IO* p, bool on) {
+    if (on) load(p);
+    else zero();
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ void put(IO* p) const {
+    if constexpr (V * sizeof(IO) == 2) *reinterpret_cast<unsigned short*>(p) = (unsigned short)w[0];
+    else if constexpr (W % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4)
+        *(reinterpret_cast<uint4*>(p) + i / 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (W % 2 == 0) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+};
+
+// N consecutive floats from a 16-byte aligned address (any when N is not a
+// multiple of 4)
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float* x) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p + i));
+      x[i] = a.x; x[i + 1] = a.y; x[i + 2] = a.z; x[i + 3] = a.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __ldg(p + i);
+  }
+}
 
 // Tokens of sequence b (lens nullable, clamped to [0, T])
 __device__ __forceinline__ int seq_len(const int64_t* lens, int b, int T) {

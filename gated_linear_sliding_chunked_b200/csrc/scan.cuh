@@ -22,8 +22,6 @@ namespace lz {
 namespace scan {
 
 constexpr int kCk = 16;      // tokens between two saved states
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct ScanParams {
   int B, T, D, G, N, softplus;
@@ -87,18 +85,6 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// sigma(x) (1 / inf = 0 where exp(-x) overflows)
-__device__ __forceinline__ float sigm(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 __device__ __forceinline__ f2 ex2v(f2 x) { return pk(ex2(lo(x)), ex2(hi(x))); }
 
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative

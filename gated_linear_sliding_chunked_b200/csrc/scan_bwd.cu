@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
         if (p.z) {
 #pragma unroll
           for (int e = 0; e < EV; ++e) {
-            const float z = nx[s].z.get(e), sz = sigm(z), zs = z * sz;
+            const float z = nx[s].z.get(e), sz = sigmoid(z), zs = z * sz;
             x.dzf[e] = x.e[e] * fmaf(-zs, sz, sz + zs);
             x.e[e] *= zs;
           }

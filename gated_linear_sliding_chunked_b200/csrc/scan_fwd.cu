@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(64 * W, W > 4 ? 1 : 2) scan_fwd_kernel(ScanPar
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
           const float z = x.z.get(e);
-          o[e] *= z * sigm(z);
+          o[e] *= z * sigmoid(z);
         }
       }
       store_n<IO, EV>((IO*)p.y + ((size_t)b * p.T + t) * p.D + c, o, nc, p.vec);
@@ -342,62 +342,72 @@ cudaError_t go_any(const ScanParams& p, cudaStream_t s) {
 
 // ---- single tokens --------------------------------------------------------
 // The state is read and written once: bound by HBM (or L2, when it fits).
-// One thread per 4 states; the L lanes of a channel add their share of y.
+// A thread holds 4 states of one channel (its rates stay in registers) and
+// takes two sequences at a time, whose loads overlap; the L lanes of a channel
+// add their shares of y.
+constexpr int kStepThreads = 256;
+
 template <typename IO, int L>
-__global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p, float* state) {
-  const size_t idx = (size_t)blockIdx.x * 256 + threadIdx.x;
-  const int l = threadIdx.x % L;
-  const size_t bc = idx / L;
-  const bool row = bc < (size_t)p.B * p.D;
-  const int b = row ? (int)(bc / p.D) : 0, c = row ? (int)(bc % p.D) : 0;
-  const int g = c / (p.D / p.G), n0 = 4 * l;
-  const bool on = row && n0 < p.N;
-  float y = 0.f, u = 0.f;
-  if (on) {
-    float4* hp = reinterpret_cast<float4*>(state + bc * p.N + n0);
-    float4 h = *hp;
-    const float4 a = *reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0);
-    const IO* bp = (const IO*)p.Bm + p.rb.at(b, 0) + (size_t)g * p.N + n0;
-    const IO* cp = (const IO*)p.Cm + p.rc.at(b, 0) + (size_t)g * p.N + n0;
-    u = to_f(((const IO*)p.u)[p.ru.at(b, 0) + c]);
-    float d = to_f(((const IO*)p.dt)[p.rdt.at(b, 0) + c]) + (p.dtb ? p.dtb[c] : 0.f);
-    if (p.softplus) d = softplus(d);
-    const float du = d * u, d2 = d * kLog2e;
-    float B4[4], C4[4];
-    if (p.vecbc) {
-      load_vec<4>(bp, B4);
-      load_vec<4>(cp, C4);
-    } else {
+__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p, float* state) {
+  const unsigned idx = blockIdx.x * kStepThreads + threadIdx.x;
+  const int l = threadIdx.x % L, c = (int)(idx / L), n0 = 4 * l;
+  const bool row = c < p.D, on = row && n0 < p.N;
+  const int g = row ? c / (p.D / p.G) : 0;
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  float bias = 0.f, Ds = 0.f;
+  if (on) A = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0));
+  if (row && p.dtb) bias = p.dtb[c];
+  if (row && p.Dskip) Ds = p.Dskip[c];
+  for (int b0 = blockIdx.y; b0 < p.B; b0 += 2 * gridDim.y) {
+    float4 h[2];
+    Pack<IO, 4> B4[2], C4[2];
+    float u[2], d[2], z[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        B4[e] = to_f(bp[e]);
-        C4[e] = to_f(cp[e]);
+    for (int k = 0; k < 2; ++k) {
+      const int b = b0 + k * gridDim.y;
+      const bool ok = on && b < p.B;
+      h[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      u[k] = d[k] = z[k] = 0.f;
+      if (ok) {
+        h[k] = *reinterpret_cast<const float4*>(state + ((size_t)b * p.D + c) * p.N + n0);
+        u[k] = to_f(((const IO*)p.u)[p.ru.at(b, 0) + c]);
+        d[k] = to_f(((const IO*)p.dt)[p.rdt.at(b, 0) + c]);
+        if (p.z) z[k] = to_f(((const IO*)p.z)[p.rz.at(b, 0) + c]);
+      }
+      B4[k].load((const IO*)p.Bm + p.rb.at(b, 0) + (size_t)g * p.N + n0, ok ? 4 : 0, p.vecbc);
+      C4[k].load((const IO*)p.Cm + p.rc.at(b, 0) + (size_t)g * p.N + n0, ok ? 4 : 0, p.vecbc);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int b = b0 + k * gridDim.y;
+      float dl = d[k] + bias;
+      if (p.softplus) dl = softplus(dl);
+      const float du = dl * u[k], d2 = dl * kLog2e;
+      float4 x = h[k];
+      x.x = fmaf(ex2(d2 * A.x), x.x, du * B4[k].get(0));
+      x.y = fmaf(ex2(d2 * A.y), x.y, du * B4[k].get(1));
+      x.z = fmaf(ex2(d2 * A.z), x.z, du * B4[k].get(2));
+      x.w = fmaf(ex2(d2 * A.w), x.w, du * B4[k].get(3));
+      if (on && b < p.B) *reinterpret_cast<float4*>(state + ((size_t)b * p.D + c) * p.N + n0) = x;
+      float y = x.x * C4[k].get(0) + x.y * C4[k].get(1) + x.z * C4[k].get(2) + x.w * C4[k].get(3);
+#pragma unroll
+      for (int m = L / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+      if (row && l == 0 && b < p.B) {
+        y = fmaf(Ds, u[k], y);
+        if (p.z) y *= z[k] * sigmoid(z[k]);
+        ((IO*)p.y)[(size_t)b * p.D + c] = from_f<IO>(y);
       }
     }
-    h.x = fmaf(ex2(d2 * a.x), h.x, du * B4[0]);
-    h.y = fmaf(ex2(d2 * a.y), h.y, du * B4[1]);
-    h.z = fmaf(ex2(d2 * a.z), h.z, du * B4[2]);
-    h.w = fmaf(ex2(d2 * a.w), h.w, du * B4[3]);
-    *hp = h;
-    y = h.x * C4[0] + h.y * C4[1] + h.z * C4[2] + h.w * C4[3];
-  }
-#pragma unroll
-  for (int m = L / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-  if (row && l == 0) {
-    if (p.Dskip) y = fmaf(p.Dskip[c], u, y);
-    if (p.z) {
-      const float z = to_f(((const IO*)p.z)[p.rz.at(b, 0) + c]);
-      y *= z * scan::sigm(z);
-    }
-    ((IO*)p.y)[bc] = from_f<IO>(y);
   }
 }
 
 template <typename IO, int L>
 cudaError_t go_step(const ScanParams& p, float* state, cudaStream_t s) {
-  const size_t n = (size_t)p.B * p.D * L;
+  const int gx = (int)(((size_t)p.D * L + kStepThreads - 1) / kStepThreads);
+  // pairs of sequences, as many blocks as the device holds
+  const int gy = std::max(1, std::min((p.B + 1) / 2, std::max(1, 148 * 8 / gx)));
   ScopedTiming tm("scan_step", s);
-  scan_step_kernel<IO, L><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, state);
+  scan_step_kernel<IO, L><<<dim3(gx, gy), kStepThreads, 0, s>>>(p, state);
   return cudaGetLastError();
 }
 
