@@ -686,12 +686,32 @@ def _step_rows(fn, name, t, shape, dtype, dev):
     return _rows(fn, name, t.unsqueeze(1), (shape[0], 1) + tuple(shape[1:]), dtype, dev)
 
 
-def _on(dev, stream):
-    """The device guard and stream of a layer call: work goes to the tensors'
-    device, on its current stream unless one is given."""
+class _Here:
+    """The device guard of a call whose tensors are on the current device."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(dev):
+    """Work goes to the tensors' device."""
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, not {dev}")
-    return torch.cuda.device(dev)
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _stream_on(dev, stream):
+    """The stream given, or the device's current one (its handle, read without
+    building a Stream object: single-token calls are a few microseconds)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _stream(stream)
 
 
 def conv_fwd(x, w, bias=None, x0=None, *, silu=True, lens=None, want_xT=False, stream=None):
@@ -709,10 +729,10 @@ def conv_fwd(x, w, bias=None, x0=None, *, silu=True, lens=None, want_xT=False, s
     _whole(fn, (D,), torch.float32, dev, bias=bias)
     _whole(fn, (B, K - 1, D), x.dtype, dev, x0=x0)
     _whole(fn, (B,), torch.int64, dev, lens=lens)
-    with _on(dev, stream):
+    with _on(dev):
         y = torch.empty(B, T, D, dtype=x.dtype, device=dev)
         xT = torch.empty(B, K - 1, D, dtype=x.dtype, device=dev) if want_xT else None
-        lz_conv_fwd(d, x, w, bias, x0, lens, y, xT, stream)
+        lz_conv_fwd(d, x, w, bias, x0, lens, y, xT, _stream_on(dev, stream))
     return y, xT
 
 
@@ -730,14 +750,15 @@ def conv_bwd(x, w, dy, bias=None, x0=None, dxT=None, *, silu=True, lens=None, wa
     _whole(fn, (B, T, D), x.dtype, dev, dy=dy)
     _whole(fn, (B, K - 1, D), x.dtype, dev, x0=x0, dxT=dxT)
     _whole(fn, (B,), torch.int64, dev, lens=lens)
-    with _on(dev, stream):
+    with _on(dev):
         dx = torch.empty(B, T, D, dtype=x.dtype, device=dev)
         dw = torch.empty(D, K, dtype=torch.float32, device=dev)
         db = torch.empty(D, dtype=torch.float32, device=dev) if bias is not None else None
         dx0 = torch.empty(B, K - 1, D, dtype=x.dtype, device=dev) if want_dx0 else None
         n = lz_layer_workspace_bytes(d, LZ_WS_CONV_BWD)
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        lz_conv_bwd(d, x, w, bias, x0, lens, dy, dxT, dx, dw, db, dx0, ws, n, stream)
+        lz_conv_bwd(d, x, w, bias, x0, lens, dy, dxT, dx, dw, db, dx0, ws, n,
+                    _stream_on(dev, stream))
     return {"dx": dx, "dw": dw, "dbias": db, "dx0": dx0}
 
 
@@ -753,10 +774,10 @@ def conv_step(hist, x, w, bias=None, *, silu=True, y=None, stream=None):
     _whole(fn, (D,), torch.float32, dev, bias=bias)
     _whole(fn, (B, K - 1, D), x.dtype, dev, hist=hist)
     _whole(fn, (B, D), x.dtype, dev, y=y)
-    with _on(dev, stream):
+    with _on(dev):
         if y is None:
             y = torch.empty(B, D, dtype=x.dtype, device=dev)
-        lz_conv_step(d, hist, x, w, bias, y, stream)
+        lz_conv_step(d, hist, x, w, bias, y, _stream_on(dev, stream))
     return y
 
 
@@ -790,7 +811,7 @@ def scan_fwd(u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, softplus=Tru
     B, T, D = u.shape
     _whole(fn, (B, D, A.shape[1]), torch.float32, dev, h0=h0)
     _whole(fn, (B,), torch.int64, dev, lens=lens)
-    with _on(dev, stream):
+    with _on(dev):
         y = torch.empty(B, T, D, dtype=u.dtype, device=dev)
         hT = torch.empty(B, D, A.shape[1], dtype=torch.float32, device=dev) if want_hT else None
         st = None
@@ -799,7 +820,8 @@ def scan_fwd(u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, softplus=Tru
                              dtype=torch.float32, device=dev)
         n = lz_layer_workspace_bytes(d, LZ_WS_SCAN_FWD)
         ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        lz_scan_fwd(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, y, hT, st, ws, n, stream)
+        lz_scan_fwd(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, y, hT, st, ws, n,
+                    _stream_on(dev, stream))
     return (y, hT, st) if want_states else (y, hT)
 
 
@@ -818,7 +840,7 @@ def scan_bwd(u, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, dt_bias=None, softplus
     if states is not None:
         _whole(fn, (lz_layer_workspace_bytes(d, LZ_WS_SCAN_STATES) // 4,), torch.float32, dev,
                states=states)
-    with _on(dev, stream):
+    with _on(dev):
         f32 = dict(dtype=torch.float32, device=dev)
         new = lambda: torch.empty(B, T, D, dtype=u.dtype, device=dev)
         du, ddt, dz = new(), new(), new() if z is not None else None
@@ -830,7 +852,7 @@ def scan_bwd(u, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, dt_bias=None, softplus
         n = lz_layer_workspace_bytes(d, LZ_WS_SCAN_BWD)
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
         lz_scan_bwd(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT, states, du, ddt,
-                    dA, dB, dC, dD, db, dz, dh0, ws, n, stream)
+                    dA, dB, dC, dD, db, dz, dh0, ws, n, _stream_on(dev, stream))
     return {"du": du, "ddt": ddt, "dA": dA, "dB": dB, "dC": dC, "dDskip": dD, "ddt_bias": db,
             "dz": dz, "dh0": dh0}
 
@@ -843,10 +865,10 @@ def scan_step(state, u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, soft
     d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, step=True)
     _whole(fn, (u.shape[0], u.shape[1], A.shape[1]), torch.float32, dev, state=state)
     _whole(fn, u.shape, u.dtype, dev, y=y)
-    with _on(dev, stream):
+    with _on(dev):
         if y is None:
             y = torch.empty(u.shape, dtype=u.dtype, device=dev)
-        lz_scan_step(d, state, u, dt, A, Bm, Cm, Dskip, z, dt_bias, y, stream)
+        lz_scan_step(d, state, u, dt, A, Bm, Cm, Dskip, z, dt_bias, y, _stream_on(dev, stream))
     return y
 
 
@@ -878,10 +900,10 @@ def block_norm_fwd(o, *, w=None, z=None, s=None, r=None, w2=None, groups=1, eps=
     fn, dev = "block_norm_fwd", o.device
     d = _norm_args(fn, o, z, r, groups, eps)
     _whole(fn, (d.D,), torch.float32, dev, w=w, s=s, w2=w2)
-    with _on(dev, stream):
+    with _on(dev):
         out = torch.empty(d.B, d.T, d.D, dtype=o.dtype, device=dev)
         n = torch.empty_like(out) if w2 is not None else None
-        lz_block_norm_fwd(d, o, w, z, s, r, w2, out, n, stream)
+        lz_block_norm_fwd(d, o, w, z, s, r, w2, out, n, _stream_on(dev, stream))
     return out, n
 
 
@@ -896,7 +918,7 @@ def block_norm_bwd(o, *, w=None, z=None, s=None, w2=None, out=None, dout=None, d
     _whole(fn, (d.B, d.T, d.D), o.dtype, dev, out=out, dout=dout, dn=dn)
     _need(dout is not None or dn is not None, fn, "dout or dn must be given")
     _need(dn is None or (out is not None and w2 is not None), fn, "dn needs out and w2")
-    with _on(dev, stream):
+    with _on(dev):
         rows = lambda: torch.empty(d.B, d.T, d.D, dtype=o.dtype, device=dev)
         par = lambda on: torch.empty(d.D, dtype=torch.float32, device=dev) if on else None
         do = torch.empty(o.shape, dtype=o.dtype, device=dev)
@@ -905,5 +927,6 @@ def block_norm_bwd(o, *, w=None, z=None, s=None, w2=None, out=None, dout=None, d
         dw, ds, dw2 = par(w is not None), par(s is not None), par(dn is not None)
         n = lz_layer_workspace_bytes(d, LZ_WS_NORM_BWD)
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        lz_block_norm_bwd(d, o, w, z, s, w2, out, dout, dn, do, dz, dr, dw, ds, dw2, ws, n, stream)
+        lz_block_norm_bwd(d, o, w, z, s, w2, out, dout, dn, do, dz, dr, dw, ds, dw2, ws, n,
+                          _stream_on(dev, stream))
     return {"do": do, "dz": dz, "dr": dr, "dw": dw, "ds": ds, "dw2": dw2}

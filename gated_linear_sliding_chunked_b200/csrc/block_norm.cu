@@ -4,11 +4,12 @@
 // A row of D features stays in registers between its two norms: every input
 // is read once and every output written once, a few operations an element, so
 // HBM bandwidth bounds it (forward up to 5 values an element, backward up to
-// 8).  A thread holds E = 16 (backward of up to 4096 features: 8) elements; up
+// 8).  A thread holds E = 8 or 16 elements; up
 // to 512 elements a row belongs to one warp (no block-wide synchronisation),
-// longer rows to a block.  Blocks walk the rows with a stride: the next row's
-// loads are in flight while this one is worked on, and the backward's
-// parameter gradients stay in registers and leave as one partial per block.
+// longer rows to a block.  The forward takes a row a block; the backward's
+// blocks walk the rows with a stride, the next row's loads in flight while this
+// one is worked on, so that the parameter gradients stay in registers and leave
+// as one partial per block.
 #include "layer.cuh"
 
 namespace lz {
@@ -45,16 +46,37 @@ struct NormParams {
   float* part;  // [blocks][3][D]: dw, ds, dw2
 };
 
-// Sum over the team that holds a row: its warp, or its block
-template <bool WARP>
-__device__ __forceinline__ float team_sum(float v, float* red) {
-  v = warp_sum(v);
-  if constexpr (WARP) return v;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
-  __syncthreads();  // the previous sum's readers are done
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  return warp_sum(lane < nw ? red[lane] : 0.f);
+// Sums of M values over the team that holds a row: its warp, or its block.  One
+// barrier: a caller alternates between two `red` of M * 32 floats, so that a
+// buffer is written again only after a barrier that its readers have passed.
+template <bool WARP, int M>
+__device__ __forceinline__ void team_sum(float (&v)[M], float* red) {
+#pragma unroll
+  for (int i = 0; i < M; ++i) v[i] = warp_sum(v[i]);
+  if constexpr (!WARP) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
+    if (lane < M) {
+      float x = v[0];
+#pragma unroll
+      for (int i = 1; i < M; ++i) x = lane == i ? v[i] : x;
+      red[lane * 32 + warp] = x;
+    }
+    __syncthreads();
+    // every thread adds the warps' shares, 4 at a time (those that are not there
+    // are left out)
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      float s = 0.f;
+      for (int w = 0; w < nw; w += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(red + i * 32 + w);
+        s += q.x;
+        if (w + 1 < nw) s += q.y;
+        if (w + 2 < nw) s += q.z;
+        if (w + 3 < nw) s += q.w;
+      }
+      v[i] = s;
+    }
+  }
 }
 
 // Per-vector partial sums ps[k] -> the sum over each vector's group
@@ -64,12 +86,12 @@ __device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int la
   constexpr int NV = E / VW;
   const int nvec = p.D / VW;
   if constexpr (MODE == GROUP_ROW) {
-    float a = 0.f;
+    float a[1] = {0.f};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) a += ps[k];
-    a = team_sum<WARP>(a, red);
+    for (int k = 0; k < NV; ++k) a[0] += ps[k];
+    team_sum<WARP>(a, red);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) ps[k] = a;
+    for (int k = 0; k < NV; ++k) ps[k] = a[0];
   } else if constexpr (MODE == GROUP_LANES) {
     const int gv = nvec / p.G;  // lanes of a group: 1, 2, .. 32
 #pragma unroll
@@ -111,104 +133,95 @@ __device__ __forceinline__ size_t o_at(const NormParams& p, const Rows& so, int 
 template <typename IO, int E, int VW, bool WARP, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
   extern __shared__ float sm[];
-  __shared__ float red[32];
+  __shared__ __align__(16) float red[2][3 * 32];
   constexpr int NV = E / VW;
   const int team = WARP ? 32 : blockDim.x;
   const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
   const int nvec = p.D / VW;
-  const int64_t row0 = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-  const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
-  struct In {
-    Raw<IO, VW> o[NV], z[NV], r[NV];
-  };
-  auto fetch = [&](int64_t row, In& in) {
-    const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
+  const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  if (row >= p.rows) return;
+  const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
+  Raw<IO, VW> ro[NV], rz[NV], rr[NV];  // the row, all of it in flight at once
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = k * team + lane, c = v * VW;
-      const bool on = v < nvec;
-      in.o[k].load_if((const IO*)p.o + o_at(p, p.so, b, t, c), on);
-      if (p.z) in.z[k].load_if((const IO*)p.z + p.sz.at(b, t) + c, on);
-      if (p.r) in.r[k].load_if((const IO*)p.r + p.sr.at(b, t) + c, on);
+  for (int k = 0; k < NV; ++k) {
+    const int v = k * team + lane, c = v * VW;
+    const bool on = v < nvec;
+    ro[k].load_if((const IO*)p.o + o_at(p, p.so, b, t, c), on);
+    if (p.z) rz[k].load_if((const IO*)p.z + p.sz.at(b, t) + c, on);
+    if (p.r) rr[k].load_if((const IO*)p.r + p.sr.at(b, t) + c, on);
+  }
+  float x[E], ps[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    ps[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      x[k * VW + e] = ro[k].get(e);
+      ps[k] = fmaf(x[k * VW + e], x[k * VW + e], ps[k]);
     }
-  };
-  In nx;
-  if (row0 < p.rows) fetch(row0, nx);
-  for (int64_t row = row0; row < p.rows; row += step) {
-    const In in = nx;
-    if (row + step < p.rows) fetch(row + step, nx);
-    float x[E], ps[NV];
+  }
+  if (p.w) {
+    group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red[0], sm);
+    const float ig = (float)p.G / (float)p.D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      ps[k] = 0.f;
+      const float rs = rsqrtf(ps[k] * ig + p.eps);
+      const int v = k * team + lane;
+      if (v < nvec) {
+        float w[VW];
+        load_floats<VW>(p.w + v * VW, w);
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        x[k * VW + e] = in.o[k].get(e);
-        ps[k] = fmaf(x[k * VW + e], x[k * VW + e], ps[k]);
+        for (int e = 0; e < VW; ++e) x[k * VW + e] *= rs * w[e];
       }
     }
-    if (p.w) {
-      group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red, sm);
-      const float ig = (float)p.G / (float)p.D;
+  }
+  float ss[1] = {0.f};
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const float rs = rsqrtf(ps[k] * ig + p.eps);
-        const int v = k * team + lane;
-        if (v < nvec) {
-          float w[VW];
-          load_floats<VW>(p.w + v * VW, w);
+  for (int k = 0; k < NV; ++k) {
+    const int v = k * team + lane;
+    if (v < nvec) {
+      const int c = v * VW;
+      float* xv = x + k * VW;
+      if (p.z) {
 #pragma unroll
-          for (int e = 0; e < VW; ++e) x[k * VW + e] *= rs * w[e];
+        for (int e = 0; e < VW; ++e) {
+          const float z = rz[k].get(e);
+          xv[e] *= z * sigmoid(z);
         }
       }
+      if (p.s) {
+        float s[VW];
+        load_floats<VW>(p.s + c, s);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) xv[e] *= s[e];
+      }
+      if (p.r) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) xv[e] += rr[k].get(e);
+      }
+      store_vec<VW>((IO*)p.out + (size_t)row * p.D + c, xv);
+      // the second norm is that of the stored stream, so that the backward
+      // finds the same values in it
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        xv[e] = to_f(from_f<IO>(xv[e]));
+        ss[0] = fmaf(xv[e], xv[e], ss[0]);
+      }
     }
-    float ss = 0.f;
+  }
+  if (p.w2) {
+    team_sum<WARP>(ss, red[1]);
+    const float rs = rsqrtf(ss[0] / (float)p.D + p.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = k * team + lane;
       if (v < nvec) {
-        const int c = v * VW;
         float* xv = x + k * VW;
-        if (p.z) {
+        float w[VW];
+        load_floats<VW>(p.w2 + v * VW, w);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            const float z = in.z[k].get(e);
-            xv[e] *= z * sigmoid(z);
-          }
-        }
-        if (p.s) {
-          float s[VW];
-          load_floats<VW>(p.s + c, s);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) xv[e] *= s[e];
-        }
-        if (p.r) {
-#pragma unroll
-          for (int e = 0; e < VW; ++e) xv[e] += in.r[k].get(e);
-        }
-        store_vec<VW>((IO*)p.out + (size_t)row * p.D + c, xv);
-        // the second norm is that of the stored stream, so that the backward
-        // finds the same values in it
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          xv[e] = to_f(from_f<IO>(xv[e]));
-          ss = fmaf(xv[e], xv[e], ss);
-        }
-      }
-    }
-    if (p.w2) {
-      const float rs = rsqrtf(team_sum<WARP>(ss, red) / (float)p.D + p.eps);
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int v = k * team + lane;
-        if (v < nvec) {
-          float* xv = x + k * VW;
-          float w[VW];
-          load_floats<VW>(p.w2 + v * VW, w);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) xv[e] *= rs * w[e];
-          store_vec<VW>((IO*)p.n + (size_t)row * p.D + v * VW, xv);
-        }
+        for (int e = 0; e < VW; ++e) xv[e] *= rs * w[e];
+        store_vec<VW>((IO*)p.n + (size_t)row * p.D + v * VW, xv);
       }
     }
   }
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
 template <typename IO, int E, int VW, bool WARP, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
   extern __shared__ float sm[];
-  __shared__ float red[32];
+  __shared__ __align__(16) float red[2][3 * 32];
   constexpr int NV = E / VW;
   const int team = WARP ? 32 : blockDim.x;
   const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
@@ -253,6 +266,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
       if (p.z) in.z[k].load_if((const IO*)p.z + p.sz.at(b, t) + c, on);
     }
   };
+  int turn = 0;  // of the two buffers of the block's sums
   In nx;
   if (row0 < p.rows) fetch(row0, nx);
   for (int64_t row = row0; row < p.rows; row += step) {
@@ -269,34 +283,53 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
         e[k * VW + j] = p.dout ? in.dout[k].get(j) : 0.f;
       }
     }
+    // first sums: of out^2, of q out and (one group) of o^2
+    float sums[3] = {0.f, 0.f, 0.f};
     if (p.dn) {
-      float ss = 0.f, qx = 0.f;
-      float w2[E];
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int v = k * team + lane;
         if (v < nvec) {
-          load_floats<VW>(p.w2 + v * VW, w2 + k * VW);
+          float w2[VW];
+          load_floats<VW>(p.w2 + v * VW, w2);
 #pragma unroll
           for (int j = 0; j < VW; ++j) {
             const float xo = in.out[k].get(j);
-            ss = fmaf(xo, xo, ss);
-            qx = fmaf(in.dn[k].get(j) * w2[k * VW + j], xo, qx);
+            sums[0] = fmaf(xo, xo, sums[0]);
+            sums[1] = fmaf(in.dn[k].get(j) * w2[j], xo, sums[1]);
           }
         }
       }
-      const float r2 = rsqrtf(team_sum<WARP>(ss, red) * id + p.eps);
-      const float m = team_sum<WARP>(qx, red) * id * r2 * r2;
+    }
+    if constexpr (MODE == GROUP_ROW) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) sums[2] += ps[k];
+    }
+    if (p.dn || (MODE == GROUP_ROW && p.w)) {
+      team_sum<WARP>(sums, red[turn]);
+      turn ^= 1;
+    }
+    if constexpr (MODE == GROUP_ROW) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) ps[k] = sums[2];
+    } else {
+      if (p.w) group_sum<E, VW, WARP, MODE>(p, ps, lane, team, nullptr, sm);
+    }
+    if (p.dn) {
+      const float r2 = rsqrtf(sums[0] * id + p.eps);
+      const float m = sums[1] * id * r2 * r2;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int v = k * team + lane;
         if (v < nvec) {
+          float w2[VW];
+          load_floats<VW>(p.w2 + v * VW, w2);
 #pragma unroll
           for (int j = 0; j < VW; ++j) {
             const int i = k * VW + j;
             const float xo = in.out[k].get(j), dn = in.dn[k].get(j);
             dw2[i] = fmaf(dn * r2, xo, dw2[i]);
-            e[i] += r2 * (dn * w2[i] - xo * m);
+            e[i] += r2 * (dn * w2[j] - xo * m);
           }
         }
       }
@@ -308,7 +341,6 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
         if (v < nvec) store_vec<VW>((IO*)p.dr + (size_t)row * p.D + v * VW, e + k * VW);
       }
     }
-    if (p.w) group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red, sm);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = k * team + lane;
@@ -351,7 +383,10 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
         }
       }
     }
-    if (p.w) group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red, sm);
+    if (p.w) {
+      group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red[turn], sm);
+      turn ^= MODE == GROUP_ROW;
+    }
     const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -435,17 +470,12 @@ int grid_rows(Kern k, int64_t rows, int threads, size_t smem, int rows_per_block
 
 template <typename IO, int E, int VW, bool WARP, int MODE>
 cudaError_t go_fwd(const NormParams& p, const Shape& sh, cudaStream_t s) {
-  constexpr int kT = WARP ? kRowWarps * 32 : 512;
-  // rows of more than 8192 features need blocks of up to 1024 threads
-  auto k = norm_fwd_kernel<IO, E, VW, WARP, MODE, kT>;
-  if constexpr (!WARP && E == 16) {
-    if (sh.threads > kT) k = norm_fwd_kernel<IO, E, VW, WARP, MODE, 1024>;
-  }
+  auto k = norm_fwd_kernel<IO, E, VW, WARP, MODE, WARP ? kRowWarps * 32 : 1024>;
   if (sh.smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
     if (e != cudaSuccess) return e;
   }
-  const int grid = grid_rows(k, p.rows, sh.threads, sh.smem, WARP ? kRowWarps : 1);
+  const unsigned grid = (unsigned)(WARP ? (p.rows + kRowWarps - 1) / kRowWarps : p.rows);
   ScopedTiming tm("block_norm_fwd", s);
   k<<<grid, sh.threads, sh.smem, s>>>(p);
   return cudaGetLastError();
@@ -549,9 +579,14 @@ extern "C" lz_status lz_block_norm_fwd(const lz_norm_dims* d, const void* o, con
   p.sz = rows_of(d->z, d->T, d->D);
   p.sr = rows_of(d->r, d->T, d->D);
   p.o = o; p.w = w; p.z = z; p.s = s; p.r = r; p.w2 = w2; p.out = out; p.n = n;
-  const Shape sh = shape_of(d, norm_vec(d, p), 16);
+  // 8 elements a thread, four blocks of 512 on an SM at 4096 features: the
+  // loads of 2048 threads in flight.  Very long rows take 16.
+  const bool narrow = d->D > kWarpD && d->D <= 8192;
+  const Shape sh = shape_of(d, norm_vec(d, p), narrow ? 8 : 16);
   cudaError_t e = cudaSuccess;
-#define LZ_CALL(IO, VW, WARP, MODE) go_fwd<IO, 16, VW, WARP, MODE>(p, sh, (cudaStream_t)stream)
+#define LZ_CALL(IO, VW, WARP, MODE)                                                 \
+  (narrow && !sh.warp ? go_fwd<IO, 8, VW, false, MODE>(p, sh, (cudaStream_t)stream) \
+                      : go_fwd<IO, 16, VW, WARP, MODE>(p, sh, (cudaStream_t)stream))
   LZ_NORM_DISPATCH(LZ_CALL);
 #undef LZ_CALL
   return layer_done(e, fn);

@@ -209,15 +209,26 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) 
         for (int e = 0; e < VW; ++e) xw[j][e] = g[j].get(e);
     }
     // s walks the tokens whose dp is formed; dx of token s - (K-1) is then complete
-    for (int s0 = t0; s0 < t1 + K - 1; s0 += RT) {
+    const int send = t1 + K - 1, slive = min(send, L);
+    Raw<IO, VW> nx[RT], ndy[RT];
+    auto fetch = [&](int s0) {
+      const IO* px = (const IO*)p.px + p.x.at(b, s0) + c;
+      const IO* pdy = (const IO*)q.dy + ((size_t)b * p.T + s0) * p.D + c;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        nx[i].load_if(px + i * p.x.ld, s0 + i < slive);
+        ndy[i].load_if(pdy + (size_t)i * p.D, s0 + i < slive);
+      }
+    };
+    fetch(t0);
+    for (int s0 = t0; s0 < send; s0 += RT) {
       Raw<IO, VW> xv[RT], dyv[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const int s = s0 + i;
-        const bool live = s < t1 + K - 1 && s < L;
-        xv[i].load_if((const IO*)p.px + p.x.at(b, s) + c, live);
-        dyv[i].load_if((const IO*)q.dy + ((size_t)b * p.T + s) * p.D + c, live);
+        xv[i] = nx[i];
+        dyv[i] = ndy[i];
       }
+      if (s0 + RT < send) fetch(s0 + RT);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         const int s = s0 + i, t = s - (K - 1);

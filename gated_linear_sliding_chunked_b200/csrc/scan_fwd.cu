@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p, f
   if (on) A = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0));
   if (row && p.dtb) bias = p.dtb[c];
   if (row && p.Dskip) Ds = p.Dskip[c];
-  for (int b0 = blockIdx.y; b0 < p.B; b0 += 2 * gridDim.y) {
+  const int b0 = blockIdx.y;
+  {
     float4 h[2];
     Pack<IO, 4> B4[2], C4[2];
     float u[2], d[2], z[2];
@@ -404,8 +405,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p, f
 template <typename IO, int L>
 cudaError_t go_step(const ScanParams& p, float* state, cudaStream_t s) {
   const int gx = (int)(((size_t)p.D * L + kStepThreads - 1) / kStepThreads);
-  // pairs of sequences, as many blocks as the device holds
-  const int gy = std::max(1, std::min((p.B + 1) / 2, std::max(1, 148 * 8 / gx)));
+  const int gy = (p.B + 1) / 2;
   ScopedTiming tm("scan_step", s);
   scan_step_kernel<IO, L><<<dim3(gx, gy), kStepThreads, 0, s>>>(p, state);
   return cudaGetLastError();
