@@ -4,7 +4,7 @@
 // A row of D features stays in registers between its two norms: every input
 // is read once and every output written once, a few operations an element, so
 // HBM bandwidth bounds it (forward up to 5 values an element, backward up to
-// 8).  A thread holds E = 8 or 16 elements; up
+// 8).  A thread holds E = 16 elements; up
 // to 512 elements a row belongs to one warp (no block-wide synchronisation),
 // longer rows to a block.  The forward takes a row a block; the backward's
 // blocks walk the rows with a stride, the next row's loads in flight while this
@@ -15,9 +15,16 @@
 namespace lz {
 namespace {
 
-constexpr int kMaxD = 16384;  // 16 elements a thread, 1024 threads
+constexpr int E = 16;         // elements of a thread
+constexpr int kMaxD = 16384;  // 1024 threads
 constexpr int kWarpD = 512;   // rows of a warp: 16 elements a lane
 constexpr int kRowWarps = 4;  // rows of a block of one-warp rows
+
+inline int shift_of(int n) {
+  int s = 0;
+  while ((1 << s) < n) ++s;
+  return (1 << s) == n ? s : -1;
+}
 
 // How the sums over a group of features are formed: the group is the whole
 // row; a power-of-two number of neighbouring lanes; anything else (partial
@@ -26,7 +33,8 @@ enum { GROUP_ROW = 0, GROUP_LANES = 1, GROUP_SMEM = 2 };
 
 struct NormParams {
   int64_t rows;
-  int T, D, G, heads;
+  int B, T, D, G, heads;
+  int dshift;  // log2 of the features of a group, -1 when that is no power of two
   float eps;
   Rows so, sz, sr;
   const void* o;
@@ -62,25 +70,13 @@ __device__ __forceinline__ void team_sum(float (&v)[M], float* red) {
       red[lane * 32 + warp] = x;
     }
     __syncthreads();
-    // every thread adds the warps' shares, 4 at a time (those that are not there
-    // are left out)
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      float s = 0.f;
-      for (int w = 0; w < nw; w += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(red + i * 32 + w);
-        s += q.x;
-        if (w + 1 < nw) s += q.y;
-        if (w + 2 < nw) s += q.z;
-        if (w + 3 < nw) s += q.w;
-      }
-      v[i] = s;
-    }
+    for (int i = 0; i < M; ++i) v[i] = warp_sum(lane < nw ? red[i * 32 + lane] : 0.f);
   }
 }
 
 // Per-vector partial sums ps[k] -> the sum over each vector's group
-template <int E, int VW, bool WARP, int MODE>
+template <int VW, bool WARP, int MODE>
 __device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int lane, int team, float* red,
                                           float* sm) {
   constexpr int NV = E / VW;
@@ -126,21 +122,21 @@ __device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int la
 // when it has o's layout)
 __device__ __forceinline__ size_t o_at(const NormParams& p, const Rows& so, int b, int t, int c) {
   if (!p.heads) return so.at(b, t) + c;
-  const int dv = p.D / p.G, g = c / dv;
+  const int dv = p.D / p.G, g = p.dshift >= 0 ? c >> p.dshift : c / dv;
   return (((size_t)b * p.G + g) * p.T + t) * dv + (c - g * dv);
 }
 
-template <typename IO, int E, int VW, bool WARP, int MODE, int MAXT>
+template <typename IO, int VW, bool WARP, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
   extern __shared__ float sm[];
-  __shared__ __align__(16) float red[2][3 * 32];
+  __shared__ float red[2][3 * 32];
   constexpr int NV = E / VW;
   const int team = WARP ? 32 : blockDim.x;
   const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
   const int nvec = p.D / VW;
-  const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-  if (row >= p.rows) return;
-  const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
+  const int b = blockIdx.y, t = WARP ? blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  if (t >= p.T) return;
+  const int64_t row = (int64_t)b * p.T + t;
   Raw<IO, VW> ro[NV], rz[NV], rr[NV];  // the row, all of it in flight at once
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -161,7 +157,7 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
     }
   }
   if (p.w) {
-    group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red[0], sm);
+    group_sum<VW, WARP, MODE>(p, ps, lane, team, red[0], sm);
     const float ig = (float)p.G / (float)p.D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -232,10 +228,10 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
 // and with mh = o rs, core = mh w, f = e s:
 //   ds = sum e core silu(z)     dz = f core silu'(z)     dw = sum f silu(z) mh
 //   do = rs (k - mh mean_group(k mh)),  k = f silu(z) w
-template <typename IO, int E, int VW, bool WARP, int MODE, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
+template <typename IO, int VW, bool WARP, int MODE, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(NormParams p) {
   extern __shared__ float sm[];
-  __shared__ __align__(16) float red[2][3 * 32];
+  __shared__ float red[2][3 * 32];
   constexpr int NV = E / VW;
   const int team = WARP ? 32 : blockDim.x;
   const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
@@ -244,9 +240,10 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
   const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
   const float ig = (float)p.G / (float)p.D, id = 1.f / (float)p.D;
   const Rows cont{p.D, (int64_t)p.T * p.D};
-  float dw[E], ds[E], dw2[E];
+  // sum over the rows of e silu(z) mh: times s it is dw, times w ds
+  float sm0[E], dw2[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i) dw[i] = ds[i] = dw2[i] = 0.f;
+  for (int i = 0; i < E; ++i) sm0[i] = dw2[i] = 0.f;
   struct In {
     Raw<IO, VW> o[NV], z[NV], out[NV], dout[NV], dn[NV];
   };
@@ -313,7 +310,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) ps[k] = sums[2];
     } else {
-      if (p.w) group_sum<E, VW, WARP, MODE>(p, ps, lane, team, nullptr, sm);
+      if (p.w) group_sum<VW, WARP, MODE>(p, ps, lane, team, nullptr, sm);
     }
     if (p.dn) {
       const float r2 = rsqrtf(sums[0] * id + p.eps);
@@ -353,38 +350,32 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
         for (int j = 0; j < VW; ++j) wv[j] = sv[j] = 1.f;
         if (p.w) load_floats<VW>(p.w + c, wv);
         if (p.s) load_floats<VW>(p.s + c, sv);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          x[k * VW + j] *= rs[k];  // mh
+          wv[j] *= sv[j];
+        }
         if (p.z) {
 #pragma unroll
           for (int j = 0; j < VW; ++j) {
             const int i = k * VW + j;
-            x[i] *= rs[k];  // mh
-            const float core = x[i] * wv[j], f = e[i] * sv[j];
             const float z = in.z[k].get(j), sg = sigmoid(z), si = z * sg;
-            dz[j] = f * core * fmaf(-si, sg, sg + si);
-            ds[i] = fmaf(e[i] * core, si, ds[i]);
-            e[i] = f * si;
+            dz[j] = e[i] * x[i] * wv[j] * fmaf(-si, sg, sg + si);
+            e[i] *= si;
           }
           if (p.dz) store_vec<VW>((IO*)p.dz + (size_t)row * p.D + c, dz);
-        } else {
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            const int i = k * VW + j;
-            x[i] *= rs[k];
-            ds[i] = fmaf(e[i], x[i] * wv[j], ds[i]);
-            e[i] *= sv[j];
-          }
         }
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
           const int i = k * VW + j;
-          dw[i] = fmaf(e[i], x[i], dw[i]);
+          sm0[i] = fmaf(e[i], x[i], sm0[i]);
           e[i] *= wv[j];  // the gradient at mh
           ps[k] = fmaf(e[i], x[i], ps[k]);
         }
       }
     }
     if (p.w) {
-      group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red[turn], sm);
+      group_sum<VW, WARP, MODE>(p, ps, lane, team, red[turn], sm);
       turn ^= MODE == GROUP_ROW;
     }
     const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
@@ -403,9 +394,13 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
   }
   // ---- the block's partials; the warps of a warp-per-row block are added in
   // order in shared memory
+  auto value = [&](int q, int i, int c) {
+    const float a = q == 2 ? dw2[i] : sm0[i];
+    const float* f = q == 0 ? p.s : q == 1 ? p.w : nullptr;
+    return f ? a * f[c] : a;
+  };
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    const float* a = q == 0 ? dw : q == 1 ? ds : dw2;
     float* part = p.part + ((size_t)blockIdx.x * 3 + q) * p.D;
     if constexpr (WARP) {
       const int warp = threadIdx.x / 32, nw = blockDim.x / 32;
@@ -413,7 +408,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const int c = (i / VW * 32 + lane) * VW + i % VW;
-        if (c < p.D) sm[warp * p.D + c] = a[i];
+        if (c < p.D) sm[warp * p.D + c] = value(q, i, c);
       }
       __syncthreads();
       for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
@@ -427,7 +422,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormParams p) {
         const int v = k * team + lane;
         if (v < nvec) {
 #pragma unroll
-          for (int j = 0; j < VW; ++j) part[v * VW + j] = a[k * VW + j];
+          for (int j = 0; j < VW; ++j) part[v * VW + j] = value(q, k * VW + j, v * VW + j);
         }
       }
     }
@@ -442,8 +437,7 @@ struct Shape {
   size_t smem;  // of the group sums
 };
 
-// E: elements of a thread
-Shape shape_of(const lz_norm_dims* d, bool vec, int E) {
+Shape shape_of(const lz_norm_dims* d, bool vec) {
   Shape s;
   s.vec = vec;
   s.vw = vec ? (int)(16 / esize(d->io)) : 1;
@@ -468,14 +462,14 @@ int grid_rows(Kern k, int64_t rows, int threads, size_t smem, int rows_per_block
   return (int)std::max<int64_t>(1, std::min<int64_t>(want, wave));
 }
 
-template <typename IO, int E, int VW, bool WARP, int MODE>
+template <typename IO, int VW, bool WARP, int MODE>
 cudaError_t go_fwd(const NormParams& p, const Shape& sh, cudaStream_t s) {
-  auto k = norm_fwd_kernel<IO, E, VW, WARP, MODE, WARP ? kRowWarps * 32 : 1024>;
+  auto k = norm_fwd_kernel<IO, VW, WARP, MODE, WARP ? kRowWarps * 32 : 1024>;
   if (sh.smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
     if (e != cudaSuccess) return e;
   }
-  const unsigned grid = (unsigned)(WARP ? (p.rows + kRowWarps - 1) / kRowWarps : p.rows);
+  const dim3 grid(WARP ? (p.T + kRowWarps - 1) / kRowWarps : p.T, p.B);
   ScopedTiming tm("block_norm_fwd", s);
   k<<<grid, sh.threads, sh.smem, s>>>(p);
   return cudaGetLastError();
@@ -485,13 +479,14 @@ cudaError_t go_fwd(const NormParams& p, const Shape& sh, cudaStream_t s) {
 constexpr int kMaxBlocks = 148 * 8;
 int bwd_part_rows(int64_t rows) { return (int)std::min<int64_t>(std::max<int64_t>(rows, 1), kMaxBlocks); }
 
-template <typename IO, int E, int VW, bool WARP, int MODE>
+template <typename IO, int VW, bool WARP, int MODE>
 cudaError_t go_bwd(const NormParams& p, const Shape& sh, int* blocks, cudaStream_t s) {
-  constexpr int kT = WARP ? kRowWarps * 32 : 512;
-  // rows of more than 8192 features need blocks of up to 1024 threads
-  auto k = norm_bwd_kernel<IO, E, VW, WARP, MODE, kT>;
-  if constexpr (!WARP && E == 16) {
-    if (sh.threads > kT) k = norm_bwd_kernel<IO, E, VW, WARP, MODE, 1024>;
+  // two blocks an SM up to 4096 features, so that one works while the other
+  // waits for its sums; longer rows need blocks of up to 1024 threads
+  auto k = norm_bwd_kernel<IO, VW, WARP, MODE, WARP ? kRowWarps * 32 : 256>;
+  if constexpr (!WARP) {
+    if (sh.threads > 256) k = norm_bwd_kernel<IO, VW, WARP, MODE, 512>;
+    if (sh.threads > 512) k = norm_bwd_kernel<IO, VW, WARP, MODE, 1024>;
   }
   const size_t smem = WARP ? std::max(sh.smem, (size_t)kRowWarps * p.D * sizeof(float)) : sh.smem;
   if (smem > 48 * 1024) {
@@ -533,8 +528,8 @@ lz_status check_norm(const char* fn, const lz_norm_dims* d) {
     return layer_fail(LZ_ERR_INVALID_ARG, "%s: heads must be 0 or 1 (got %d)", fn, d->heads);
   if (!(d->eps > 0.f && d->eps < 3.0e38f))
     return layer_fail(LZ_ERR_INVALID_ARG, "%s: eps must be finite and > 0", fn);
-  if ((int64_t)d->B * d->T >= (int64_t(1) << 31))
-    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: B * T must be below 2^31", fn);
+  if (d->B > 65535 || (int64_t)d->B * d->T >= (int64_t(1) << 31))
+    return layer_fail(LZ_ERR_UNSUPPORTED, "%s: B must be <= 65535 and B * T below 2^31", fn);
   if (!rows_ok(d->o) || !rows_ok(d->z) || !rows_ok(d->r))
     return layer_fail(LZ_ERR_INVALID_ARG, "%s: bad row strides", fn);
   return LZ_OK;
@@ -574,19 +569,14 @@ extern "C" lz_status lz_block_norm_fwd(const lz_norm_dims* d, const void* o, con
   if (st != LZ_OK) return st;
   NormParams p{};
   p.rows = (int64_t)d->B * d->T;
-  p.T = d->T; p.D = d->D; p.G = d->G; p.heads = d->heads; p.eps = d->eps;
+  p.B = d->B; p.T = d->T; p.D = d->D; p.dshift = shift_of(d->D / d->G); p.G = d->G; p.heads = d->heads; p.eps = d->eps;
   p.so = rows_of(d->o, d->T, d->D);
   p.sz = rows_of(d->z, d->T, d->D);
   p.sr = rows_of(d->r, d->T, d->D);
   p.o = o; p.w = w; p.z = z; p.s = s; p.r = r; p.w2 = w2; p.out = out; p.n = n;
-  // 8 elements a thread, four blocks of 512 on an SM at 4096 features: the
-  // loads of 2048 threads in flight.  Very long rows take 16.
-  const bool narrow = d->D > kWarpD && d->D <= 8192;
-  const Shape sh = shape_of(d, norm_vec(d, p), narrow ? 8 : 16);
+  const Shape sh = shape_of(d, norm_vec(d, p));
   cudaError_t e = cudaSuccess;
-#define LZ_CALL(IO, VW, WARP, MODE)                                                 \
-  (narrow && !sh.warp ? go_fwd<IO, 8, VW, false, MODE>(p, sh, (cudaStream_t)stream) \
-                      : go_fwd<IO, 16, VW, WARP, MODE>(p, sh, (cudaStream_t)stream))
+#define LZ_CALL(IO, VW, WARP, MODE) go_fwd<IO, VW, WARP, MODE>(p, sh, (cudaStream_t)stream)
   LZ_NORM_DISPATCH(LZ_CALL);
 #undef LZ_CALL
   return layer_done(e, fn);
@@ -616,20 +606,15 @@ extern "C" lz_status lz_block_norm_bwd(const lz_norm_dims* d, const void* o, con
     return layer_fail(LZ_ERR_INVALID_ARG, "%s: workspace too small (%zu bytes, need %zu)", fn, ws_bytes, need);
   NormParams p{};
   p.rows = rows;
-  p.T = std::max(d->T, 1); p.D = d->D; p.G = d->G; p.heads = d->heads; p.eps = d->eps;
+  p.B = d->B; p.T = std::max(d->T, 1); p.D = d->D; p.dshift = shift_of(d->D / d->G); p.G = d->G; p.heads = d->heads; p.eps = d->eps;
   p.so = rows_of(d->o, d->T, d->D);
   p.sz = rows_of(d->z, d->T, d->D);
   p.o = o; p.w = w; p.z = z; p.s = s; p.w2 = w2; p.out = const_cast<void*>(out);
   p.dout = dout; p.dn = dn; p.d_o = dOo; p.dz = dz; p.dr = dr; p.part = (float*)ws;
-  // 8 elements a thread leave room for the next row's loads beside the
-  // parameter gradients, up to the 512 threads that 128 registers allow
-  const bool narrow = d->D > kWarpD && d->D <= 4096;
-  const Shape sh = shape_of(d, norm_vec(d, p), narrow ? 8 : 16);
+  const Shape sh = shape_of(d, norm_vec(d, p));
   cudaError_t e = cudaSuccess;
   int blocks = 0;
-#define LZ_CALL(IO, VW, WARP, MODE)                                                          \
-  (narrow && !sh.warp ? go_bwd<IO, 8, VW, false, MODE>(p, sh, &blocks, (cudaStream_t)stream) \
-                      : go_bwd<IO, 16, VW, WARP, MODE>(p, sh, &blocks, (cudaStream_t)stream))
+#define LZ_CALL(IO, VW, WARP, MODE) go_bwd<IO, VW, WARP, MODE>(p, sh, &blocks, (cudaStream_t)stream)
   LZ_NORM_DISPATCH(LZ_CALL);
 #undef LZ_CALL
   if (e == cudaSuccess && (dw || ds || dw2))

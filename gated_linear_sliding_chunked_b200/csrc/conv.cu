@@ -6,6 +6,8 @@
 // vector of neighbouring channels and walks a run of tokens with the last K-1
 // inputs in registers, so that a token is read once and only the K-1 tokens
 // before a run are read twice (they come out of L2).
+#include <type_traits>
+
 #include "layer.cuh"
 
 namespace lz {
@@ -68,33 +70,37 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvParams p) {
   const int t0 = run * p.run, t1 = min(p.T, t0 + p.run), te = min(t1, L);
   IO* y = (IO*)p.y + ((size_t)b * p.T + t0) * p.D + c;
   const IO* x = (const IO*)p.px + p.x.at(b, t0) + c;
-  float w[K * VW], bias[VW], h[K > 1 ? K - 1 : 1][VW];
+  using V = Vec<VW>;
+  V w[K], bias, h[K > 1 ? K - 1 : 1];
   if (t0 < te) {
     Raw<IO, VW> v[RT], g[K > 1 ? K - 1 : 1];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) load_x<IO, K, VW>(p, b, t0 - (K - 1) + j, c, g[j]);
 #pragma unroll
     for (int i = 0; i < RT; ++i) v[i].load_if(x + i * p.x.ld, t0 + i < te);
-    load_taps<K, VW>(p, c, w, bias);
+    {
+      float wf[K * VW], bf[VW];
+      load_taps<K, VW>(p, c, wf, bf);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j)
+      for (int j = 0; j < K; ++j) w[j].set([&](int e) { return wf[e * K + j]; });
+      bias.set([&](int e) { return bf[e]; });
+    }
 #pragma unroll
-      for (int e = 0; e < VW; ++e) h[j][e] = g[j].get(e);
+    for (int j = 0; j < K - 1; ++j) h[j].set([&](int e) { return g[j].get(e); });
     for (int t = t0;;) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
+        V x, a;
+        x.set([&](int e) { return v[i].get(e); });
+        a.fma(w[K - 1], x, bias);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) a.fma(w[j], h[j], a);
+#pragma unroll
+        for (int j = 0; j + 1 < K - 1; ++j) h[j] = h[j + 1];
+        if (K > 1) h[K > 1 ? K - 2 : 0] = x;
         float o[VW];
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          const float xe = v[i].get(e);
-          float a = fmaf(w[e * K + K - 1], xe, bias[e]);
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) a = fmaf(w[e * K + j], h[j][e], a);
-#pragma unroll
-          for (int j = 0; j + 1 < K - 1; ++j) h[j][e] = h[j + 1][e];
-          if (K > 1) h[K - 2 < 0 ? 0 : K - 2][e] = xe;
-          o[e] = a;
-        }
+        for (int e = 0; e < VW; ++e) o[e] = a.get(e);
         if (p.silu) {
 #pragma unroll
           for (int e = 0; e < VW; ++e) o[e] *= sigmoid(o[e]);
@@ -179,6 +185,7 @@ template <typename IO, int K, int VW>
 __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) {
   __shared__ float red[kWarps][32 * VW];
   constexpr int KW = K > 1 ? K - 1 : 1;
+  using V = Vec<VW>;
   const ConvParams& p = q.f;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int b = blockIdx.z;
@@ -187,38 +194,110 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) 
   const int L = seq_len(p.lens, b, p.T);
   const int t0 = (blockIdx.y * kWarps + warp) * p.run, t1 = min(p.T, t0 + p.run);
   const bool first = t0 == 0 && q.dx0;
-  float w[K * VW], bias[VW], xw[KW][VW], dpw[KW][VW], dw[K][VW], db[VW];
+  V w[K], bias, xw[KW], dpw[KW], dw[K], db;
+  db.fill(0.f);
 #pragma unroll
-  for (int e = 0; e < VW; ++e) {
-    db[e] = 0.f;
+  for (int j = 0; j < K; ++j) dw[j].fill(0.f);
 #pragma unroll
-    for (int j = 0; j < K; ++j) dw[j][e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < KW; ++j) dpw[j][e] = xw[j][e] = 0.f;
+  for (int j = 0; j < KW; ++j) {
+    dpw[j].fill(0.f);
+    xw[j].fill(0.f);
   }
   if (on && (t0 < t1 || first)) {
-    load_taps<K, VW>(p, c, w, bias);
-    IO* dx = (IO*)q.dx + (size_t)b * p.T * p.D + c;
+    {
+      float wf[K * VW], bf[VW];
+      load_taps<K, VW>(p, c, wf, bf);
+#pragma unroll
+      for (int j = 0; j < K; ++j) w[j].set([&](int e) { return wf[e * K + j]; });
+      bias.set([&](int e) { return bf[e]; });
+    }
     if (t0 < L) {
       Raw<IO, VW> g[KW];
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) load_x<IO, K, VW>(p, b, t0 - (K - 1) + j, c, g[j]);
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) xw[j][e] = g[j].get(e);
+      for (int j = 0; j < K - 1; ++j) xw[j].set([&](int e) { return g[j].get(e); });
     }
-    // s walks the tokens whose dp is formed; dx of token s - (K-1) is then complete
+    // s walks the tokens whose dp is formed; dx of token s - (K-1) is then
+    // complete.  RT tokens at a time, the next ones' loads in flight.
     const int send = t1 + K - 1, slive = min(send, L);
+    // [t0 + RT, sin): whole chunks of this run's own tokens, all live, whose dx
+    // rows get nothing from the final history
+    const int sin = min(t1, q.dxT ? L : slive);
+    const IO* px = (const IO*)p.px + p.x.at(b, t0) + c;
+    const IO* pdy = (const IO*)q.dy + ((size_t)b * p.T + t0) * p.D + c;
+    IO* pdx = (IO*)q.dx + ((int64_t)b * p.T + t0 - (K - 1)) * p.D + c;  // (used from token t0 on)
     Raw<IO, VW> nx[RT], ndy[RT];
     auto fetch = [&](int s0) {
-      const IO* px = (const IO*)p.px + p.x.at(b, s0) + c;
-      const IO* pdy = (const IO*)q.dy + ((size_t)b * p.T + s0) * p.D + c;
+      if (s0 + RT <= slive) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          nx[i].load(px + i * p.x.ld);
+          ndy[i].load(pdy + (int64_t)i * p.D);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          nx[i].load_if(px + i * p.x.ld, s0 + i < slive);
+          ndy[i].load_if(pdy + (int64_t)i * p.D, s0 + i < slive);
+        }
+      }
+      px += RT * p.x.ld;
+      pdy += (int64_t)RT * p.D;
+    };
+    auto chunk = [&](int s0, const Raw<IO, VW> (&xv)[RT], const Raw<IO, VW> (&dyv)[RT], auto edge) {
+      constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        nx[i].load_if(px + i * p.x.ld, s0 + i < slive);
-        ndy[i].load_if(pdy + (size_t)i * p.D, s0 + i < slive);
+        const int s = s0 + i, t = s - (K - 1);
+        V x, a, dp, o;
+        x.set([&](int e) { return xv[i].get(e); });
+        if (p.silu) {
+          a.fma(w[K - 1], x, bias);
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) a.fma(w[j], xw[j], a);
+          // (dy is zero behind the end, and with it dp)
+          dp.set([&](int e) {
+            const float v = a.get(e), sg = sigmoid(v), vs = v * sg;
+            return dyv[i].get(e) * fmaf(-vs, sg, sg + vs);
+          });
+        } else {
+          dp.set([&](int e) { return dyv[i].get(e); });
+        }
+        if (!EDGE || s < t1) {  // (tokens of the next run are that run's own)
+          db.add(dp);
+          dw[K - 1].fma(dp, x, dw[K - 1]);
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) dw[j].fma(dp, xw[j], dw[j]);
+        }
+        // dx_t = sum_j w_j dp_{s-j}
+        o.mul(w[0], dp);
+#pragma unroll
+        for (int j = 1; j < K; ++j) o.fma(w[j], dpw[KW - j], o);
+#pragma unroll
+        for (int j = 0; j + 1 < K - 1; ++j) {
+          xw[j] = xw[j + 1];
+          dpw[j] = dpw[j + 1];
+        }
+        if (K > 1) {
+          xw[KW - 1] = x;
+          dpw[KW - 1] = dp;
+        }
+        if (!EDGE || (t < t1 && (t >= t0 || first))) {
+          float of[VW];
+#pragma unroll
+          for (int e = 0; e < VW; ++e) of[e] = o.get(e);
+          if (EDGE && q.dxT && t >= L - (K - 1) && t < L) {
+            float g[VW];  // token t is this row of the final history
+            load_vec<VW>((const IO*)q.dxT + ((size_t)b * (K - 1) + (t - (L - (K - 1)))) * p.D + c, g);
+#pragma unroll
+            for (int e = 0; e < VW; ++e) of[e] += g[e];
+          }
+          if (!EDGE || t >= 0) store_vec<VW>(pdx + (int64_t)i * p.D, of);
+          else store_vec<VW>((IO*)q.dx0 + ((size_t)b * (K - 1) + t + K - 1) * p.D + c, of);
+        }
       }
+      pdx += (int64_t)RT * p.D;
     };
     fetch(t0);
     for (int s0 = t0; s0 < send; s0 += RT) {
@@ -229,54 +308,8 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) 
         dyv[i] = ndy[i];
       }
       if (s0 + RT < send) fetch(s0 + RT);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int s = s0 + i, t = s - (K - 1);
-        float dp[VW], o[VW];
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          const float xe = xv[i].get(e);
-          float a = fmaf(w[e * K + K - 1], xe, bias[e]);
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) a = fmaf(w[e * K + j], xw[j][e], a);
-          // (dy is zero behind the end, and with it dp)
-          float g = dyv[i].get(e);
-          if (p.silu) {
-            const float sg = sigmoid(a), as = a * sg;
-            g *= fmaf(-as, sg, sg + as);
-          }
-          dp[e] = g;
-          const float own = s < t1 ? g : 0.f;  // tokens of the next run are its own
-          db[e] += own;
-          dw[K - 1][e] = fmaf(own, xe, dw[K - 1][e]);
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) dw[j][e] = fmaf(own, xw[j][e], dw[j][e]);
-          // dx_t = sum_j w_j dp_{s-j}
-          o[e] = w[e * K] * g;
-#pragma unroll
-          for (int j = 1; j < K; ++j) o[e] = fmaf(w[e * K + j], dpw[K - 1 - j][e], o[e]);
-#pragma unroll
-          for (int j = 0; j + 1 < K - 1; ++j) {
-            xw[j][e] = xw[j + 1][e];
-            dpw[j][e] = dpw[j + 1][e];
-          }
-          if (K > 1) {
-            xw[KW - 1][e] = xe;
-            dpw[KW - 1][e] = g;
-          }
-        }
-        if (t < t1 && (t >= t0 || first)) {
-          const int jT = t - (L - (K - 1));  // token t is row jT of the final history
-          if (q.dxT && jT >= 0 && t < L) {
-            float g[VW];
-            load_vec<VW>((const IO*)q.dxT + ((size_t)b * (K - 1) + jT) * p.D + c, g);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) o[e] += g[e];
-          }
-          if (t >= 0) store_vec<VW>(dx + (size_t)t * p.D, o);
-          else store_vec<VW>((IO*)q.dx0 + ((size_t)b * (K - 1) + t + K - 1) * p.D + c, o);
-        }
-      }
+      if (s0 > t0 && s0 + RT <= sin) chunk(s0, xv, dyv, std::false_type{});
+      else chunk(s0, xv, dyv, std::true_type{});
     }
   }
   // ---- the block's partial of dw, dbias: warps added in order
@@ -286,7 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) 
   for (int j = 0; j <= K; ++j) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VW; ++e) red[warp][lane * VW + e] = j < K ? dw[j < K ? j : 0][e] : db[e];
+    for (int e = 0; e < VW; ++e) red[warp][lane * VW + e] = j < K ? dw[j < K ? j : 0].get(e) : db.get(e);
     __syncthreads();
     for (int x = threadIdx.x; x < 32 * VW; x += kWarps * 32) {
       const int ch = blockIdx.x * 32 * VW + x;

@@ -21,6 +21,31 @@ struct Rows {
   __host__ __device__ size_t at(int b, int t) const { return (size_t)b * bs + (size_t)t * ld; }
 };
 
+// Pairs of fp32 values in 64-bit registers: one instruction for two lanes of
+// arithmetic (fma.rn.f32x2 and the like), rounded as the scalar ones.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pk(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float lo(f2 x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi(f2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // VW consecutive elements as floats (one 16- or 8-byte access, or one element)
 template <int VW>
 __device__ __forceinline__ void load_vec(const float* p, float* x) {
@@ -153,6 +178,45 @@ __device__ __forceinline__ void load_floats(const float* p, float* x) {
     for (int i = 0; i < N; ++i) x[i] = __ldg(p + i);
   }
 }
+
+// V floats in registers, as pairs where V is even
+template <int V>
+struct Vec {
+  f2 p[V / 2];
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? hi(p[i / 2]) : lo(p[i / 2]); }
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = pk(x, x);
+  }
+  template <typename F>
+  __device__ __forceinline__ void set(F f) {  // f(i): value i
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = pk(f(2 * i), f(2 * i + 1));
+  }
+  __device__ __forceinline__ void fma(const Vec& a, const Vec& b, const Vec& c) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = fma2(a.p[i], b.p[i], c.p[i]);
+  }
+  __device__ __forceinline__ void mul(const Vec& a, const Vec& b) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = mul2(a.p[i], b.p[i]);
+  }
+  __device__ __forceinline__ void add(const Vec& a) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = add2(p[i], a.p[i]);
+  }
+};
+template <>
+struct Vec<1> {
+  float x;
+  __device__ __forceinline__ float get(int) const { return x; }
+  __device__ __forceinline__ void fill(float v) { x = v; }
+  template <typename F>
+  __device__ __forceinline__ void set(F f) { x = f(0); }
+  __device__ __forceinline__ void fma(const Vec& a, const Vec& b, const Vec& c) { x = fmaf(a.x, b.x, c.x); }
+  __device__ __forceinline__ void mul(const Vec& a, const Vec& b) { x = a.x * b.x; }
+  __device__ __forceinline__ void add(const Vec& a) { x += a.x; }
+};
 
 // Tokens of sequence b (lens nullable, clamped to [0, T])
 __device__ __forceinline__ int seq_len(const int64_t* lens, int b, int T) {

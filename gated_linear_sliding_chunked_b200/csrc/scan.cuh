@@ -60,31 +60,6 @@ struct ScanParams {
   void* dC;
 };
 
-// Pairs of fp32 values in 64-bit registers: one instruction for two lanes of
-// arithmetic (fma.rn.f32x2 and the like), rounded as the scalar ones.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pk(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float lo(f2 x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float hi(f2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ f2 ex2v(f2 x) { return pk(ex2(lo(x)), ex2(hi(x))); }
 
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative

@@ -342,72 +342,84 @@ cudaError_t go_any(const ScanParams& p, cudaStream_t s) {
 
 // ---- single tokens --------------------------------------------------------
 // The state is read and written once: bound by HBM (or L2, when it fits).
-// A thread holds 4 states of one channel (its rates stay in registers) and
-// takes two sequences at a time, whose loads overlap; the L lanes of a channel
-// add their shares of y.
+// A thread holds R = 8 states (4 where N is no multiple of 8) of one channel, so
+// that what is done once a channel (softplus, the gate, addresses) weighs less,
+// for two sequences whose loads overlap; the L lanes of a channel add their
+// shares of y.
 constexpr int kStepThreads = 256;
 
-template <typename IO, int L>
+template <typename IO, int L, int R>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p, float* state) {
+  constexpr int Q = R / 4;
   const unsigned idx = blockIdx.x * kStepThreads + threadIdx.x;
-  const int l = threadIdx.x % L, c = (int)(idx / L), n0 = 4 * l;
+  const int l = threadIdx.x % L, c = (int)(idx / L), n0 = R * l;
   const bool row = c < p.D, on = row && n0 < p.N;
-  const int g = row ? c / (p.D / p.G) : 0;
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int g = p.G > 1 && row ? c / (p.D / p.G) : 0;
+  float4 A[Q], h[2][Q];
+  Pack<IO, 4> B4[2][Q], C4[2][Q];
+  float u[2], d[2], z[2];
   float bias = 0.f, Ds = 0.f;
-  if (on) A = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int b = blockIdx.y + k * gridDim.y;
+    const bool ok = on && b < p.B;
+    u[k] = d[k] = z[k] = 0.f;
+    const float4* hp = reinterpret_cast<const float4*>(state + ((size_t)b * p.D + c) * p.N + n0);
+    const IO* pb = (const IO*)p.Bm + p.rb.at(b, 0) + (size_t)g * p.N + n0;
+    const IO* pc = (const IO*)p.Cm + p.rc.at(b, 0) + (size_t)g * p.N + n0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      h[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ok) h[k][q] = hp[q];
+      B4[k][q].load(pb + 4 * q, ok ? 4 : 0, p.vecbc);
+      C4[k][q].load(pc + 4 * q, ok ? 4 : 0, p.vecbc);
+    }
+    if (ok) {
+      u[k] = to_f(((const IO*)p.u)[p.ru.at(b, 0) + c]);
+      d[k] = to_f(((const IO*)p.dt)[p.rdt.at(b, 0) + c]);
+      if (p.z) z[k] = to_f(((const IO*)p.z)[p.rz.at(b, 0) + c]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    A[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) A[q] = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)c * p.N + n0) + q);
+  }
   if (row && p.dtb) bias = p.dtb[c];
   if (row && p.Dskip) Ds = p.Dskip[c];
-  const int b0 = blockIdx.y;
-  {
-    float4 h[2];
-    Pack<IO, 4> B4[2], C4[2];
-    float u[2], d[2], z[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int b = b0 + k * gridDim.y;
-      const bool ok = on && b < p.B;
-      h[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      u[k] = d[k] = z[k] = 0.f;
-      if (ok) {
-        h[k] = *reinterpret_cast<const float4*>(state + ((size_t)b * p.D + c) * p.N + n0);
-        u[k] = to_f(((const IO*)p.u)[p.ru.at(b, 0) + c]);
-        d[k] = to_f(((const IO*)p.dt)[p.rdt.at(b, 0) + c]);
-        if (p.z) z[k] = to_f(((const IO*)p.z)[p.rz.at(b, 0) + c]);
-      }
-      B4[k].load((const IO*)p.Bm + p.rb.at(b, 0) + (size_t)g * p.N + n0, ok ? 4 : 0, p.vecbc);
-      C4[k].load((const IO*)p.Cm + p.rc.at(b, 0) + (size_t)g * p.N + n0, ok ? 4 : 0, p.vecbc);
+  for (int k = 0; k < 2; ++k) {
+    const int b = blockIdx.y + k * gridDim.y;
+    float dl = d[k] + bias;
+    if (p.softplus) dl = softplus(dl);
+    const float du = dl * u[k], d2 = dl * kLog2e;
+    float y = 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float4 x = h[k][q];
+      const Pack<IO, 4>&Bq = B4[k][q], &Cq = C4[k][q];
+      x.x = fmaf(ex2(d2 * A[q].x), x.x, du * Bq.get(0));
+      x.y = fmaf(ex2(d2 * A[q].y), x.y, du * Bq.get(1));
+      x.z = fmaf(ex2(d2 * A[q].z), x.z, du * Bq.get(2));
+      x.w = fmaf(ex2(d2 * A[q].w), x.w, du * Bq.get(3));
+      if (on && b < p.B) reinterpret_cast<float4*>(state + ((size_t)b * p.D + c) * p.N + n0)[q] = x;
+      y += x.x * Cq.get(0) + x.y * Cq.get(1) + x.z * Cq.get(2) + x.w * Cq.get(3);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int b = b0 + k * gridDim.y;
-      float dl = d[k] + bias;
-      if (p.softplus) dl = softplus(dl);
-      const float du = dl * u[k], d2 = dl * kLog2e;
-      float4 x = h[k];
-      x.x = fmaf(ex2(d2 * A.x), x.x, du * B4[k].get(0));
-      x.y = fmaf(ex2(d2 * A.y), x.y, du * B4[k].get(1));
-      x.z = fmaf(ex2(d2 * A.z), x.z, du * B4[k].get(2));
-      x.w = fmaf(ex2(d2 * A.w), x.w, du * B4[k].get(3));
-      if (on && b < p.B) *reinterpret_cast<float4*>(state + ((size_t)b * p.D + c) * p.N + n0) = x;
-      float y = x.x * C4[k].get(0) + x.y * C4[k].get(1) + x.z * C4[k].get(2) + x.w * C4[k].get(3);
-#pragma unroll
-      for (int m = L / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-      if (row && l == 0 && b < p.B) {
-        y = fmaf(Ds, u[k], y);
-        if (p.z) y *= z[k] * sigmoid(z[k]);
-        ((IO*)p.y)[(size_t)b * p.D + c] = from_f<IO>(y);
-      }
+    for (int m = L / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+    if (row && l == 0 && b < p.B) {
+      y = fmaf(Ds, u[k], y);
+      if (p.z) y *= z[k] * sigmoid(z[k]);
+      ((IO*)p.y)[(size_t)b * p.D + c] = from_f<IO>(y);
     }
   }
 }
 
-template <typename IO, int L>
+template <typename IO, int L, int R>
 cudaError_t go_step(const ScanParams& p, float* state, cudaStream_t s) {
   const int gx = (int)(((size_t)p.D * L + kStepThreads - 1) / kStepThreads);
-  const int gy = (p.B + 1) / 2;
   ScopedTiming tm("scan_step", s);
-  scan_step_kernel<IO, L><<<dim3(gx, gy), kStepThreads, 0, s>>>(p, state);
+  scan_step_kernel<IO, L, R><<<dim3(gx, (p.B + 1) / 2), kStepThreads, 0, s>>>(p, state);
   return cudaGetLastError();
 }
 
@@ -420,12 +432,19 @@ cudaError_t launch_scan_fwd(const scan::ScanParams& p, bool bf, cudaStream_t s) 
 
 template <typename IO>
 static cudaError_t launch_scan_step(const scan::ScanParams& p, float* state, cudaStream_t s) {
+  if (p.N % 8 == 0) {
+    switch (scan::states_of(p.N)) {
+      case 8: return scan::go_step<IO, 1, 8>(p, state, s);
+      case 16: return scan::go_step<IO, 2, 8>(p, state, s);
+      case 32: return scan::go_step<IO, 4, 8>(p, state, s);
+      case 64: return scan::go_step<IO, 8, 8>(p, state, s);
+    }
+  }
   switch (scan::states_of(p.N)) {
-    case 4: return scan::go_step<IO, 1>(p, state, s);
-    case 8: return scan::go_step<IO, 2>(p, state, s);
-    case 16: return scan::go_step<IO, 4>(p, state, s);
-    case 32: return scan::go_step<IO, 8>(p, state, s);
-    case 64: return scan::go_step<IO, 16>(p, state, s);
+    case 4: return scan::go_step<IO, 1, 4>(p, state, s);
+    case 16: return scan::go_step<IO, 4, 4>(p, state, s);
+    case 32: return scan::go_step<IO, 8, 4>(p, state, s);
+    case 64: return scan::go_step<IO, 16, 4>(p, state, s);
   }
   return cudaErrorInvalidValue;
 }
