@@ -649,23 +649,26 @@ def _need(ok, fn, what):
 def _whole(fn, shape, dtype, dev, **tensors):
     """Contiguous tensors (or None) of one shape, dtype and device."""
     for name, t in tensors.items():
-        if t is not None and not (t.shape == shape and t.dtype == dtype and t.device == dev
-                                  and t.is_contiguous()):
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != dev
+                              or not t.is_contiguous()):
             raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape "
                              f"{tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}"
                              f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+_CONT = LzRows(0, 0)  # contiguous rows
 
 
 def _rows(fn, name, t, shape, dtype, dev):
     """Row strides of a strided input of `shape` ([B, T, ...] for prompts): the
     axes behind the tokens must be contiguous."""
     if t is None:
-        return LzRows(0, 0)
-    if not (t.shape == shape and t.dtype == dtype and t.device == dev):
+        return _CONT
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
         raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {tuple(shape)} on {dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     if t.is_contiguous():
-        return LzRows(0, 0)
+        return _CONT
     width = 1
     for n, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
         if n > 1 and st != width:
@@ -682,7 +685,7 @@ def _step_rows(fn, name, t, shape, dtype, dev):
     """The same for single tokens: [B, ...]."""
     if t is None or (t.is_contiguous() and t.shape == shape and t.dtype == dtype
                      and t.device == dev):
-        return LzRows(0, 0)
+        return _CONT
     return _rows(fn, name, t.unsqueeze(1), (shape[0], 1) + tuple(shape[1:]), dtype, dev)
 
 
@@ -884,7 +887,7 @@ def _norm_args(fn, o, z, r, groups, eps):
     dev, dtype = o.device, o.dtype
     if heads:
         _whole(fn, o.shape, dtype, dev, o=o)
-    ro = LzRows(0, 0) if heads else _rows(fn, "o", o, o.shape, dtype, dev)
+    ro = _CONT if heads else _rows(fn, "o", o, o.shape, dtype, dev)
     return LzNormDims(B, T, D, groups, int(heads), io_of(dtype), float(eps), ro,
                       _rows(fn, "z", z, (B, T, D), dtype, dev),
                       _rows(fn, "r", r, (B, T, D), dtype, dev))

@@ -7,9 +7,9 @@
 // 8).  A thread holds E = 16 elements; up
 // to 512 elements a row belongs to one warp (no block-wide synchronisation),
 // longer rows to a block.  The forward takes a row a block; the backward's
-// blocks walk the rows with a stride, the next row's loads in flight while this
-// one is worked on, so that the parameter gradients stay in registers and leave
-// as one partial per block.
+// blocks walk the rows with a stride, the next row on its way to shared memory
+// while this one is worked on, so that the parameter gradients stay in registers
+// and leave as one partial per block.
 #include "layer.cuh"
 
 namespace lz {
@@ -52,6 +52,7 @@ struct NormParams {
   void* dz;
   void* dr;
   float* part;  // [blocks][3][D]: dw, ds, dw2
+  int ring;     // floats of shared memory in front of the rows in flight
 };
 
 // Sums of M values over the team that holds a row: its warp, or its block.  One
@@ -91,8 +92,11 @@ __device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int la
   } else if constexpr (MODE == GROUP_LANES) {
     const int gv = nvec / p.G;  // lanes of a group: 1, 2, .. 32
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      for (int o = gv / 2; o > 0; o >>= 1) ps[k] += __shfl_xor_sync(0xffffffffu, ps[k], o);
+    for (int o = 16; o > 0; o >>= 1)
+      if (gv > o) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) ps[k] += __shfl_xor_sync(0xffffffffu, ps[k], o);
+      }
   } else {  // (block teams only) sm: nvec partials, then G sums
     const int gv = nvec / p.G, warp = threadIdx.x / 32, l = threadIdx.x % 32;
     float* gs = sm + nvec;
@@ -118,107 +122,122 @@ __device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int la
   }
 }
 
-// Address of feature c of row (b, t) of the block's output o (or its gradient
-// when it has o's layout)
-__device__ __forceinline__ size_t o_at(const NormParams& p, const Rows& so, int b, int t, int c) {
-  if (!p.heads) return so.at(b, t) + c;
-  const int dv = p.D / p.G, g = p.dshift >= 0 ? c >> p.dshift : c / dv;
-  return (((size_t)b * p.G + g) * p.T + t) * dv + (c - g * dv);
+// Where a row's features stand: a run of them, or (heads) a run of D/G in each
+// head's [T, D/G].
+template <typename IO>
+struct RowAt {
+  IO* p;
+  int64_t head;  // elements from head to head
+  int dv, dshift, heads;
+  __device__ __forceinline__ IO* at(int c) const {
+    if (!heads) return p + c;
+    const int g = dshift >= 0 ? c >> dshift : c / dv;
+    return p + (g * head + (c - g * dv));
+  }
+};
+template <typename IO>
+__device__ __forceinline__ RowAt<IO> row_at(const NormParams& p, IO* base, const Rows& so, int b, int t) {
+  const int dv = p.D / p.G;
+  const int64_t head = (int64_t)p.T * dv;
+  return {base + (p.heads ? b * p.G * head + (int64_t)t * dv : (int64_t)so.at(b, t)), head, dv, p.dshift, p.heads};
 }
 
-template <typename IO, int VW, bool WARP, int MODE, int MAXT>
+// FULL: every thread has E features (D is the team's threads times E)
+template <typename IO, int VW, bool WARP, int MODE, bool FULL, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   __shared__ float red[2][3 * 32];
   constexpr int NV = E / VW;
+  using V = Vec<VW>;
   const int team = WARP ? 32 : blockDim.x;
   const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
   const int nvec = p.D / VW;
+  auto has = [&](int k) { return FULL || k * team + lane < nvec; };
+  auto col = [&](int k) { return (k * team + lane) * VW; };
   const int b = blockIdx.y, t = WARP ? blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
   if (t >= p.T) return;
-  const int64_t row = (int64_t)b * p.T + t;
+  const int64_t row = ((int64_t)b * p.T + t) * p.D;
+  const auto o = row_at<const IO>(p, (const IO*)p.o, p.so, b, t);
+  const IO* pz = p.z ? (const IO*)p.z + p.sz.at(b, t) : nullptr;
+  const IO* pr = p.r ? (const IO*)p.r + p.sr.at(b, t) : nullptr;
   Raw<IO, VW> ro[NV], rz[NV], rr[NV];  // the row, all of it in flight at once
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int v = k * team + lane, c = v * VW;
-    const bool on = v < nvec;
-    ro[k].load_if((const IO*)p.o + o_at(p, p.so, b, t, c), on);
-    if (p.z) rz[k].load_if((const IO*)p.z + p.sz.at(b, t) + c, on);
-    if (p.r) rr[k].load_if((const IO*)p.r + p.sr.at(b, t) + c, on);
-  }
-  float x[E], ps[NV];
+  for (int k = 0; k < NV; ++k) ro[k].load_if(o.at(col(k)), has(k));
+  if (pz) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    ps[k] = 0.f;
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      x[k * VW + e] = ro[k].get(e);
-      ps[k] = fmaf(x[k * VW + e], x[k * VW + e], ps[k]);
-    }
+    for (int k = 0; k < NV; ++k) rz[k].load_if(pz + col(k), has(k));
   }
+  if (pr) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) rr[k].load_if(pr + col(k), has(k));
+  }
+  V x[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) x[k] = vec_of(ro[k]);
   if (p.w) {
+    float ps[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      V q;
+      q.mul(x[k], x[k]);
+      ps[k] = q.sum();
+    }
     group_sum<VW, WARP, MODE>(p, ps, lane, team, red[0], sm);
     const float ig = (float)p.G / (float)p.D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const float rs = rsqrtf(ps[k] * ig + p.eps);
-      const int v = k * team + lane;
-      if (v < nvec) {
-        float w[VW];
-        load_floats<VW>(p.w + v * VW, w);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) x[k * VW + e] *= rs * w[e];
-      }
+      if (!has(k)) continue;
+      V rs, w = vec_at<VW>(p.w + col(k));
+      rs.fill(rsqrtf(ps[k] * ig + p.eps));
+      w.mul(w, rs);
+      x[k].mul(x[k], w);
     }
+  }
+  if (pz) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      V z = vec_of(rz[k]), sg;
+      sg.sigmoid(z);
+      z.mul(z, sg);
+      x[k].mul(x[k], z);
+    }
+  }
+  if (p.s) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (has(k)) x[k].mul(x[k], vec_at<VW>(p.s + col(k)));
+  }
+  if (pr) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) x[k].add(vec_of(rr[k]));
   }
   float ss[1] = {0.f};
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int v = k * team + lane;
-    if (v < nvec) {
-      const int c = v * VW;
-      float* xv = x + k * VW;
-      if (p.z) {
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          const float z = rz[k].get(e);
-          xv[e] *= z * sigmoid(z);
-        }
-      }
-      if (p.s) {
-        float s[VW];
-        load_floats<VW>(p.s + c, s);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) xv[e] *= s[e];
-      }
-      if (p.r) {
-#pragma unroll
-        for (int e = 0; e < VW; ++e) xv[e] += rr[k].get(e);
-      }
-      store_vec<VW>((IO*)p.out + (size_t)row * p.D + c, xv);
-      // the second norm is that of the stored stream, so that the backward
-      // finds the same values in it
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        xv[e] = to_f(from_f<IO>(xv[e]));
-        ss[0] = fmaf(xv[e], xv[e], ss[0]);
-      }
+    if (!has(k)) continue;
+    raw_of(ro[k], x[k]);
+    ro[k].put((IO*)p.out + row + col(k));
+    // the second norm is that of the stored stream, so that the backward finds
+    // the same values in it
+    if (p.w2) {
+      x[k] = vec_of(ro[k]);
+      V q;
+      q.mul(x[k], x[k]);
+      ss[0] += q.sum();
     }
   }
   if (p.w2) {
     team_sum<WARP>(ss, red[1]);
-    const float rs = rsqrtf(ss[0] / (float)p.D + p.eps);
+    V rs;
+    rs.fill(rsqrtf(ss[0] / (float)p.D + p.eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = k * team + lane;
-      if (v < nvec) {
-        float* xv = x + k * VW;
-        float w[VW];
-        load_floats<VW>(p.w2 + v * VW, w);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) xv[e] *= rs * w[e];
-        store_vec<VW>((IO*)p.n + (size_t)row * p.D + v * VW, xv);
-      }
+      if (!has(k)) continue;
+      V w = vec_at<VW>(p.w2 + col(k));
+      w.mul(w, rs);
+      x[k].mul(x[k], w);
+      raw_of(ro[k], x[k]);
+      ro[k].put((IO*)p.n + row + col(k));
     }
   }
 }
@@ -228,74 +247,123 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormParams p) {
 // and with mh = o rs, core = mh w, f = e s:
 //   ds = sum e core silu(z)     dz = f core silu'(z)     dw = sum f silu(z) mh
 //   do = rs (k - mh mean_group(k mh)),  k = f silu(z) w
-template <typename IO, int VW, bool WARP, int MODE, int MAXT>
+template <typename IO, int VW, bool WARP, int MODE, bool FULL, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(NormParams p) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   __shared__ float red[2][3 * 32];
   constexpr int NV = E / VW;
+  using V = Vec<VW>;
   const int team = WARP ? 32 : blockDim.x;
   const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
   const int nvec = p.D / VW;
+  auto has = [&](int k) { return FULL || k * team + lane < nvec; };
+  auto col = [&](int k) { return (k * team + lane) * VW; };
   const int64_t row0 = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
   const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
   const float ig = (float)p.G / (float)p.D, id = 1.f / (float)p.D;
   const Rows cont{p.D, (int64_t)p.T * p.D};
   // sum over the rows of e silu(z) mh: times s it is dw, times w ds
-  float sm0[E], dw2[E];
+  V sm0[NV], dw2[NV];
 #pragma unroll
-  for (int i = 0; i < E; ++i) sm0[i] = dw2[i] = 0.f;
+  for (int k = 0; k < NV; ++k) {
+    sm0[k].fill(0.f);
+    dw2[k].fill(0.f);
+  }
+  // RING: the next row is copied to shared memory while this one is worked on,
+  // every thread its own vectors (so that no barrier is needed); in registers it
+  // would cost 40 of them
+  constexpr bool RING = VW > 1 && !WARP && MAXT <= 512;
+  enum { O, Z, OUT, DOUT, DN, N_IN };
   struct In {
-    Raw<IO, VW> o[NV], z[NV], out[NV], dout[NV], dn[NV];
+    Raw<IO, VW> v[N_IN][NV];
   };
-  auto fetch = [&](int64_t row, In& in) {
+  In in;
+  uint4* ring = reinterpret_cast<uint4*>(sm + p.ring);  // [2][N_IN][NV][threads]
+  auto slot = [&](int st, int i, int k) -> uint4* {
+    return ring + ((st * N_IN + i) * NV + k) * MAXT + threadIdx.x;
+  };
+  auto fetch = [&](int64_t row, int st) {
     const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
     const size_t at = (size_t)row * p.D;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = k * team + lane, c = v * VW;
-      const bool on = v < nvec;
-      if (p.dn) {
-        in.out[k].load_if((const IO*)p.out + at + c, on);
-        in.dn[k].load_if((const IO*)p.dn + at + c, on);
+    auto one = [&](int i, int k, const IO* q) {
+      if constexpr (RING) {
+        if (has(k)) cp_async16(slot(st, i, k), q);
+      } else {
+        in.v[i][k].load_if(q, has(k));
       }
-      in.o[k].load_if((const IO*)p.o + o_at(p, p.so, b, t, c), on);
-      if (p.dout) in.dout[k].load_if((const IO*)p.dout + at + c, on);
-      if (p.z) in.z[k].load_if((const IO*)p.z + p.sz.at(b, t) + c, on);
+    };
+    if (p.dn) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        one(OUT, k, (const IO*)p.out + at + col(k));
+        one(DN, k, (const IO*)p.dn + at + col(k));
+      }
+    }
+    const auto o = row_at<const IO>(p, (const IO*)p.o, p.so, b, t);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) one(O, k, o.at(col(k)));
+    if (p.dout) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) one(DOUT, k, (const IO*)p.dout + at + col(k));
+    }
+    if (p.z) {
+      const IO* pz = (const IO*)p.z + p.sz.at(b, t);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) one(Z, k, pz + col(k));
+    }
+    if constexpr (RING) cp_commit();
+  };
+  int st = 0;
+  auto val = [&](int i, int k) -> V {
+    if constexpr (RING) {
+      Raw<IO, VW> r;
+      r.zero();
+      if (has(k)) {
+        const uint4 u = *slot(st, i, k);
+        r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+      }
+      return vec_of(r);
+    } else {
+      return vec_of(in.v[i][k]);
     }
   };
   int turn = 0;  // of the two buffers of the block's sums
-  In nx;
-  if (row0 < p.rows) fetch(row0, nx);
-  for (int64_t row = row0; row < p.rows; row += step) {
-    const In in = nx;
-    if (row + step < p.rows) fetch(row + step, nx);
-    float e[E], x[E], ps[NV], rs[NV];
+  if (RING && row0 < p.rows) fetch(row0, 0);
+  for (int64_t row = row0; row < p.rows; row += step, st ^= RING) {
+    if constexpr (RING) {
+      if (row + step < p.rows) {
+        fetch(row + step, st ^ 1);
+        cp_wait<1>();
+      } else {
+        cp_wait<0>();
+      }
+    } else {
+      fetch(row, 0);
+    }
+    const int64_t at = row * p.D;
+    V e[NV], x[NV];
+    float ps[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      ps[k] = 0.f;
-#pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        x[k * VW + j] = in.o[k].get(j);
-        ps[k] = fmaf(x[k * VW + j], x[k * VW + j], ps[k]);
-        e[k * VW + j] = p.dout ? in.dout[k].get(j) : 0.f;
-      }
+      x[k] = val(O, k);
+      V q;
+      q.mul(x[k], x[k]);
+      ps[k] = q.sum();
+      if (p.dout) e[k] = val(DOUT, k);
+      else e[k].fill(0.f);
     }
     // first sums: of out^2, of q out and (one group) of o^2
     float sums[3] = {0.f, 0.f, 0.f};
     if (p.dn) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int v = k * team + lane;
-        if (v < nvec) {
-          float w2[VW];
-          load_floats<VW>(p.w2 + v * VW, w2);
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            const float xo = in.out[k].get(j);
-            sums[0] = fmaf(xo, xo, sums[0]);
-            sums[1] = fmaf(in.dn[k].get(j) * w2[j], xo, sums[1]);
-          }
-        }
+        if (!has(k)) continue;
+        V xo = val(OUT, k), q = val(DN, k), s;
+        q.mul(q, vec_at<VW>(p.w2 + col(k)));
+        s.mul(xo, xo);
+        sums[0] += s.sum();
+        q.mul(q, xo);
+        sums[1] += q.sum();
       }
     }
     if constexpr (MODE == GROUP_ROW) {
@@ -313,89 +381,97 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
       if (p.w) group_sum<VW, WARP, MODE>(p, ps, lane, team, nullptr, sm);
     }
     if (p.dn) {
-      const float r2 = rsqrtf(sums[0] * id + p.eps);
-      const float m = sums[1] * id * r2 * r2;
+      const float r2s = rsqrtf(sums[0] * id + p.eps);
+      V r2, m;
+      r2.fill(r2s);
+      m.fill(-sums[1] * id * r2s * r2s * r2s);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int v = k * team + lane;
-        if (v < nvec) {
-          float w2[VW];
-          load_floats<VW>(p.w2 + v * VW, w2);
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            const int i = k * VW + j;
-            const float xo = in.out[k].get(j), dn = in.dn[k].get(j);
-            dw2[i] = fmaf(dn * r2, xo, dw2[i]);
-            e[i] += r2 * (dn * w2[j] - xo * m);
-          }
-        }
+        if (!has(k)) continue;
+        V xo = val(OUT, k), q = val(DN, k);
+        q.mul(q, r2);  // dn rs2
+        dw2[k].fma(q, xo, dw2[k]);
+        e[k].fma(q, vec_at<VW>(p.w2 + col(k)), e[k]);
+        e[k].fma(xo, m, e[k]);
       }
     }
     if (p.dr) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int v = k * team + lane;
-        if (v < nvec) store_vec<VW>((IO*)p.dr + (size_t)row * p.D + v * VW, e + k * VW);
+        if (!has(k)) continue;
+        Raw<IO, VW> r;
+        raw_of(r, e[k]);
+        r.put((IO*)p.dr + at + col(k));
       }
     }
+    float rs[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = k * team + lane;
       rs[k] = p.w ? rsqrtf(ps[k] * ig + p.eps) : 1.f;
       ps[k] = 0.f;
-      if (v < nvec) {
-        const int c = v * VW;
-        float dz[VW], wv[VW], sv[VW];
-#pragma unroll
-        for (int j = 0; j < VW; ++j) wv[j] = sv[j] = 1.f;
-        if (p.w) load_floats<VW>(p.w + c, wv);
-        if (p.s) load_floats<VW>(p.s + c, sv);
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          x[k * VW + j] *= rs[k];  // mh
-          wv[j] *= sv[j];
-        }
-        if (p.z) {
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            const int i = k * VW + j;
-            const float z = in.z[k].get(j), sg = sigmoid(z), si = z * sg;
-            dz[j] = e[i] * x[i] * wv[j] * fmaf(-si, sg, sg + si);
-            e[i] *= si;
-          }
-          if (p.dz) store_vec<VW>((IO*)p.dz + (size_t)row * p.D + c, dz);
-        }
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          const int i = k * VW + j;
-          sm0[i] = fmaf(e[i], x[i], sm0[i]);
-          e[i] *= wv[j];  // the gradient at mh
-          ps[k] = fmaf(e[i], x[i], ps[k]);
-        }
+      if (!has(k)) continue;
+      V f;  // w s
+      f.fill(rs[k]);
+      x[k].mul(x[k], f);  // mh
+      if (p.w) {
+        f = vec_at<VW>(p.w + col(k));
+        if (p.s) f.mul(f, vec_at<VW>(p.s + col(k)));
+      } else if (p.s) {
+        f = vec_at<VW>(p.s + col(k));
+      } else {
+        f.fill(1.f);
       }
+      if (p.z) {
+        const V z = val(Z, k);
+        V sg, si, d;
+        sg.sigmoid(z);
+        si.mul(z, sg);
+        if (p.dz) {  // sg + si - si sg
+          V one;
+          one.fill(1.f);
+          d.fill(-1.f);
+          d.fma(sg, d, one);
+          d.fma(si, d, sg);
+          d.mul(d, e[k]);
+          d.mul(d, x[k]);
+          d.mul(d, f);
+          Raw<IO, VW> r;
+          raw_of(r, d);
+          r.put((IO*)p.dz + at + col(k));
+        }
+        e[k].mul(e[k], si);
+      }
+      sm0[k].fma(e[k], x[k], sm0[k]);
+      e[k].mul(e[k], f);  // the gradient at mh
+      V q;
+      q.mul(e[k], x[k]);
+      ps[k] = q.sum();
     }
     if (p.w) {
       group_sum<VW, WARP, MODE>(p, ps, lane, team, red[turn], sm);
       turn ^= MODE == GROUP_ROW;
     }
     const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
+    const auto d_o = row_at<IO>(p, (IO*)p.d_o, cont, b, t);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = k * team + lane;
-      if (v < nvec) {
-        if (p.w) {
-          const float m = ps[k] * ig;
-#pragma unroll
-          for (int j = 0; j < VW; ++j) e[k * VW + j] = rs[k] * (e[k * VW + j] - x[k * VW + j] * m);
-        }
-        store_vec<VW>((IO*)p.d_o + o_at(p, cont, b, t, v * VW), e + k * VW);
+      if (!has(k)) continue;
+      if (p.w) {
+        V m, r;
+        m.fill(-ps[k] * ig);
+        r.fill(rs[k]);
+        e[k].fma(x[k], m, e[k]);
+        e[k].mul(e[k], r);
       }
+      Raw<IO, VW> r;
+      raw_of(r, e[k]);
+      r.put(d_o.at(col(k)));
     }
   }
   // ---- the block's partials; the warps of a warp-per-row block are added in
   // order in shared memory
   auto value = [&](int q, int i, int c) {
-    const float a = q == 2 ? dw2[i] : sm0[i];
+    const float a = q == 2 ? dw2[i / VW].get(i % VW) : sm0[i / VW].get(i % VW);
     const float* f = q == 0 ? p.s : q == 1 ? p.w : nullptr;
     return f ? a * f[c] : a;
   };
@@ -433,6 +509,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
 
 struct Shape {
   bool vec, warp;
+  bool full;  // every thread of a team has E features
   int vw, threads, mode;
   size_t smem;  // of the group sums
 };
@@ -448,6 +525,7 @@ Shape shape_of(const lz_norm_dims* d, bool vec) {
   s.warp = d->D <= kWarpD && s.mode != GROUP_SMEM;
   s.threads = s.warp ? kRowWarps * 32 : (nvec * s.vw + E - 1) / E;
   s.threads = (s.threads + 31) / 32 * 32;
+  s.full = vec && d->D == (s.warp ? 32 : s.threads) * E;
   s.smem = s.mode == GROUP_SMEM ? (size_t)(nvec + d->G) * sizeof(float) : 0;
   return s;
 }
@@ -464,7 +542,11 @@ int grid_rows(Kern k, int64_t rows, int threads, size_t smem, int rows_per_block
 
 template <typename IO, int VW, bool WARP, int MODE>
 cudaError_t go_fwd(const NormParams& p, const Shape& sh, cudaStream_t s) {
-  auto k = norm_fwd_kernel<IO, VW, WARP, MODE, WARP ? kRowWarps * 32 : 1024>;
+  constexpr int kT = WARP ? kRowWarps * 32 : 1024;
+  auto k = norm_fwd_kernel<IO, VW, WARP, MODE, false, kT>;
+  if constexpr (VW > 1) {
+    if (sh.full) k = norm_fwd_kernel<IO, VW, WARP, MODE, true, kT>;
+  }
   if (sh.smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
     if (e != cudaSuccess) return e;
@@ -480,15 +562,26 @@ constexpr int kMaxBlocks = 148 * 8;
 int bwd_part_rows(int64_t rows) { return (int)std::min<int64_t>(std::max<int64_t>(rows, 1), kMaxBlocks); }
 
 template <typename IO, int VW, bool WARP, int MODE>
-cudaError_t go_bwd(const NormParams& p, const Shape& sh, int* blocks, cudaStream_t s) {
+cudaError_t go_bwd(NormParams p, const Shape& sh, int* blocks, cudaStream_t s) {
+  size_t smem = WARP ? std::max(sh.smem, (size_t)kRowWarps * p.D * sizeof(float)) : sh.smem;
   // two blocks an SM up to 4096 features, so that one works while the other
   // waits for its sums; longer rows need blocks of up to 1024 threads
-  auto k = norm_bwd_kernel<IO, VW, WARP, MODE, WARP ? kRowWarps * 32 : 256>;
-  if constexpr (!WARP) {
-    if (sh.threads > 256) k = norm_bwd_kernel<IO, VW, WARP, MODE, 512>;
-    if (sh.threads > 512) k = norm_bwd_kernel<IO, VW, WARP, MODE, 1024>;
+  constexpr int kT = WARP ? kRowWarps * 32 : 256;
+  auto k = norm_bwd_kernel<IO, VW, WARP, MODE, false, kT>;
+  if constexpr (VW > 1) {
+    if (sh.full) k = norm_bwd_kernel<IO, VW, WARP, MODE, true, kT>;
   }
-  const size_t smem = WARP ? std::max(sh.smem, (size_t)kRowWarps * p.D * sizeof(float)) : sh.smem;
+  if constexpr (!WARP) {
+    const int T = sh.threads > 256 ? 512 : 256;
+    p.ring = (int)((smem + 15) / 16 * 4);
+    // two rows in flight beside the sums' scratch, where they fit
+    const size_t ring = (size_t)p.ring * 4 + 2 * 5 * (E / VW) * (size_t)T * 16;
+    const bool fits = VW > 1 && sh.threads <= 512 && ring <= 200 * 1024;
+    if (sh.threads > 256 && fits) k = norm_bwd_kernel<IO, VW, WARP, MODE, false, 512>;
+    if (!fits && (VW > 1 || sh.threads > 512)) k = norm_bwd_kernel<IO, VW, WARP, MODE, false, 1024>;
+    if (!fits && VW == 1 && sh.threads > 256 && sh.threads <= 512) k = norm_bwd_kernel<IO, VW, WARP, MODE, false, 512>;
+    if (fits) smem = ring;
+  }
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -113,8 +113,73 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// 16 bytes to shared memory without waiting
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // sigma(x) (1 / inf = 0 where exp(-x) overflows)
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+
+// V floats in registers, as pairs where V is even
+template <int V>
+struct Vec {
+  f2 p[V / 2];
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? hi(p[i / 2]) : lo(p[i / 2]); }
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = pk(x, x);
+  }
+  template <typename F>
+  __device__ __forceinline__ void set(F f) {  // f(i): value i
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = pk(f(2 * i), f(2 * i + 1));
+  }
+  __device__ __forceinline__ void fma(const Vec& a, const Vec& b, const Vec& c) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = fma2(a.p[i], b.p[i], c.p[i]);
+  }
+  __device__ __forceinline__ void mul(const Vec& a, const Vec& b) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = mul2(a.p[i], b.p[i]);
+  }
+  __device__ __forceinline__ void add(const Vec& a) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = add2(p[i], a.p[i]);
+  }
+  __device__ __forceinline__ float sum() const {
+    f2 s = p[0];
+#pragma unroll
+    for (int i = 1; i < V / 2; ++i) s = add2(s, p[i]);
+    return lo(s) + hi(s);
+  }
+  // sigma of every value
+  __device__ __forceinline__ void sigmoid(const Vec& a) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const f2 x = mul2(a.p[i], pk(-kLog2e, -kLog2e));
+      const f2 y = add2(pk(ex2(lo(x)), ex2(hi(x))), pk(1.f, 1.f));
+      p[i] = pk(rcp(lo(y)), rcp(hi(y)));
+    }
+  }
+};
+template <>
+struct Vec<1> {
+  float x;
+  __device__ __forceinline__ float get(int) const { return x; }
+  __device__ __forceinline__ void fill(float v) { x = v; }
+  template <typename F>
+  __device__ __forceinline__ void set(F f) { x = f(0); }
+  __device__ __forceinline__ void fma(const Vec& a, const Vec& b, const Vec& c) { x = fmaf(a.x, b.x, c.x); }
+  __device__ __forceinline__ void mul(const Vec& a, const Vec& b) { x = a.x * b.x; }
+  __device__ __forceinline__ void add(const Vec& a) { x += a.x; }
+  __device__ __forceinline__ float sum() const { return x; }
+  __device__ __forceinline__ void sigmoid(const Vec& a) { x = rcp(1.f + ex2(-kLog2e * a.x)); }
+};
 
 // V consecutive elements of a row as they are in memory (V * sizeof(IO) bytes:
 // a multiple of 4; V = 1: one element)
@@ -152,6 +217,22 @@ struct Raw {
     if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
     else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
+  // from floats, rounded once
+  __device__ __forceinline__ void set(const float* x) {
+    if constexpr (sizeof(IO) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(x[i]);
+    } else if constexpr (V == 1) {
+      const bf16 h = __float2bfloat16_rn(x[0]);
+      w[0] = *reinterpret_cast<const unsigned short*>(&h);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
   __device__ __forceinline__ void put(IO* p) const {
     if constexpr (V * sizeof(IO) == 2) *reinterpret_cast<unsigned short*>(p) = (unsigned short)w[0];
     else if constexpr (W % 4 == 0) {
@@ -162,6 +243,20 @@ struct Raw {
     else *reinterpret_cast<uint32_t*>(p) = w[0];
   }
 };
+
+template <typename IO, int V>
+__device__ __forceinline__ Vec<V> vec_of(const Raw<IO, V>& r) {
+  Vec<V> v;
+  v.set([&](int i) { return r.get(i); });
+  return v;
+}
+template <typename IO, int V>
+__device__ __forceinline__ void raw_of(Raw<IO, V>& r, const Vec<V>& v) {
+  float x[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = v.get(i);
+  r.set(x);
+}
 
 // N consecutive floats from a 16-byte aligned address (any when N is not a
 // multiple of 4)
@@ -179,44 +274,14 @@ __device__ __forceinline__ void load_floats(const float* p, float* x) {
   }
 }
 
-// V floats in registers, as pairs where V is even
 template <int V>
-struct Vec {
-  f2 p[V / 2];
-  __device__ __forceinline__ float get(int i) const { return i & 1 ? hi(p[i / 2]) : lo(p[i / 2]); }
-  __device__ __forceinline__ void fill(float x) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) p[i] = pk(x, x);
-  }
-  template <typename F>
-  __device__ __forceinline__ void set(F f) {  // f(i): value i
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) p[i] = pk(f(2 * i), f(2 * i + 1));
-  }
-  __device__ __forceinline__ void fma(const Vec& a, const Vec& b, const Vec& c) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) p[i] = fma2(a.p[i], b.p[i], c.p[i]);
-  }
-  __device__ __forceinline__ void mul(const Vec& a, const Vec& b) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) p[i] = mul2(a.p[i], b.p[i]);
-  }
-  __device__ __forceinline__ void add(const Vec& a) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) p[i] = add2(p[i], a.p[i]);
-  }
-};
-template <>
-struct Vec<1> {
-  float x;
-  __device__ __forceinline__ float get(int) const { return x; }
-  __device__ __forceinline__ void fill(float v) { x = v; }
-  template <typename F>
-  __device__ __forceinline__ void set(F f) { x = f(0); }
-  __device__ __forceinline__ void fma(const Vec& a, const Vec& b, const Vec& c) { x = fmaf(a.x, b.x, c.x); }
-  __device__ __forceinline__ void mul(const Vec& a, const Vec& b) { x = a.x * b.x; }
-  __device__ __forceinline__ void add(const Vec& a) { x += a.x; }
-};
+__device__ __forceinline__ Vec<V> vec_at(const float* p) {
+  float x[V];
+  load_floats<V>(p, x);
+  Vec<V> v;
+  v.set([&](int i) { return x[i]; });
+  return v;
+}
 
 // Tokens of sequence b (lens nullable, clamped to [0, T])
 __device__ __forceinline__ int seq_len(const int64_t* lens, int b, int T) {
