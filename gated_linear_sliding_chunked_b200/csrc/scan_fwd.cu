@@ -343,43 +343,46 @@ cudaError_t go_any(const ScanParams& p, cudaStream_t s) {
 // ---- single tokens --------------------------------------------------------
 // The state is read and written once: bound by HBM (or L2, when it fits).
 // A thread holds R = 8 states (4 where N is no multiple of 8) of one channel, so
-// that what is done once a channel (softplus, the gate, addresses) weighs less,
-// for two sequences whose loads overlap; the L lanes of a channel add their
-// shares of y.
+// that what is done once a channel (softplus, the gate, addresses) weighs less;
+// its rates stay in registers while it walks sequences, the next one's loads in
+// flight.  The L lanes of a channel add their shares of y.
 constexpr int kStepThreads = 256;
 
 template <typename IO, int L, int R>
-__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p, float* state) {
+__global__ void __launch_bounds__(kStepThreads, 3) scan_step_kernel(ScanParams p, float* state) {
   constexpr int Q = R / 4;
   const unsigned idx = blockIdx.x * kStepThreads + threadIdx.x;
   const int l = threadIdx.x % L, c = (int)(idx / L), n0 = R * l;
   const bool row = c < p.D, on = row && n0 < p.N;
   const int g = p.G > 1 && row ? c / (p.D / p.G) : 0;
-  float4 A[Q], h[2][Q];
-  Pack<IO, 4> B4[2][Q], C4[2][Q];
-  float u[2], d[2], z[2];
-  float bias = 0.f, Ds = 0.f;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int b = blockIdx.y + k * gridDim.y;
-    const bool ok = on && b < p.B;
-    u[k] = d[k] = z[k] = 0.f;
+  struct In {
+    float4 h[Q];
+    Pack<IO, 4> B[Q], C[Q];
+    IO u, d, z;
+  };
+  auto fetch = [&](int b, In& x) {
     const float4* hp = reinterpret_cast<const float4*>(state + ((size_t)b * p.D + c) * p.N + n0);
     const IO* pb = (const IO*)p.Bm + p.rb.at(b, 0) + (size_t)g * p.N + n0;
     const IO* pc = (const IO*)p.Cm + p.rc.at(b, 0) + (size_t)g * p.N + n0;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      h[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (ok) h[k][q] = hp[q];
-      B4[k][q].load(pb + 4 * q, ok ? 4 : 0, p.vecbc);
-      C4[k][q].load(pc + 4 * q, ok ? 4 : 0, p.vecbc);
+      if (on) x.h[q] = hp[q];
+      else x.h[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      x.B[q].load(pb + 4 * q, on ? 4 : 0, p.vecbc);
+      x.C[q].load(pc + 4 * q, on ? 4 : 0, p.vecbc);
     }
-    if (ok) {
-      u[k] = to_f(((const IO*)p.u)[p.ru.at(b, 0) + c]);
-      d[k] = to_f(((const IO*)p.dt)[p.rdt.at(b, 0) + c]);
-      if (p.z) z[k] = to_f(((const IO*)p.z)[p.rz.at(b, 0) + c]);
+    if (on) {
+      x.u = ((const IO*)p.u)[p.ru.at(b, 0) + c];
+      x.d = ((const IO*)p.dt)[p.rdt.at(b, 0) + c];
+      if (p.z) x.z = ((const IO*)p.z)[p.rz.at(b, 0) + c];
+    } else {
+      x.u = x.d = x.z = from_f<IO>(0.f);
     }
-  }
+  };
+  float4 A[Q];
+  float bias = 0.f, Ds = 0.f;
+  In nx;
+  if ((int)blockIdx.y < p.B) fetch(blockIdx.y, nx);
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     A[q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -387,29 +390,33 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p, f
   }
   if (row && p.dtb) bias = p.dtb[c];
   if (row && p.Dskip) Ds = p.Dskip[c];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int b = blockIdx.y + k * gridDim.y;
-    float dl = d[k] + bias;
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const In in = nx;
+    if (b + (int)gridDim.y < p.B) fetch(b + gridDim.y, nx);
+    const float u = to_f(in.u);
+    float dl = to_f(in.d) + bias;
     if (p.softplus) dl = softplus(dl);
-    const float du = dl * u[k], d2 = dl * kLog2e;
+    const float du = dl * u, d2 = dl * kLog2e;
     float y = 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      float4 x = h[k][q];
-      const Pack<IO, 4>&Bq = B4[k][q], &Cq = C4[k][q];
+      float4 x = in.h[q];
+      const Pack<IO, 4>&Bq = in.B[q], &Cq = in.C[q];
       x.x = fmaf(ex2(d2 * A[q].x), x.x, du * Bq.get(0));
       x.y = fmaf(ex2(d2 * A[q].y), x.y, du * Bq.get(1));
       x.z = fmaf(ex2(d2 * A[q].z), x.z, du * Bq.get(2));
       x.w = fmaf(ex2(d2 * A[q].w), x.w, du * Bq.get(3));
-      if (on && b < p.B) reinterpret_cast<float4*>(state + ((size_t)b * p.D + c) * p.N + n0)[q] = x;
+      if (on) reinterpret_cast<float4*>(state + ((size_t)b * p.D + c) * p.N + n0)[q] = x;
       y += x.x * Cq.get(0) + x.y * Cq.get(1) + x.z * Cq.get(2) + x.w * Cq.get(3);
     }
 #pragma unroll
     for (int m = L / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-    if (row && l == 0 && b < p.B) {
-      y = fmaf(Ds, u[k], y);
-      if (p.z) y *= z[k] * sigmoid(z[k]);
+    if (row && l == 0) {
+      y = fmaf(Ds, u, y);
+      if (p.z) {
+        const float z = to_f(in.z);
+        y *= z * sigmoid(z);
+      }
       ((IO*)p.y)[(size_t)b * p.D + c] = from_f<IO>(y);
     }
   }
@@ -418,8 +425,10 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanParams p, f
 template <typename IO, int L, int R>
 cudaError_t go_step(const ScanParams& p, float* state, cudaStream_t s) {
   const int gx = (int)(((size_t)p.D * L + kStepThreads - 1) / kStepThreads);
+  // three blocks an SM, each with its share of the sequences
+  const int gy = std::max(1, std::min(p.B, 148 * 3 / gx));
   ScopedTiming tm("scan_step", s);
-  scan_step_kernel<IO, L, R><<<dim3(gx, (p.B + 1) / 2), kStepThreads, 0, s>>>(p, state);
+  scan_step_kernel<IO, L, R><<<dim3(gx, gy), kStepThreads, 0, s>>>(p, state);
   return cudaGetLastError();
 }
 
