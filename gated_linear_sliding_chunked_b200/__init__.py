@@ -646,47 +646,42 @@ def _need(ok, fn, what):
         raise ValueError(f"{fn}: {what}")
 
 
-def _whole(fn, shape, dtype, dev, **tensors):
-    """Contiguous tensors (or None) of one shape, dtype and device."""
-    for name, t in tensors.items():
-        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != dev
+def _bad(fn, name, t, shape, dtype, dev, rows=False):
+    raise ValueError(f"{fn}: {name} must be a {'' if rows else 'contiguous '}{dtype} tensor of shape "
+                     f"{tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                     f"{'' if rows or t.is_contiguous() else ', not contiguous'}")
+
+
+def _whole(fn, dev, *tensors):
+    """Checks (name, tensor or None, shape, dtype): contiguous, on dev."""
+    for name, t, shape, dtype in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.device != dev
                               or not t.is_contiguous()):
-            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape "
-                             f"{tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                             f"{'' if t.is_contiguous() else ', not contiguous'}")
+            _bad(fn, name, t, shape, dtype, dev)
 
 
 _CONT = LzRows(0, 0)  # contiguous rows
 
 
-def _rows(fn, name, t, shape, dtype, dev):
-    """Row strides of a strided input of `shape` ([B, T, ...] for prompts): the
-    axes behind the tokens must be contiguous."""
+def _rows(fn, name, t, shape, dtype, dev, lead=2):
+    """Row strides of a strided input of `shape`: [B, T, ...] (lead 2), or [B,
+    ...] for single tokens (lead 1).  The axes behind must be contiguous."""
     if t is None:
         return _CONT
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {tuple(shape)} on {dev}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        _bad(fn, name, t, shape, dtype, dev, rows=True)
     if t.is_contiguous():
         return _CONT
+    st = t.stride()
     width = 1
-    for n, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-        if n > 1 and st != width:
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] > 1 and st[i] != width:
             raise ValueError(f"{fn}: {name}: only the batch and token axes may be strided")
-        width *= n
-    B, T = t.shape[:2]
-    ld = t.stride(1) if T > 1 else max(width, 1)
+        width *= shape[i]
+    ld = st[1] if lead == 2 and shape[1] > 1 else width or 1
     if ld < 1:
         raise ValueError(f"{fn}: {name}: one token's row shared by all tokens is not supported")
-    return LzRows(ld, t.stride(0) if B > 1 else 0)
-
-
-def _step_rows(fn, name, t, shape, dtype, dev):
-    """The same for single tokens: [B, ...]."""
-    if t is None or (t.is_contiguous() and t.shape == shape and t.dtype == dtype
-                     and t.device == dev):
-        return _CONT
-    return _rows(fn, name, t.unsqueeze(1), (shape[0], 1) + tuple(shape[1:]), dtype, dev)
+    return LzRows(ld, st[0] if shape[0] > 1 else 0)
 
 
 class _Here:
@@ -728,10 +723,8 @@ def conv_fwd(x, w, bias=None, x0=None, *, silu=True, lens=None, want_xT=False, s
     (B, T, D), K = x.shape, w.shape[1]
     d = LzConvDims(B, T, D, K, io_of(x.dtype), int(bool(silu)),
                    _rows(fn, "x", x, x.shape, x.dtype, dev))
-    _whole(fn, (D, K), torch.float32, dev, w=w)
-    _whole(fn, (D,), torch.float32, dev, bias=bias)
-    _whole(fn, (B, K - 1, D), x.dtype, dev, x0=x0)
-    _whole(fn, (B,), torch.int64, dev, lens=lens)
+    _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
+           ("x0", x0, (B, K - 1, D), x.dtype), ("lens", lens, (B,), torch.int64))
     with _on(dev):
         y = torch.empty(B, T, D, dtype=x.dtype, device=dev)
         xT = torch.empty(B, K - 1, D, dtype=x.dtype, device=dev) if want_xT else None
@@ -748,11 +741,9 @@ def conv_bwd(x, w, dy, bias=None, x0=None, dxT=None, *, silu=True, lens=None, wa
     (B, T, D), K = x.shape, w.shape[1]
     d = LzConvDims(B, T, D, K, io_of(x.dtype), int(bool(silu)),
                    _rows(fn, "x", x, x.shape, x.dtype, dev))
-    _whole(fn, (D, K), torch.float32, dev, w=w)
-    _whole(fn, (D,), torch.float32, dev, bias=bias)
-    _whole(fn, (B, T, D), x.dtype, dev, dy=dy)
-    _whole(fn, (B, K - 1, D), x.dtype, dev, x0=x0, dxT=dxT)
-    _whole(fn, (B,), torch.int64, dev, lens=lens)
+    _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
+           ("dy", dy, (B, T, D), x.dtype), ("x0", x0, (B, K - 1, D), x.dtype),
+           ("dxT", dxT, (B, K - 1, D), x.dtype), ("lens", lens, (B,), torch.int64))
     with _on(dev):
         dx = torch.empty(B, T, D, dtype=x.dtype, device=dev)
         dw = torch.empty(D, K, dtype=torch.float32, device=dev)
@@ -772,11 +763,9 @@ def conv_step(hist, x, w, bias=None, *, silu=True, y=None, stream=None):
     _need(x.dim() == 2 and w.dim() == 2, fn, "x must be [B, D] and w [D, K]")
     (B, D), K = x.shape, w.shape[1]
     d = LzConvDims(B, 1, D, K, io_of(x.dtype), int(bool(silu)),
-                   _step_rows(fn, "x", x, x.shape, x.dtype, dev))
-    _whole(fn, (D, K), torch.float32, dev, w=w)
-    _whole(fn, (D,), torch.float32, dev, bias=bias)
-    _whole(fn, (B, K - 1, D), x.dtype, dev, hist=hist)
-    _whole(fn, (B, D), x.dtype, dev, y=y)
+                   _rows(fn, "x", x, (B, D), x.dtype, dev, 1))
+    _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
+           ("hist", hist, (B, K - 1, D), x.dtype), ("y", y, (B, D), x.dtype))
     with _on(dev):
         if y is None:
             y = torch.empty(B, D, dtype=x.dtype, device=dev)
@@ -784,22 +773,24 @@ def conv_step(hist, x, w, bias=None, *, silu=True, y=None, stream=None):
     return y
 
 
-def _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, step=False):
-    """Checks a scan call's inputs; returns its dims."""
-    lead = 1 if step else 2
-    _need(u.dim() == lead + 1 and A.dim() == 2, fn, "u must be %s and A [D, N]"
-          % ("[B, D]" if step else "[B, T, D]"))
-    _need(Bm.dim() in (lead + 1, lead + 2), fn, "Bm must be [.., N] or [.., G, N]")
-    dev, dtype, D, N = u.device, u.dtype, u.shape[-1], A.shape[1]
-    G = Bm.shape[-2] if Bm.dim() == lead + 2 else 1
-    bc = tuple(u.shape[:lead]) + ((G, N) if Bm.dim() == lead + 2 else (N,))
-    rows = _step_rows if step else _rows
-    r = [rows(fn, n, t, u.shape, dtype, dev) for n, t in (("u", u), ("dt", dt), ("z", z))]
-    r += [rows(fn, n, t, bc, dtype, dev) for n, t in (("Bm", Bm), ("Cm", Cm))]
-    _whole(fn, (D, N), torch.float32, dev, A=A)
-    _whole(fn, (D,), torch.float32, dev, Dskip=Dskip, dt_bias=dt_bias)
-    T = 1 if step else u.shape[1]
-    return LzScanDims(u.shape[0], T, D, G, N, io_of(dtype), int(bool(softplus)), *r)
+def _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, lead=2):
+    """Checks a scan call's inputs (lead 2: prompts, 1: single tokens); returns
+    its dims."""
+    us, bs = u.shape, Bm.shape
+    _need(len(us) == lead + 1 and A.dim() == 2, fn,
+          f"u must be {'[B, T, D]' if lead == 2 else '[B, D]'} and A [D, N]")
+    _need(len(bs) in (lead + 1, lead + 2), fn, "Bm must be [.., N] or [.., G, N]")
+    dev, dtype, D, N = u.device, u.dtype, us[-1], A.shape[1]
+    G = bs[lead] if len(bs) == lead + 2 else 1
+    bc = us[:lead] + ((G, N) if len(bs) == lead + 2 else (N,))
+    _whole(fn, dev, ("A", A, (D, N), torch.float32), ("Dskip", Dskip, (D,), torch.float32),
+           ("dt_bias", dt_bias, (D,), torch.float32))
+    return LzScanDims(us[0], us[1] if lead == 2 else 1, D, G, N, io_of(dtype),
+                      1 if softplus else 0, _rows(fn, "u", u, us, dtype, dev, lead),
+                      _rows(fn, "dt", dt, us, dtype, dev, lead),
+                      _rows(fn, "z", z, us, dtype, dev, lead),
+                      _rows(fn, "Bm", Bm, bc, dtype, dev, lead),
+                      _rows(fn, "Cm", Cm, bc, dtype, dev, lead))
 
 
 def scan_fwd(u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, softplus=True, h0=None,
@@ -812,8 +803,8 @@ def scan_fwd(u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, softplus=Tru
     fn, dev = "scan_fwd", u.device
     d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus)
     B, T, D = u.shape
-    _whole(fn, (B, D, A.shape[1]), torch.float32, dev, h0=h0)
-    _whole(fn, (B,), torch.int64, dev, lens=lens)
+    _whole(fn, dev, ("h0", h0, (B, D, A.shape[1]), torch.float32),
+           ("lens", lens, (B,), torch.int64))
     with _on(dev):
         y = torch.empty(B, T, D, dtype=u.dtype, device=dev)
         hT = torch.empty(B, D, A.shape[1], dtype=torch.float32, device=dev) if want_hT else None
@@ -837,12 +828,11 @@ def scan_bwd(u, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, dt_bias=None, softplus
     d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus)
     B, T, D = u.shape
     N = A.shape[1]
-    _whole(fn, (B, T, D), u.dtype, dev, dy=dy)
-    _whole(fn, (B, D, N), torch.float32, dev, h0=h0, dhT=dhT)
-    _whole(fn, (B,), torch.int64, dev, lens=lens)
+    _whole(fn, dev, ("dy", dy, (B, T, D), u.dtype), ("h0", h0, (B, D, N), torch.float32),
+           ("dhT", dhT, (B, D, N), torch.float32), ("lens", lens, (B,), torch.int64))
     if states is not None:
-        _whole(fn, (lz_layer_workspace_bytes(d, LZ_WS_SCAN_STATES) // 4,), torch.float32, dev,
-               states=states)
+        _whole(fn, dev, ("states", states,
+                         (lz_layer_workspace_bytes(d, LZ_WS_SCAN_STATES) // 4,), torch.float32))
     with _on(dev):
         f32 = dict(dtype=torch.float32, device=dev)
         new = lambda: torch.empty(B, T, D, dtype=u.dtype, device=dev)
@@ -865,9 +855,8 @@ def scan_step(state, u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, soft
     """One generation step: u, dt, z [B, D], Bm, Cm [B, N] or [B, G, N], state
     [B, D, N] fp32 in place; returns y [B, D]."""
     fn, dev = "scan_step", u.device
-    d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, step=True)
-    _whole(fn, (u.shape[0], u.shape[1], A.shape[1]), torch.float32, dev, state=state)
-    _whole(fn, u.shape, u.dtype, dev, y=y)
+    d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, 1)
+    _whole(fn, dev, ("state", state, (d.B, d.D, d.N), torch.float32), ("y", y, u.shape, u.dtype))
     with _on(dev):
         if y is None:
             y = torch.empty(u.shape, dtype=u.dtype, device=dev)
@@ -886,11 +875,11 @@ def _norm_args(fn, o, z, r, groups, eps):
         B, T, D = o.shape
     dev, dtype = o.device, o.dtype
     if heads:
-        _whole(fn, o.shape, dtype, dev, o=o)
+        _whole(fn, dev, ("o", o, o.shape, dtype))
     ro = _CONT if heads else _rows(fn, "o", o, o.shape, dtype, dev)
-    return LzNormDims(B, T, D, groups, int(heads), io_of(dtype), float(eps), ro,
-                      _rows(fn, "z", z, (B, T, D), dtype, dev),
-                      _rows(fn, "r", r, (B, T, D), dtype, dev))
+    shape = (B, T, D)
+    return LzNormDims(B, T, D, groups, 1 if heads else 0, io_of(dtype), eps, ro,
+                      _rows(fn, "z", z, shape, dtype, dev), _rows(fn, "r", r, shape, dtype, dev))
 
 
 def block_norm_fwd(o, *, w=None, z=None, s=None, r=None, w2=None, groups=1, eps=1e-5, stream=None):
@@ -902,7 +891,9 @@ def block_norm_fwd(o, *, w=None, z=None, s=None, r=None, w2=None, groups=1, eps=
     [D] fp32.  Returns (out, n); n is None without w2."""
     fn, dev = "block_norm_fwd", o.device
     d = _norm_args(fn, o, z, r, groups, eps)
-    _whole(fn, (d.D,), torch.float32, dev, w=w, s=s, w2=w2)
+    par = (d.D,)
+    _whole(fn, dev, ("w", w, par, torch.float32), ("s", s, par, torch.float32),
+           ("w2", w2, par, torch.float32))
     with _on(dev):
         out = torch.empty(d.B, d.T, d.D, dtype=o.dtype, device=dev)
         n = torch.empty_like(out) if w2 is not None else None
@@ -917,8 +908,10 @@ def block_norm_bwd(o, *, w=None, z=None, s=None, w2=None, out=None, dout=None, d
     out: the forward's, needed with dn."""
     fn, dev = "block_norm_bwd", o.device
     d = _norm_args(fn, o, z, None, groups, eps)
-    _whole(fn, (d.D,), torch.float32, dev, w=w, s=s, w2=w2)
-    _whole(fn, (d.B, d.T, d.D), o.dtype, dev, out=out, dout=dout, dn=dn)
+    P, R = (d.D,), (d.B, d.T, d.D)
+    _whole(fn, dev, ("w", w, P, torch.float32), ("s", s, P, torch.float32),
+           ("w2", w2, P, torch.float32), ("out", out, R, o.dtype), ("dout", dout, R, o.dtype),
+           ("dn", dn, R, o.dtype))
     _need(dout is not None or dn is not None, fn, "dout or dn must be given")
     _need(dn is None or (out is not None and w2 is not None), fn, "dn needs out and w2")
     with _on(dev):
