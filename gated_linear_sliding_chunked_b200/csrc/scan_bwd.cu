@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
   A2[1] = mul2(A2[1], pk(kLog2e, kLog2e));
   if (!END) {
     if (p.dhT) load_state(p.dhT + sidx, p.N, on0, on1, gr);
+#pragma unroll 4
     for (int s = p.nseg - 1; s > seg; --s) {
       f2 x[2];
       load_state(p.segE + s * sstep + sidx, p.N, on0, on1, x);

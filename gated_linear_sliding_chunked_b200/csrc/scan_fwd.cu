@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(64 * W, W > 4 ? 1 : 2) scan_fwd_kernel(ScanPar
         h[0] = pk(x.x, x.y);
         h[1] = pk(x.z, x.w);
       }
+#pragma unroll 4
       for (int s = 0; s < seg; ++s) {
         const float4 x = *reinterpret_cast<const float4*>(p.segE + s * sstep + sidx);
         const float d = p.segD[((size_t)s * p.B + b) * p.D + c];
@@ -501,7 +502,7 @@ void plan(const lz_scan_dims* d, int* W, int* nct, int* seg, int* nseg) {
   auto busiest = [&](int w) { return (tiles(w) * gb + kSMs - 1) / kSMs * w; };
   const int64_t base = tiles(4) * gb;
   int n = 1;
-  if (base > 0 && base * 3 <= kSMs * 2) n = (int)std::min<int64_t>(32, kSMs * 4 / base);
+  if (base > 0 && base * 3 <= kSMs * 2) n = (int)std::min<int64_t>(32, kSMs * 2 / base);
   *W = N >= 16 && n == 1 && busiest(7) < busiest(4) ? 7 : 4;
   *nct = tiles(*W);
   int len = ((d->T + n - 1) / n + 31) / 32 * 32;
