@@ -160,18 +160,11 @@ __device__ __forceinline__ void load_f(const float* p, float* x) {
 // V values to consecutive elements, n of which exist
 template <typename IO, int V>
 __device__ __forceinline__ void store_n(IO* p, const float* x, int n, bool vec) {
-  constexpr int M = 16 / (int)sizeof(IO) < V ? 16 / (int)sizeof(IO) : V;
-  if (vec && M > 1) {
+  if (vec) {
     if (n > 0) {
-#pragma unroll
-      for (int i = 0; i < V; i += M) {
-        if constexpr (M == 2) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(x[i], x[i + 1]);
-          *reinterpret_cast<__nv_bfloat162*>(p + i) = h;
-        } else {
-          store_vec<M>(p + i, x + i);
-        }
-      }
+      Raw<IO, V> r;
+      r.set(x);
+      r.put(p);
     }
   } else {
 #pragma unroll

@@ -125,6 +125,15 @@ def test_scan_matches_definition(dtype, B, T, D, G, N, z, h0, skip, lens, stride
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("N", [4, 8, 12, 16, 24, 32, 48, 64])
+def test_every_width_of_state(dtype, N):
+    """Whole vectors of channels, several tiles and segments, at every width:
+    each has its own split of states over lanes and of tokens over threads."""
+    test_scan_matches_definition(dtype, 2, 150, 64, 2, N, True, True, True, [150, 97], False, True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,D,G,N", [(BF, 64, 1, 16), (BF, 9, 3, 12), (F, 40, 2, 64),
                                          (F, 5, 1, 4)])
 def test_prompt_then_steps_is_the_whole_sequence(dtype, D, G, N):
