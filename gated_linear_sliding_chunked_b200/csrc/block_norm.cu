@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
     const size_t at = (size_t)row * p.D;
     auto one = [&](int i, int k, const IO* q) {
       if constexpr (RING) {
-        if (has(k)) cp_async16(slot(st, i, k), q);
+        if (has(k)) cp_async<16>(slot(st, i, k), q);
       } else {
         in.v[i][k].load_if(q, has(k));
       }
@@ -318,10 +318,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
     if constexpr (RING) {
       Raw<IO, VW> r;
       r.zero();
-      if (has(k)) {
-        const uint4 u = *slot(st, i, k);
-        r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
-      }
+      if (has(k)) r.load_shared(slot(st, i, k));
       return vec_of(r);
     } else {
       return vec_of(in.v[i][k]);

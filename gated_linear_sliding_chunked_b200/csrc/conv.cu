@@ -403,7 +403,7 @@ struct StepLaunch {
 int bwd_blocks(const lz_conv_dims* d, int* run) {
   // long runs re-read the least; short ones keep every SM busy (at least two
   // blocks each) when there are few tokens and channels
-  int r = 64;
+  int r = 128;
   const int cb = (d->D + 127) / 128;
   while (r > 8 && (size_t)d->B * cb * ((d->T + r * kWarps - 1) / (r * kWarps)) < 296) r /= 2;
   *run = r;
