@@ -5,10 +5,11 @@ namespace lz {
 namespace scan {
 namespace {
 
-// L: lanes of a channel, 4 states a lane; W: scan warps of a block
-template <int L, int W>
+// L: lanes of a channel, 4 states a lane; W: scan warps of a block; WE: its
+// elementwise warps
+template <int L, int W, int WE>
 struct Geo {
-  static constexpr int NS = 32 * W, NE = 32 * W;  // scan threads, elementwise threads
+  static constexpr int NS = 32 * W, NE = 32 * WE;  // scan threads, elementwise threads
   static constexpr int CH = NS / L;         // channels of a block
   static constexpr int NP = 4 * L;          // states, padded
   static constexpr int U = L < 4 ? L : 4;   // tokens whose lane sums are formed together
@@ -34,9 +35,9 @@ __device__ __forceinline__ void load_bc(const IO* p, f2& x, f2& y) {
 
 // Tile: 8 elements of (token, channel) for each elementwise thread, as long as
 // that is at most 32 tokens.
-template <int L, int W>
+template <int L, int W, int WE>
 struct Tile {
-  using G = Geo<L, W>;
+  using G = Geo<L, W, WE>;
   static constexpr int TT = L >= 4 ? 32 : 8 * L;
   static constexpr int EV = TT * G::CH / G::NE;              // elements of a thread: neighbours in a row
   static constexpr int DS = G::CH + 2;                       // row of dd, off the banks of the row before
@@ -44,10 +45,10 @@ struct Tile {
   static constexpr int BN = (BV + G::NE - 1) / G::NE;        // those of a thread
 };
 
-template <typename IO, int L, int W>
+template <typename IO, int L, int W, int WE>
 struct alignas(16) Smem {
-  using X = Tile<L, W>;
-  using G = Geo<L, W>;
+  using X = Tile<L, W, WE>;
+  using G = Geo<L, W, WE>;
   float2 dd[2][X::TT * X::DS];  // delta, delta * u
   IO bf[2][X::TT * G::NP], cf[2][X::TT * G::NP];
   float ys[2][X::TT * G::YS];
@@ -57,18 +58,18 @@ struct alignas(16) Smem {
 // inputs of the next U tokens are formed before the state passes through
 // these, and the whole tile is one run of instructions, so that the loads and
 // exponentials of the former fill the waits of the latter.
-template <typename IO, int L, int W, bool END>
+template <typename IO, int L, int W, int WE, bool END>
 __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const IO* __restrict__ bf,
                                           const IO* __restrict__ cf, float* __restrict__ ys, const f2 (&A2)[2],
                                           f2 (&h)[2], float& sumd, int lane, int l, float* states, size_t ck_step,
                                           int ck_left) {
-  using G = Geo<L, W>;
-  constexpr int NP = G::NP, U = G::U, TT = Tile<L, W>::TT, NG = TT / U;
+  using G = Geo<L, W, WE>;
+  constexpr int NP = G::NP, U = G::U, TT = Tile<L, W, WE>::TT, NG = TT / U;
   f2 a[2][U][2], x[2][U][2];
   auto form = [&](int i, f2 (&a)[U][2], f2 (&x)[U][2]) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const float2 d = dd[(i + j) * Tile<L, W>::DS];
+      const float2 d = dd[(i + j) * Tile<L, W, WE>::DS];
       f2 B0, B1;
       load_bc(bf + (i + j) * NP, B0, B1);
       const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
@@ -113,14 +114,14 @@ __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const I
 // END: only the segment's effect on the state (its end value from a zero
 // start and the sum of delta), which the blocks of the later segments fold
 // into the state they start from.
-template <typename IO, int L, int W, bool END>
-__global__ void __launch_bounds__(64 * W, W > 4 ? 1 : 2) scan_fwd_kernel(ScanParams p) {
-  using G = Geo<L, W>;
-  using X = Tile<L, W>;
+template <typename IO, int L, int W, int WE, bool END>
+__global__ void __launch_bounds__(32 * (W + WE), W + WE > 8 ? 1 : 2) scan_fwd_kernel(ScanParams p) {
+  using G = Geo<L, W, WE>;
+  using X = Tile<L, W, WE>;
   constexpr int CH = G::CH, TT = X::TT, EV = X::EV, BN = X::BN, DS = X::DS;
   constexpr int NS = G::NS, NE = G::NE;
   extern __shared__ __align__(16) char raw[];
-  using S = Smem<IO, L, W>;
+  using S = Smem<IO, L, W, WE>;
   S& sm = *reinterpret_cast<S*>(raw);
   const int tid = threadIdx.x;
   const int g = blockIdx.x / p.nct, ct = blockIdx.x % p.nct;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(64 * W, W > 4 ? 1 : 2) scan_fwd_kernel(ScanPar
     // (a tile of 8 tokens starts at a 16th one every other time)
     const int t = t0 + k * TT;
     const bool ck = p.states && on && t % kCk == 0;
-    scan_tile<IO, L, W, END>(dd, bf, cf, ys, A2, h, sumd, lane, l,
+    scan_tile<IO, L, W, WE, END>(dd, bf, cf, ys, A2, h, sumd, lane, l,
                           p.states + (((size_t)b * ((p.T + kCk - 1) / kCk) + t / kCk) * p.D + c) * p.N + n0,
                           (size_t)p.D * p.N, ck ? te - t : 0);
     __syncthreads();
@@ -309,33 +310,37 @@ __global__ void __launch_bounds__(64 * W, W > 4 ? 1 : 2) scan_fwd_kernel(ScanPar
   }
 }
 
-template <typename IO, int L, int W>
+template <typename IO, int L, int W, int WE = W>
 cudaError_t go(const ScanParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(Smem<IO, L, W>);
+  const size_t smem = sizeof(Smem<IO, L, W, WE>);
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, W, WE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, W, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = cudaFuncSetAttribute(scan_fwd_kernel<IO, L, W, WE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   if (p.nseg > 1) {
     ScopedTiming tm("scan_fwd_ends", s);
-    scan_fwd_kernel<IO, L, W, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), 64 * W, smem, s>>>(p);
+    scan_fwd_kernel<IO, L, W, WE, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), 32 * (W + WE), smem, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   ScopedTiming tm("scan_fwd", s);
-  scan_fwd_kernel<IO, L, W, false><<<dim3(p.G * p.nct, p.B, p.nseg), 64 * W, smem, s>>>(p);
+  scan_fwd_kernel<IO, L, W, WE, false><<<dim3(p.G * p.nct, p.B, p.nseg), 32 * (W + WE), smem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename IO>
 cudaError_t go_any(const ScanParams& p, cudaStream_t s) {
+  // blocks with an SM to themselves take twice the elementwise warps: with one
+  // scan warp to a scheduler, these are what a tile waits for (1 x 2048 tokens,
+  // 4096 channels, 16 states: see the time beside plan())
+  const bool alone = p.nseg == 1 && (int64_t)p.nct * p.G * p.B <= 148;
   switch (states_of(p.N)) {
-    case 4: return go<IO, 1, 4>(p, s);
-    case 8: return go<IO, 2, 4>(p, s);
-    case 16: return p.W == 7 ? go<IO, 4, 7>(p, s) : go<IO, 4, 4>(p, s);
-    case 32: return p.W == 7 ? go<IO, 8, 7>(p, s) : go<IO, 8, 4>(p, s);
+    case 4: return alone ? go<IO, 1, 4, 8>(p, s) : go<IO, 1, 4>(p, s);
+    case 8: return alone ? go<IO, 2, 4, 8>(p, s) : go<IO, 2, 4>(p, s);
+    case 16: return p.W == 7 ? go<IO, 4, 7>(p, s) : alone ? go<IO, 4, 4, 8>(p, s) : go<IO, 4, 4>(p, s);
+    case 32: return p.W == 7 ? go<IO, 8, 7>(p, s) : alone ? go<IO, 8, 4, 8>(p, s) : go<IO, 8, 4>(p, s);
     case 64: return p.W == 7 ? go<IO, 16, 7>(p, s) : go<IO, 16, 4>(p, s);
   }
   return cudaErrorInvalidValue;
