@@ -66,19 +66,16 @@ __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const I
   using G = Geo<L, W, WE>;
   constexpr int NP = G::NP, U = G::U, TT = Tile<L, W, WE>::TT, NG = TT / U;
   f2 a[2][U][2], x[2][U][2];
-  auto form = [&](int i, f2 (&a)[U][2], f2 (&x)[U][2]) {
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const float2 d = dd[(i + j) * Tile<L, W, WE>::DS];
-      f2 B0, B1;
-      load_bc(bf + (i + j) * NP, B0, B1);
-      const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
-      a[j][0] = ex2v(mul2(A2[0], d2));
-      a[j][1] = ex2v(mul2(A2[1], d2));
-      x[j][0] = mul2(du2, B0);
-      x[j][1] = mul2(du2, B1);
-      if (END) sumd += d.x;
-    }
+  auto form = [&](int i, f2 (&a)[2], f2 (&x)[2]) {
+    const float2 d = dd[i * Tile<L, W, WE>::DS];
+    f2 B0, B1;
+    load_bc(bf + i * NP, B0, B1);
+    const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
+    a[0] = ex2v(mul2(A2[0], d2));
+    a[1] = ex2v(mul2(A2[1], d2));
+    x[0] = mul2(du2, B0);
+    x[1] = mul2(du2, B1);
+    if (END) sumd += d.x;
   };
   // C h of U tokens: summed over the lanes a step later
   float yv[2][U];
@@ -87,15 +84,16 @@ __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const I
     reduce_scatter<U, L / 2, 1>(v, lane, j);
     if (l % (L / U) == 0) ys[(i + j) * G::YS] = v[0];
   };
-  form(0, a[0], x[0]);
+#pragma unroll
+  for (int j = 0; j < U; ++j) form(j, a[0][j], x[0][j]);
 #pragma unroll
   for (int q = 0; q < NG; ++q) {
     const int i = q * U;
-    if (q + 1 < NG) form(i + U, a[(q + 1) & 1], x[(q + 1) & 1]);
     if (!END && i % kCk == 0 && i < ck_left)  // the state before every 16th token
       *reinterpret_cast<float4*>(states + i / kCk * ck_step) = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
 #pragma unroll
     for (int j = 0; j < U; ++j) {
+      if (q + 1 < NG) form(i + U + j, a[(q + 1) & 1][j], x[(q + 1) & 1][j]);
       h[0] = fma2(a[q & 1][j][0], h[0], x[q & 1][j][0]);
       h[1] = fma2(a[q & 1][j][1], h[1], x[q & 1][j][1]);
       if (!END) {
