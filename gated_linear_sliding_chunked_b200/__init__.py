@@ -697,10 +697,17 @@ class _Here:
 _HERE = _Here()
 
 
-def _on(dev):
-    """Work goes to the tensors' device."""
+def _on(dev, stream):
+    """Work goes to the tensors' device.  With a stream given, outputs and
+    scratch are allocated for it too: scratch is given back when the call
+    returns, and only that stream's order keeps it until the kernels are
+    done."""
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, not {dev}")
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        return torch.cuda.stream(stream)
     return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
@@ -725,7 +732,7 @@ def conv_fwd(x, w, bias=None, x0=None, *, silu=True, lens=None, want_xT=False, s
                    _rows(fn, "x", x, x.shape, x.dtype, dev))
     _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
            ("x0", x0, (B, K - 1, D), x.dtype), ("lens", lens, (B,), torch.int64))
-    with _on(dev):
+    with _on(dev, stream):
         y = torch.empty(B, T, D, dtype=x.dtype, device=dev)
         xT = torch.empty(B, K - 1, D, dtype=x.dtype, device=dev) if want_xT else None
         lz_conv_fwd(d, x, w, bias, x0, lens, y, xT, _stream_on(dev, stream))
@@ -744,7 +751,7 @@ def conv_bwd(x, w, dy, bias=None, x0=None, dxT=None, *, silu=True, lens=None, wa
     _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
            ("dy", dy, (B, T, D), x.dtype), ("x0", x0, (B, K - 1, D), x.dtype),
            ("dxT", dxT, (B, K - 1, D), x.dtype), ("lens", lens, (B,), torch.int64))
-    with _on(dev):
+    with _on(dev, stream):
         dx = torch.empty(B, T, D, dtype=x.dtype, device=dev)
         dw = torch.empty(D, K, dtype=torch.float32, device=dev)
         db = torch.empty(D, dtype=torch.float32, device=dev) if bias is not None else None
@@ -766,7 +773,7 @@ def conv_step(hist, x, w, bias=None, *, silu=True, y=None, stream=None):
                    _rows(fn, "x", x, (B, D), x.dtype, dev, 1))
     _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
            ("hist", hist, (B, K - 1, D), x.dtype), ("y", y, (B, D), x.dtype))
-    with _on(dev):
+    with _on(dev, stream):
         if y is None:
             y = torch.empty(B, D, dtype=x.dtype, device=dev)
         lz_conv_step(d, hist, x, w, bias, y, _stream_on(dev, stream))
@@ -805,7 +812,7 @@ def scan_fwd(u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, softplus=Tru
     B, T, D = u.shape
     _whole(fn, dev, ("h0", h0, (B, D, A.shape[1]), torch.float32),
            ("lens", lens, (B,), torch.int64))
-    with _on(dev):
+    with _on(dev, stream):
         y = torch.empty(B, T, D, dtype=u.dtype, device=dev)
         hT = torch.empty(B, D, A.shape[1], dtype=torch.float32, device=dev) if want_hT else None
         st = None
@@ -833,7 +840,7 @@ def scan_bwd(u, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, dt_bias=None, softplus
     if states is not None:
         _whole(fn, dev, ("states", states,
                          (lz_layer_workspace_bytes(d, LZ_WS_SCAN_STATES) // 4,), torch.float32))
-    with _on(dev):
+    with _on(dev, stream):
         f32 = dict(dtype=torch.float32, device=dev)
         new = lambda: torch.empty(B, T, D, dtype=u.dtype, device=dev)
         du, ddt, dz = new(), new(), new() if z is not None else None
@@ -857,7 +864,7 @@ def scan_step(state, u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, soft
     fn, dev = "scan_step", u.device
     d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, 1)
     _whole(fn, dev, ("state", state, (d.B, d.D, d.N), torch.float32), ("y", y, u.shape, u.dtype))
-    with _on(dev):
+    with _on(dev, stream):
         if y is None:
             y = torch.empty(u.shape, dtype=u.dtype, device=dev)
         lz_scan_step(d, state, u, dt, A, Bm, Cm, Dskip, z, dt_bias, y, _stream_on(dev, stream))
@@ -894,7 +901,7 @@ def block_norm_fwd(o, *, w=None, z=None, s=None, r=None, w2=None, groups=1, eps=
     par = (d.D,)
     _whole(fn, dev, ("w", w, par, torch.float32), ("s", s, par, torch.float32),
            ("w2", w2, par, torch.float32))
-    with _on(dev):
+    with _on(dev, stream):
         out = torch.empty(d.B, d.T, d.D, dtype=o.dtype, device=dev)
         n = torch.empty_like(out) if w2 is not None else None
         lz_block_norm_fwd(d, o, w, z, s, r, w2, out, n, _stream_on(dev, stream))
@@ -914,7 +921,7 @@ def block_norm_bwd(o, *, w=None, z=None, s=None, w2=None, out=None, dout=None, d
            ("dn", dn, R, o.dtype))
     _need(dout is not None or dn is not None, fn, "dout or dn must be given")
     _need(dn is None or (out is not None and w2 is not None), fn, "dn needs out and w2")
-    with _on(dev):
+    with _on(dev, stream):
         rows = lambda: torch.empty(d.B, d.T, d.D, dtype=o.dtype, device=dev)
         par = lambda on: torch.empty(d.D, dtype=torch.float32, device=dev) if on else None
         do = torch.empty(o.shape, dtype=o.dtype, device=dev)

@@ -156,3 +156,32 @@ def test_attention_output_through_the_gated_norm():
     # one rounding to bf16 (2^-8 of each value) over everything else
     close("out", out, ref.detach().cpu(), 2.0 ** -8)
     close("do", got["do"], o64.grad.cpu(), 2.0 ** -8)
+
+
+def test_calls_on_another_stream_keep_their_scratch():
+    """Calls on a side stream while the current one allocates and fills memory
+    of the same sizes: what the side stream's kernels still use is not handed
+    out (their scratch is freed as soon as the call returns)."""
+    g = torch.Generator().manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g).cuda()
+    x, w, dy = r(2, 3000, 256), r(256, 4), r(2, 3000, 256)
+    o, wn = r(1, 4000, 512), r(512)
+    dt, A, bc = r(2, 3000, 256), -torch.rand(256, 16, generator=g).cuda(), r(2, 3000, 16)
+
+    def calls(stream=None):
+        out = [L.conv_bwd(x, w, dy, stream=stream), L.block_norm_bwd(o, w=wn, dout=o, stream=stream),
+               L.scan_bwd(x, dt, A, bc, bc, dy, stream=stream)]
+        return [t for d in out for t in d.values() if t is not None]
+
+    want = calls()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)  # the side stream's work starts late
+        side.wait_stream(torch.cuda.current_stream())
+        got = calls(handle)
+        for n in (1 << 12, 1 << 16, 1 << 20, 1 << 22, 1 << 24):
+            for _ in range(4):
+                torch.full((n,), float("nan"), device="cuda")
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
