@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
-         "--expt-relaxed-constexpr", f"-I{os.path.join(ROOT, 'include')}"]
+         "--expt-relaxed-constexpr", "--threads", "0",  # one compilation a core
+         f"-I{os.path.join(ROOT, 'include')}"]
 
 
 def sources():
