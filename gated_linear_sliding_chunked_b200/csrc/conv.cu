@@ -6,7 +6,7 @@
 // vector of neighbouring channels and walks a run of tokens with the last K-1
 // inputs in registers, so that a token is read once and only the K-1 tokens
 // before a run are read twice (they come out of L2).  At 2 x 8192 tokens, 4096
-// channels, 4 taps (bf16) the backward takes 98 to 102 us: 60 % of the copy
+// channels, 4 taps (bf16) the backward takes 98 us: 62 % of the copy
 // bandwidth; its 24 instructions an element and few resident warps (163
 // registers) hold it there.
 #include <type_traits>
@@ -402,15 +402,26 @@ struct StepLaunch {
   }
 };
 
-// tokens of a block of the backward
+// Tokens of a run of the backward, and blocks over a sequence.  The blocks come
+// in rounds of as many as the SMs hold at once (by registers, at 4 taps), and a
+// run costs its tokens and some 8 more to begin and end: the run whose rounds
+// cost the least.
 int bwd_blocks(const lz_conv_dims* d, int* run) {
-  // long runs re-read the least; short ones keep every SM busy (at least two
-  // blocks each) when there are few tokens and channels
-  int r = 128;
-  const int cb = (d->D + 127) / 128;
-  while (r > 8 && (size_t)d->B * cb * ((d->T + r * kWarps - 1) / (r * kWarps)) < 296) r /= 2;
-  *run = r;
-  return std::max(1, (d->T + r * kWarps - 1) / (r * kWarps));
+  const bool bf = d->io == LZ_BF16, vec = d->D % (bf ? 8 : 4) == 0;
+  const int64_t cols = (int64_t)d->B * ((d->D + (vec ? 127 : 31)) / (vec ? 128 : 32));
+  const int64_t slots = 148 * (vec ? bf ? 3 : 2 : 6);
+  int64_t best = 0;
+  int tb = 1;
+  for (int r = 256; r >= 8; r -= 8) {
+    const int n = std::max(1, (d->T + r * kWarps - 1) / (r * kWarps));
+    const int64_t cost = ((cols * n + slots - 1) / slots) * (r + 8);
+    if (!best || cost < best) {
+      best = cost;
+      *run = r;
+      tb = n;
+    }
+  }
+  return tb;
 }
 
 template <typename IO, int K, int VW>
