@@ -4,23 +4,22 @@
 // A row of D features stays in registers between its two norms: every input
 // is read once and every output written once, a few operations an element, so
 // HBM bandwidth bounds it (forward up to 5 values an element, backward up to
-// 8).  A thread holds E = 16 elements; up to 512 elements a row belongs to one
-// warp (no block-wide synchronisation), longer rows to a block.  The forward takes a row a block; the backward's
-// blocks walk the rows with a stride, the next row on its way to shared memory
-// while this one is worked on, so that the parameter gradients stay in registers
-// and leave as one partial per block.  At 2 x 8192 rows of 4096 (bf16): forward
-// by 32 heads with a gate 76 to 80 us (77 % of the copy bandwidth), backward of
-// everything 250 us (65 %: two sums over a row, with a barrier each, between its
-// loads and its stores).
+// 8).  A thread holds 16 elements; up to 512 elements a row belongs to 4 to 32
+// lanes of a warp (no block-wide synchronisation), longer rows to a block.  The
+// forward takes a row a team; the backward's blocks walk the rows with a stride,
+// the next row on its way to shared memory while this one is worked on, so that
+// the parameter gradients stay in registers and leave as one partial per block.
+// At 2 x 8192 rows of 4096 (bf16): forward by 32 heads with a gate 76 to 80 us
+// (77 % of the copy bandwidth), backward of everything 246 to 254 us (66 %: two
+// sums over a row, with a barrier each, between its loads and its stores); rows
+// of 1024: backward 68 us (60 %).
 #include "layer.cuh"
 
 namespace lz {
 namespace {
 
-constexpr int E = 16;         // elements of a thread
-constexpr int kMaxD = 16384;  // 1024 threads
-constexpr int kWarpD = 512;   // rows of a warp: 16 elements a lane
-constexpr int kRowWarps = 4;  // rows of a block of one-warp rows
+constexpr int kMaxD = 16384;  // 1024 threads of 16 elements
+constexpr int kWarpBlock = 128;  // threads of a block whose rows belong to (parts of) warps
 
 inline int shift_of(int n) {
   int s = 0;
@@ -55,16 +54,24 @@ struct NormParams {
   void* dr;
   float* part;  // [blocks][3][D]: dw, ds, dw2
   int ring;     // floats of shared memory in front of the rows in flight
+  int team, tshift;  // lanes of a row that belongs to a warp or a part of one, log2 of it
 };
 
-// Sums of M values over the team that holds a row: its warp, or its block.  One
-// barrier: a caller alternates between two `red` of M * 32 floats, so that a
-// buffer is written again only after a barrier that its readers have passed.
+// Sums of M values over the team that holds a row: 4 to 32 lanes of a warp, or a
+// block.  One barrier: a caller alternates between two `red` of M * 32 floats, so
+// that a buffer is written again only after a barrier that its readers have passed.
 template <bool WARP, int M>
-__device__ __forceinline__ void team_sum(float (&v)[M], float* red) {
+__device__ __forceinline__ void team_sum(float (&v)[M], int team, float* red) {
+  if constexpr (WARP) {
 #pragma unroll
-  for (int i = 0; i < M; ++i) v[i] = warp_sum(v[i]);
-  if constexpr (!WARP) {
+    for (int o = 16; o > 0; o >>= 1)
+      if (team > o) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = warp_sum(v[i]);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
     if (lane < M) {
       float x = v[0];
@@ -79,7 +86,7 @@ __device__ __forceinline__ void team_sum(float (&v)[M], float* red) {
 }
 
 // Per-vector partial sums ps[k] -> the sum over each vector's group
-template <int VW, bool WARP, int MODE>
+template <int E, int VW, bool WARP, int MODE>
 __device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int lane, int team, float* red,
                                           float* sm) {
   constexpr int NV = E / VW;
@@ -88,7 +95,7 @@ __device__ __forceinline__ void group_sum(const NormParams& p, float* ps, int la
     float a[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < NV; ++k) a[0] += ps[k];
-    team_sum<WARP>(a, red);
+    team_sum<WARP>(a, team, red);
 #pragma unroll
     for (int k = 0; k < NV; ++k) ps[k] = a[0];
   } else if constexpr (MODE == GROUP_LANES) {
@@ -144,20 +151,29 @@ __device__ __forceinline__ RowAt<IO> row_at(const NormParams& p, IO* base, const
   return {base + (p.heads ? b * p.G * head + (int64_t)t * dv : (int64_t)so.at(b, t)), head, dv, p.dshift, p.heads};
 }
 
-// FULL: every thread has E features (D is the team's threads times E)
-template <typename IO, int VW, bool WARP, int MODE, bool FULL, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 5 : 1) norm_fwd_kernel(NormParams p) {
+// Blocks of 256 threads that share an SM in the forward.  16-bit rows of 4096
+// features: five (2 x 8192 rows of 32 groups: 80 us against 86 us with the four
+// that 60 registers would allow); the others need more registers.
+template <typename IO, int VW>
+constexpr int kFwdBlocks = VW == 1 ? 4 : sizeof(IO) == 4 ? 3 : 5;
+
+// E: elements of a thread.  FULL: every thread has E features (D is the team's
+// threads times E).
+template <typename IO, int E, int VW, bool WARP, int MODE, bool FULL, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? kFwdBlocks<IO, VW> : 1) norm_fwd_kernel(NormParams p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ float red[2][3 * 32];
   constexpr int NV = E / VW;
   using V = Vec<VW>;
-  const int team = WARP ? 32 : blockDim.x;
-  const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+  const int team = WARP ? p.team : blockDim.x;
+  const int lane = WARP ? threadIdx.x & (team - 1) : threadIdx.x;
   const int nvec = p.D / VW;
-  auto has = [&](int k) { return FULL || k * team + lane < nvec; };
+  const int b = blockIdx.y;
+  const unsigned ut = WARP ? blockIdx.x * (kWarpBlock >> p.tshift) + (threadIdx.x >> p.tshift) : blockIdx.x;
+  const int t = (int)ut;
+  const bool live = !WARP || ut < (unsigned)p.T;  // (the lanes of a warp stay together for its sums)
+  auto has = [&](int k) { return live && (FULL || k * team + lane < nvec); };
   auto col = [&](int k) { return (k * team + lane) * VW; };
-  const int b = blockIdx.y, t = WARP ? blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-  if (t >= p.T) return;
   const int64_t row = ((int64_t)b * p.T + t) * p.D;
   const auto o = row_at<const IO>(p, (const IO*)p.o, p.so, b, t);
   const IO* pz = p.z ? (const IO*)p.z + p.sz.at(b, t) : nullptr;
@@ -184,7 +200,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 5 : 1) norm_fwd_kernel(Nor
       q.mul(x[k], x[k]);
       ps[k] = q.sum();
     }
-    group_sum<VW, WARP, MODE>(p, ps, lane, team, red[0], sm);
+    group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red[0], sm);
     const float ig = (float)p.G / (float)p.D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -229,7 +245,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 5 : 1) norm_fwd_kernel(Nor
     }
   }
   if (p.w2) {
-    team_sum<WARP>(ss, red[1]);
+    team_sum<WARP>(ss, team, red[1]);
     V rs;
     rs.fill(rsqrtf(ss[0] / (float)p.D + p.eps));
 #pragma unroll
@@ -249,19 +265,23 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 5 : 1) norm_fwd_kernel(Nor
 // and with mh = o rs, core = mh w, f = e s:
 //   ds = sum e core silu(z)     dz = f core silu'(z)     dw = sum f silu(z) mh
 //   do = rs (k - mh mean_group(k mh)),  k = f silu(z) w
-template <typename IO, int VW, bool WARP, int MODE, bool FULL, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(NormParams p) {
+template <typename IO, int E, int VW, bool WARP, int MODE, bool FULL, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 512 ? (VW == 1 ? 768 : 512) / MAXT : 1) norm_bwd_kernel(NormParams p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ float red[2][3 * 32];
   constexpr int NV = E / VW;
   using V = Vec<VW>;
-  const int team = WARP ? 32 : blockDim.x;
-  const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+  const int team = WARP ? p.team : blockDim.x;
+  const int lane = WARP ? threadIdx.x & (team - 1) : threadIdx.x;
   const int nvec = p.D / VW;
-  auto has = [&](int k) { return FULL || k * team + lane < nvec; };
   auto col = [&](int k) { return (k * team + lane) * VW; };
-  const int64_t row0 = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-  const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
+  // a warp's rows follow one another: it goes on while the first is there
+  const int sub = WARP ? (threadIdx.x & 31) >> p.tshift : 0;
+  const int64_t row0 = WARP ? (((int64_t)blockIdx.x * kWarpBlock + threadIdx.x) >> p.tshift) - sub : blockIdx.x;
+  const int64_t step = WARP ? (int64_t)gridDim.x * (kWarpBlock >> p.tshift) : gridDim.x;
+  auto there = [&](int64_t row, int k) {
+    return (!WARP || row < p.rows) && (FULL || k * team + lane < nvec);
+  };
   const float ig = (float)p.G / (float)p.D, id = 1.f / (float)p.D;
   const Rows cont{p.D, (int64_t)p.T * p.D};
   // sum over the rows of e silu(z) mh: times s it is dw, times w ds
@@ -273,20 +293,22 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
   }
   // RING: the next row is copied to shared memory while this one is worked on,
   // every thread its own vectors (so that no barrier is needed); in registers it
-  // would cost 40 of them
-  constexpr bool RING = VW > 1 && !WARP && MAXT <= 512;
+  // would cost 40 of them.  (The threads' vectors lie side by side: where a
+  // thread's own did, the copies of a warp's 512 bytes went to 32 places and the
+  // whole took 380 us, not 250.)
+  constexpr bool RING = VW > 1 && MAXT <= 512;
   enum { O, Z, OUT, DOUT, DN, N_IN };
   struct In {
     Raw<IO, VW> v[N_IN][NV];
   };
   In in;
-  uint4* ring = reinterpret_cast<uint4*>(sm + p.ring);  // [2][N_IN][NV][threads]
-  auto slot = [&](int st, int i, int k) -> uint4* {
-    return ring + ((st * N_IN + i) * NV + k) * MAXT + threadIdx.x;
-  };
+  uint4* ring = reinterpret_cast<uint4*>(sm + p.ring) + threadIdx.x;  // [2][N_IN][NV][threads]
+  const int bd = WARP ? kWarpBlock : blockDim.x;
+  auto slot = [&](int st, int i, int k) -> uint4* { return ring + ((st * N_IN + i) * NV + k) * bd; };
   auto fetch = [&](int64_t row, int st) {
     const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
     const size_t at = (size_t)row * p.D;
+    auto has = [&](int k) { return there(row, k); };
     auto one = [&](int i, int k, const IO* q) {
       if constexpr (RING) {
         if (has(k)) cp_async<16>(slot(st, i, k), q);
@@ -316,6 +338,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
     if constexpr (RING) cp_commit();
   };
   int st = 0;
+  int64_t row = row0 + sub;
+  auto has = [&](int k) { return there(row, k); };
   auto val = [&](int i, int k) -> V {
     if constexpr (RING) {
       Raw<IO, VW> r;
@@ -327,10 +351,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
     }
   };
   int turn = 0;  // of the two buffers of the block's sums
-  if (RING && row0 < p.rows) fetch(row0, 0);
-  for (int64_t row = row0; row < p.rows; row += step, st ^= RING) {
+  if (RING && row0 < p.rows) fetch(row, 0);
+  for (; row - sub < p.rows; row += step, st ^= RING) {
     if constexpr (RING) {
-      if (row + step < p.rows) {
+      if (row - sub + step < p.rows) {
         fetch(row + step, st ^ 1);
         cp_wait<1>();
       } else {
@@ -370,14 +394,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
       for (int k = 0; k < NV; ++k) sums[2] += ps[k];
     }
     if (p.dn || (MODE == GROUP_ROW && p.w)) {
-      team_sum<WARP>(sums, red[turn]);
+      team_sum<WARP>(sums, team, red[turn]);
       turn ^= 1;
     }
     if constexpr (MODE == GROUP_ROW) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) ps[k] = sums[2];
     } else {
-      if (p.w) group_sum<VW, WARP, MODE>(p, ps, lane, team, nullptr, sm);
+      if (p.w) group_sum<E, VW, WARP, MODE>(p, ps, lane, team, nullptr, sm);
     }
     if (p.dn) {
       const float r2s = rsqrtf(sums[0] * id + p.eps);
@@ -447,7 +471,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
       ps[k] = q.sum();
     }
     if (p.w) {
-      group_sum<VW, WARP, MODE>(p, ps, lane, team, red[turn], sm);
+      group_sum<E, VW, WARP, MODE>(p, ps, lane, team, red[turn], sm);
       turn ^= MODE == GROUP_ROW;
     }
     const int b = (int)((unsigned)row / (unsigned)p.T), t = (int)row - b * p.T;
@@ -467,8 +491,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
       r.put(d_o.at(col(k)));
     }
   }
-  // ---- the block's partials; the warps of a warp-per-row block are added in
-  // order in shared memory
+  // ---- the block's partials; the teams of a block of several rows are added
+  // in order in shared memory
   auto value = [&](int q, int i, int c) {
     const float a = q == 2 ? dw2[i / VW].get(i % VW) : sm0[i / VW].get(i % VW);
     const float* f = q == 0 ? p.s : q == 1 ? p.w : nullptr;
@@ -478,17 +502,16 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
   for (int q = 0; q < 3; ++q) {
     float* part = p.part + ((size_t)blockIdx.x * 3 + q) * p.D;
     if constexpr (WARP) {
-      const int warp = threadIdx.x / 32, nw = blockDim.x / 32;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const int c = (i / VW * 32 + lane) * VW + i % VW;
-        if (c < p.D) sm[warp * p.D + c] = value(q, i, c);
+        const int c = (i / VW * team + lane) * VW + i % VW;
+        if (c < p.D) sm[(threadIdx.x >> p.tshift) * p.D + c] = value(q, i, c);
       }
       __syncthreads();
-      for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
+      for (int c = threadIdx.x; c < p.D; c += kWarpBlock) {
         float tot = 0.f;
-        for (int w = 0; w < nw; ++w) tot += sm[w * p.D + c];
+        for (int w = 0; w < kWarpBlock >> p.tshift; ++w) tot += sm[w * p.D + c];
         part[c] = tot;
       }
     } else {
@@ -497,7 +520,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
         const int v = k * team + lane;
         if (v < nvec) {
 #pragma unroll
-          for (int j = 0; j < VW; ++j) part[v * VW + j] = value(q, k * VW + j, v * VW + j);
+          for (int j = 0; j < VW; j += VW < 4 ? 1 : 4) {
+            float f[VW < 4 ? 1 : 4];
+#pragma unroll
+            for (int i = 0; i < (VW < 4 ? 1 : 4); ++i) f[i] = value(q, k * VW + j + i, v * VW + j + i);
+            if constexpr (VW < 4) part[v * VW + j] = f[0];
+            else *reinterpret_cast<float4*>(part + v * VW + j) = make_float4(f[0], f[1], f[2], f[3]);
+          }
         }
       }
     }
@@ -507,24 +536,34 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(Nor
 // ---- host -----------------------------------------------------------------
 
 struct Shape {
-  bool vec, warp;
-  bool full;  // every thread of a team has E features
-  int vw, threads, mode;
+  bool warp;    // rows belong to warps or parts of them
+  bool full;    // every thread of a team has E features
+  int e, vw;    // elements of a thread, of a vector
+  int team;     // threads of a row
+  int threads;  // of a block
+  int mode;
   size_t smem;  // of the group sums
 };
 
-Shape shape_of(const lz_norm_dims* d, bool vec) {
+// 16 elements a thread; fewer, up to 4096 features, where vectors are single
+// elements, whose unpacked values take more registers (8192 rows of 1001 16-bit
+// features: forward 8 elements 45 us, 4 elements 51, 16 elements 76; backward 125,
+// 109 and 219 us).
+Shape shape_of(const lz_norm_dims* d, bool vec, bool bwd) {
   Shape s;
-  s.vec = vec;
   s.vw = vec ? (int)(16 / esize(d->io)) : 1;
+  s.e = vec || d->D > 4096 ? 16 : bwd ? 4 : 8;
   const int nvec = d->D / s.vw;
   const int gd = d->D / d->G;
   const int gv = gd % s.vw == 0 ? gd / s.vw : 0;
   s.mode = d->G == 1 ? GROUP_ROW : (gv >= 1 && gv <= 32 && (gv & (gv - 1)) == 0) ? GROUP_LANES : GROUP_SMEM;
-  s.warp = d->D <= kWarpD && s.mode != GROUP_SMEM;
-  s.threads = s.warp ? kRowWarps * 32 : (nvec * s.vw + E - 1) / E;
-  s.threads = (s.threads + 31) / 32 * 32;
-  s.full = vec && d->D == (s.warp ? 32 : s.threads) * E;
+  // short rows: a power-of-two part of a warp each, no smaller than a group
+  int lanes = 4;
+  while (lanes * s.e < d->D || (s.mode == GROUP_LANES && lanes < gv)) lanes *= 2;
+  s.warp = lanes <= 32 && s.mode != GROUP_SMEM;
+  s.team = s.warp ? lanes : ((d->D + s.e - 1) / s.e + 31) / 32 * 32;
+  s.threads = s.warp ? kWarpBlock : s.team;
+  s.full = vec && d->D == s.team * s.e;
   s.smem = s.mode == GROUP_SMEM ? (size_t)(nvec + d->G) * sizeof(float) : 0;
   return s;
 }
@@ -540,22 +579,23 @@ int grid_rows(Kern k, int64_t rows, int threads, size_t smem, int rows_per_block
 }
 
 template <typename IO, int VW, bool WARP, int MODE>
-cudaError_t go_fwd(const NormParams& p, const Shape& sh, cudaStream_t s) {
-  // five blocks an SM up to 4096 features (2 x 8192 rows of 32 groups: 80 us
-  // against 86 us with the four that 60 registers would allow)
-  constexpr int kT = WARP ? kRowWarps * 32 : 256;
-  auto k = norm_fwd_kernel<IO, VW, WARP, MODE, false, kT>;
+cudaError_t go_fwd(NormParams p, const Shape& sh, cudaStream_t s) {
+  constexpr int kT = WARP ? kWarpBlock : 256;
+  constexpr int kE = VW > 1 ? 16 : 8;
+  p.team = sh.team;
+  p.tshift = shift_of(sh.team);
+  auto k = norm_fwd_kernel<IO, kE, VW, WARP, MODE, false, kT>;
   if constexpr (VW > 1) {
-    if (sh.full) k = norm_fwd_kernel<IO, VW, WARP, MODE, true, kT>;
+    if (sh.full) k = norm_fwd_kernel<IO, kE, VW, WARP, MODE, true, kT>;
   }
   if constexpr (!WARP) {
-    if (sh.threads > kT) k = norm_fwd_kernel<IO, VW, WARP, MODE, false, 1024>;
+    if (sh.threads > kT) k = norm_fwd_kernel<IO, kE, VW, WARP, MODE, false, 1024>;
+    if (sh.e != kE) k = norm_fwd_kernel<IO, 16, VW, WARP, MODE, false, 1024>;
   }
-  if (sh.smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
-    if (e != cudaSuccess) return e;
-  }
-  const dim3 grid(WARP ? (p.T + kRowWarps - 1) / kRowWarps : p.T, p.B);
+  const cudaError_t e = want_smem(k, sh.smem);
+  if (e != cudaSuccess) return e;
+  const int rpb = sh.threads / sh.team;
+  const dim3 grid((p.T + rpb - 1) / rpb, p.B);
   ScopedTiming tm("block_norm_fwd", s);
   k<<<grid, sh.threads, sh.smem, s>>>(p);
   return cudaGetLastError();
@@ -567,30 +607,32 @@ int bwd_part_rows(int64_t rows) { return (int)std::min<int64_t>(std::max<int64_t
 
 template <typename IO, int VW, bool WARP, int MODE>
 cudaError_t go_bwd(NormParams p, const Shape& sh, int* blocks, cudaStream_t s) {
-  size_t smem = WARP ? std::max(sh.smem, (size_t)kRowWarps * p.D * sizeof(float)) : sh.smem;
-  // two blocks an SM up to 4096 features, so that one works while the other
-  // waits for its sums; longer rows need blocks of up to 1024 threads
-  constexpr int kT = WARP ? kRowWarps * 32 : 256;
-  auto k = norm_bwd_kernel<IO, VW, WARP, MODE, false, kT>;
+  const int rpb = sh.threads / sh.team;
+  size_t smem = WARP ? (size_t)rpb * p.D * sizeof(float) : sh.smem;
+  constexpr int kT = WARP ? kWarpBlock : 256;
+  constexpr int kE = VW > 1 ? 16 : 4;
+  p.team = sh.team;
+  p.tshift = shift_of(sh.team);
+  p.ring = (int)((smem + 15) / 16 * 4);
+  // two rows in flight beside the sums' scratch
+  const size_t ring = (size_t)p.ring * 4 + 2 * 16 * 5 * (kE / VW) * (size_t)sh.threads;
+  auto k = norm_bwd_kernel<IO, kE, VW, WARP, MODE, false, kT>;
   if constexpr (VW > 1) {
-    if (sh.full) k = norm_bwd_kernel<IO, VW, WARP, MODE, true, kT>;
+    if (sh.full) k = norm_bwd_kernel<IO, kE, VW, WARP, MODE, true, kT>;
   }
+  bool ringed = VW > 1;
   if constexpr (!WARP) {
-    const int T = sh.threads > 256 ? 512 : 256;
-    p.ring = (int)((smem + 15) / 16 * 4);
-    // two rows in flight beside the sums' scratch, where they fit
-    const size_t ring = (size_t)p.ring * 4 + 2 * 5 * (E / VW) * (size_t)T * 16;
-    const bool fits = VW > 1 && sh.threads <= 512 && ring <= 200 * 1024;
-    if (sh.threads > 256 && fits) k = norm_bwd_kernel<IO, VW, WARP, MODE, false, 512>;
-    if (!fits && (VW > 1 || sh.threads > 512)) k = norm_bwd_kernel<IO, VW, WARP, MODE, false, 1024>;
-    if (!fits && VW == 1 && sh.threads > 256 && sh.threads <= 512) k = norm_bwd_kernel<IO, VW, WARP, MODE, false, 512>;
-    if (fits) smem = ring;
+    if (sh.threads > kT) k = norm_bwd_kernel<IO, kE, VW, WARP, MODE, false, (VW > 1 ? 512 : 1024)>;
+    // rows too long for that
+    if (VW > 1 ? sh.threads > 512 || ring > 200 * 1024 : sh.e != kE) {
+      k = norm_bwd_kernel<IO, 16, VW, WARP, MODE, false, 1024>;
+      ringed = false;
+    }
   }
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  const int grid = std::min(grid_rows(k, p.rows, sh.threads, smem, WARP ? kRowWarps : 1), bwd_part_rows(p.rows));
+  if (ringed) smem = ring;
+  const cudaError_t e = want_smem(k, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = std::min(grid_rows(k, p.rows, sh.threads, smem, rpb), bwd_part_rows(p.rows));
   *blocks = grid;
   ScopedTiming tm("block_norm_bwd", s);
   k<<<grid, sh.threads, smem, s>>>(p);
@@ -600,9 +642,9 @@ cudaError_t go_bwd(NormParams p, const Shape& sh, int* blocks, cudaStream_t s) {
 #define LZ_NORM_DISPATCH(CALL)                                              \
   do {                                                                      \
     if (d->io == LZ_BF16) {                                                 \
-      if (sh.vec) LZ_NORM_MODE(CALL, bf16, 8) else LZ_NORM_MODE(CALL, bf16, 1) \
+      if (sh.vw > 1) LZ_NORM_MODE(CALL, bf16, 8) else LZ_NORM_MODE(CALL, bf16, 1) \
     } else {                                                                \
-      if (sh.vec) LZ_NORM_MODE(CALL, float, 4) else LZ_NORM_MODE(CALL, float, 1) \
+      if (sh.vw > 1) LZ_NORM_MODE(CALL, float, 4) else LZ_NORM_MODE(CALL, float, 1) \
     }                                                                       \
   } while (0)
 #define LZ_NORM_MODE(CALL, IO, VW)                                          \
@@ -671,7 +713,7 @@ extern "C" lz_status lz_block_norm_fwd(const lz_norm_dims* d, const void* o, con
   p.sz = rows_of(d->z, d->T, d->D);
   p.sr = rows_of(d->r, d->T, d->D);
   p.o = o; p.w = w; p.z = z; p.s = s; p.r = r; p.w2 = w2; p.out = out; p.n = n;
-  const Shape sh = shape_of(d, norm_vec(d, p));
+  const Shape sh = shape_of(d, norm_vec(d, p), false);
   cudaError_t e = cudaSuccess;
 #define LZ_CALL(IO, VW, WARP, MODE) go_fwd<IO, VW, WARP, MODE>(p, sh, (cudaStream_t)stream)
   LZ_NORM_DISPATCH(LZ_CALL);
@@ -708,7 +750,7 @@ extern "C" lz_status lz_block_norm_bwd(const lz_norm_dims* d, const void* o, con
   p.sz = rows_of(d->z, d->T, d->D);
   p.o = o; p.w = w; p.z = z; p.s = s; p.w2 = w2; p.out = const_cast<void*>(out);
   p.dout = dout; p.dn = dn; p.d_o = dOo; p.dz = dz; p.dr = dr; p.part = (float*)ws;
-  const Shape sh = shape_of(d, norm_vec(d, p));
+  const Shape sh = shape_of(d, norm_vec(d, p), true);
   cudaError_t e = cudaSuccess;
   int blocks = 0;
 #define LZ_CALL(IO, VW, WARP, MODE) go_bwd<IO, VW, WARP, MODE>(p, sh, &blocks, (cudaStream_t)stream)

@@ -305,6 +305,13 @@ __device__ __forceinline__ int seq_len(const int64_t* lens, int b, int T) {
 
 // ---- host -----------------------------------------------------------------
 
+// Shared memory beyond 48 KB has to be asked for
+template <class Kern>
+inline cudaError_t want_smem(Kern k, size_t smem) {
+  return smem > 48 * 1024 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                          : cudaSuccess;
+}
+
 inline lz_status layer_fail(lz_status st, const char* fmt, ...) {
   char buf[256];
   va_list ap;

@@ -206,13 +206,6 @@ constexpr int row_of(int CH, int x) { return CH + (x - CH % 32 + 32) % 32; }
 // are written in vectors of 4
 __host__ __device__ inline size_t part_ld(int D, int N) { return ((size_t)D * (N + 2) + 3) / 4 * 4; }
 
-// Shared memory beyond 48 KB has to be asked for
-template <class Kern>
-inline cudaError_t want_smem(Kern k, size_t smem) {
-  return smem > 48 * 1024 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-                          : cudaSuccess;
-}
-
 // N rounded up to a power of two, at least 4
 inline int states_of(int N) {
   int n = 4;

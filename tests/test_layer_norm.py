@@ -57,6 +57,18 @@ CASES = [  # dtype, B, T, D, G, parts, heads, strided
     (F, 2, 2, 9001, 1, ALL, False, False),
     (F, 1, 700, 72, 1, ("z", "s"), False, False),
     (F, 1, 2, 16384, 2, ("w", "w2"), False, False),
+    # rows on parts of a warp, the last of them past the end; rows that the same lanes come back to
+    (BF, 3, 67, 64, 1, ALL, False, False),
+    (BF, 2, 37, 128, 2, ALL, True, False),
+    (F, 2, 45, 64, 2, ALL, False, False),       # the groups ask for 8 lanes, the row for 4
+    (BF, 1, 131, 200, 1, ALL, False, True),
+    (F, 2, 21, 100, 1, ALL, False, False),
+    (BF, 1, 20011, 64, 1, ALL, False, False),
+    (BF, 4, 33, 250, 1, ALL, False, False),
+    (F, 2, 19, 50, 2, ALL, False, True),
+    (BF, 1, 3, 2501, 1, ALL, False, False),
+    (BF, 1, 2, 5001, 3, ALL, False, False),
+    (BF, 2, 301, 8192, 1, ALL, False, False),
 ]
 
 
