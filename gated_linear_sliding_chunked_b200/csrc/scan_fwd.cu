@@ -1,6 +1,6 @@
 // Selective state space scan, forward and single tokens.
 //
-// Per (token, channel, state): one exp (16 a cycle and SM) and some 8 more
+// Per (token, channel, state): one exp (16 a cycle and SM) and some 10 more
 // instructions with everything counted, against 8 bytes a (token, channel):
 // bound by the special-function unit and the issue slots.  At 2 x 8192 tokens,
 // 4096 channels, 16 states (bf16, gated) 515 to 537 us: 54 to 56 % of the
