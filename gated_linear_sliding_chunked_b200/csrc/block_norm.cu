@@ -595,7 +595,7 @@ cudaError_t go_fwd(NormParams p, const Shape& sh, cudaStream_t s) {
   const cudaError_t e = want_smem(k, sh.smem);
   if (e != cudaSuccess) return e;
   const int rpb = sh.threads / sh.team;
-  const dim3 grid((p.T + rpb - 1) / rpb, p.B);
+  const dim3 grid((p.T - 1) / rpb + 1, p.B);
   ScopedTiming tm("block_norm_fwd", s);
   k<<<grid, sh.threads, sh.smem, s>>>(p);
   return cudaGetLastError();

@@ -356,18 +356,20 @@ lz_status check_conv(const char* fn, const lz_conv_dims* d) {
   return LZ_OK;
 }
 
-// Vectors of 16 bytes where rows and pointers allow it, else single elements
-bool conv_vec(const lz_conv_dims* d, const void* x, const Rows& r) {
-  const int vw = d->io == LZ_BF16 ? 8 : 4;
+// Vectors of vw elements where rows and pointers allow it, else single elements
+bool conv_vec(const lz_conv_dims* d, const void* x, const Rows& r, int vw) {
   return d->D % vw == 0 && rows_vec(x, r, vw, esize(d->io));
 }
 
-template <template <typename, int, int> class Launch, typename P>
+// Over sequences 4 channels a thread: with 8 the forward takes 128 registers, not
+// 78 (4 taps, 16 bits; 2 x 8192 x 4096: 70 us against 59), and the backward's
+// windows do not fit.  BFV: those of a 16-bit vector.
+template <template <typename, int, int> class Launch, int BFV, typename P>
 cudaError_t dispatch_k(const P& p, int K, bool bf, bool vec, cudaStream_t s) {
   switch (K) {
-#define LZ_K(k)                                                                       \
-  case k:                                                                             \
-    if (bf) return vec ? Launch<bf16, k, 8>::go(p, s) : Launch<bf16, k, 1>::go(p, s); \
+#define LZ_K(k)                                                                         \
+  case k:                                                                               \
+    if (bf) return vec ? Launch<bf16, k, BFV>::go(p, s) : Launch<bf16, k, 1>::go(p, s); \
     return vec ? Launch<float, k, 4>::go(p, s) : Launch<float, k, 1>::go(p, s);
     LZ_K(1) LZ_K(2) LZ_K(3) LZ_K(4) LZ_K(5) LZ_K(6) LZ_K(7) LZ_K(8)
 #undef LZ_K
@@ -379,11 +381,9 @@ template <typename IO, int K, int VW>
 struct FwdLaunch {
   static cudaError_t go(const ConvParams& p, cudaStream_t s) {
     const size_t nrun = std::max(1, (p.T + p.run - 1) / p.run);
-    // 8-byte vectors of 4 taps: 78 registers, not 128 (2 x 8192 x 4096 bf16: 59 us against 70)
-    constexpr int W = VW == 8 ? 4 : VW;
-    const dim3 grid((unsigned)((nrun * (p.D / W) + NT - 1) / NT), p.B);
+    const dim3 grid((unsigned)((nrun * (p.D / VW) + NT - 1) / NT), p.B);
     ScopedTiming tm("conv_fwd", s);
-    conv_fwd_kernel<IO, K, W><<<grid, NT, 0, s>>>(p);
+    conv_fwd_kernel<IO, K, VW><<<grid, NT, 0, s>>>(p);
     return cudaGetLastError();
   }
 };
@@ -409,9 +409,9 @@ struct StepLaunch {
 // run costs its tokens and some 8 more to begin and end: the run whose rounds
 // cost the least.
 int bwd_blocks(const lz_conv_dims* d, int* run) {
-  const bool bf = d->io == LZ_BF16, vec = d->D % (bf ? 8 : 4) == 0;
+  const bool vec = d->D % 4 == 0;
   const int64_t cols = (int64_t)d->B * ((d->D + (vec ? 127 : 31)) / (vec ? 128 : 32));
-  const int64_t slots = 148 * (vec ? bf ? 3 : 2 : 6);
+  const int64_t slots = 148 * (!vec ? 6 : d->io == LZ_BF16 ? 3 : 2);
   int64_t best = 0;
   int tb = 1;
   for (int r = 256; r >= 8; r -= 8) {
@@ -429,12 +429,11 @@ int bwd_blocks(const lz_conv_dims* d, int* run) {
 template <typename IO, int K, int VW>
 struct BwdLaunch {
   static cudaError_t go(const ConvBwdParams& q, cudaStream_t s) {
-    constexpr int W = VW == 8 ? 4 : VW;  // 8-byte vectors: the windows of 8 channels do not fit
     const ConvParams& p = q.f;
     const int tb = std::max(1, (p.T + p.run * kWarps - 1) / (p.run * kWarps));
-    const dim3 grid((p.D + 32 * W - 1) / (32 * W), tb, p.B);
+    const dim3 grid((p.D + 32 * VW - 1) / (32 * VW), tb, p.B);
     ScopedTiming tm("conv_bwd", s);
-    conv_bwd_kernel<IO, K, W><<<grid, kWarps * 32, 0, s>>>(q);
+    conv_bwd_kernel<IO, K, VW><<<grid, kWarps * 32, 0, s>>>(q);
     return cudaGetLastError();
   }
 };
@@ -464,12 +463,12 @@ extern "C" lz_status lz_conv_fwd(const lz_conv_dims* d, const void* x, const flo
   if (st == LZ_OK) st = check_distinct(fn, {y, xT}, {x, x0});
   if (st != LZ_OK) return st;
   ConvParams p{d->B, d->T, d->D, d->silu, RT, rows_of(d->x, d->T, d->D), x, w, bias, x0, lens, y, xT};
-  const bool vec = conv_vec(d, x, p.x);
+  const bool vec = conv_vec(d, x, p.x, 4);
   // long runs re-read less of the input (K - 1 tokens each, from L2); with few
   // of them runs of RT tokens put more threads on the machine
   const size_t vecs = d->D / (vec ? 4 : 1);
   while (p.run < 4 * RT && (size_t)d->B * ((d->T + 2 * p.run - 1) / (2 * p.run)) * vecs >= 148 * 2048) p.run *= 2;
-  return layer_done(dispatch_k<FwdLaunch>(p, d->K, d->io == LZ_BF16, vec, (cudaStream_t)stream), fn);
+  return layer_done(dispatch_k<FwdLaunch, 4>(p, d->K, d->io == LZ_BF16, vec, (cudaStream_t)stream), fn);
 }
 
 extern "C" lz_status lz_conv_bwd(const lz_conv_dims* d, const void* x, const float* w, const float* bias,
@@ -496,7 +495,7 @@ extern "C" lz_status lz_conv_bwd(const lz_conv_dims* d, const void* x, const flo
                   dy, dxT, dx, dx0, (float*)ws};
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  if (d->B > 0) e = dispatch_k<BwdLaunch>(q, d->K, d->io == LZ_BF16, conv_vec(d, x, q.f.x), s);
+  if (d->B > 0) e = dispatch_k<BwdLaunch, 4>(q, d->K, d->io == LZ_BF16, conv_vec(d, x, q.f.x, 4), s);
   if (e == cudaSuccess)
     e = launch_sum_rows({(const float*)ws, d->B * tb, (size_t)d->D * (d->K + 1), dw, (size_t)d->D * d->K, dbias,
                          (size_t)d->D, nullptr, 0},
@@ -516,5 +515,5 @@ extern "C" lz_status lz_conv_step(const lz_conv_dims* d, void* hist, const void*
   if (st != LZ_OK) return st;
   StepParams q{{d->B, 1, d->D, d->silu, RT, rows_of(d->x, 1, d->D), x, w, bias, nullptr, nullptr, y, nullptr}, hist};
   return layer_done(
-      dispatch_k<StepLaunch>(q, d->K, d->io == LZ_BF16, conv_vec(d, x, q.p.x), (cudaStream_t)stream), fn);
+      dispatch_k<StepLaunch, 8>(q, d->K, d->io == LZ_BF16, conv_vec(d, x, q.p.x, (int)(16 / esize(d->io))), (cudaStream_t)stream), fn);
 }

@@ -185,3 +185,35 @@ def test_calls_on_another_stream_keep_their_scratch():
                 torch.full((n,), float("nan"), device="cuda")
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("D", [48, 1024, 2056, 37])
+def test_captured_norms_and_convolutions_replay(D):
+    """Forward and backward in one CUDA graph, replayed on new inputs: the bits of the eager calls."""
+    gen = torch.Generator().manual_seed(D)
+    r = lambda *s: torch.randn(*s, generator=gen).cuda()
+    make = lambda: dict(x=r(2, 21, D).bfloat16(), z=r(2, 21, D).bfloat16(), w=r(D), wc=r(D, 4), b=r(D),
+                        x0=r(2, 3, D).bfloat16(), dy=r(2, 21, D).bfloat16())
+
+    def call(v):
+        y, xT = L.conv_fwd(v["x"], v["wc"], v["b"], v["x0"], want_xT=True)
+        out, n = L.block_norm_fwd(y, w=v["w"], z=v["z"], r=v["x"], w2=v["b"])
+        g = L.block_norm_bwd(y, w=v["w"], z=v["z"], w2=v["b"], out=out, dn=v["dy"], want_dr=True)
+        c = L.conv_bwd(v["x"], v["wc"], g["do"], v["b"], v["x0"], want_dx0=True)
+        return [y, xT, out, n] + [t for d in (g, c) for t in d.values() if t is not None]
+
+    a, b = make(), make()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(a)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(a)
+    want = call(b)
+    for k in a:
+        a[k].copy_(b[k])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))

@@ -40,6 +40,8 @@ CASES = [  # dtype, B, T, D, K, lens, strided, bias, hist, silu
     (torch.bfloat16, 2, 65, 40, 3, [2, 64], True, False, True, False),
     (torch.bfloat16, 1, 50, 13, 4, None, True, True, True, True),
     (torch.bfloat16, 2, 300, 128, 8, [299, 7], False, True, True, True),
+    (torch.bfloat16, 2, 90, 84, 4, [90, 31], True, True, True, True),  # 8-byte vectors only
+    (torch.bfloat16, 1, 33, 84, 8, None, False, True, True, True),
     (torch.bfloat16, 1, 2100, 264, 4, None, False, True, False, True),
     (torch.float32, 2, 37, 20, 4, None, False, True, True, True),
     (torch.float32, 2, 5, 1, 1, None, False, True, False, True),
