@@ -416,14 +416,13 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
     };
     if (!END) {
       // behind the sequence's end: zeros
-      for (int t = max(t0, te); t < t1; ++t)
-        for (int x = et; x < CH; x += NE)
-          if (c0 + x < cmax) {
-            const size_t at = ((size_t)b * p.T + t) * p.D + c0 + x;
-            ((IO*)p.du)[at] = from_f<IO>(0.f);
-            ((IO*)p.ddt)[at] = from_f<IO>(0.f);
-            if (p.dz) ((IO*)p.dz)[at] = from_f<IO>(0.f);
-          }
+      const float zero[EV] = {};
+      for (int t = max(t0, te) + i0; t < t1; t += IS) {
+        const size_t at = ((size_t)b * p.T + t) * p.D + c;
+        store_n<IO, EV>((IO*)p.du + at, zero, nc, p.vec);
+        store_n<IO, EV>((IO*)p.ddt + at, zero, nc, p.vec);
+        if (p.dz) store_n<IO, EV>((IO*)p.dz + at, zero, nc, p.vec);
+      }
     }
     if (ntile > 0) {
       load(0);

@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(32 * (W + WE), W + WE > 8 ? 1 : 2) scan_fwd_ke
       if (ntile > 0) finish(ntile - 1, last);
     if (!END && p.y) {
       // behind the sequence's end: zeros
-      for (int t = max(t0, te); t < t1; ++t)
-        for (int x = et; x < CH; x += NE)
-          if (c0 + x < cmax) ((IO*)p.y)[((size_t)b * p.T + t) * p.D + c0 + x] = from_f<IO>(0.f);
+      const float zero[EV] = {};
+      for (int t = max(t0, te) + i; t < t1; t += TT)
+        store_n<IO, EV>((IO*)p.y + ((size_t)b * p.T + t) * p.D + c, zero, nc, p.vec);
     }
     return;
   }
