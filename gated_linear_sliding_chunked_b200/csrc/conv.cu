@@ -416,6 +416,7 @@ int bwd_blocks(const lz_conv_dims* d, int* run) {
   int tb = 1;
   for (int r = 256; r >= 8; r -= 8) {
     const int n = std::max(1, (d->T + r * kWarps - 1) / (r * kWarps));
+    if (n > 65535) break;  // (a grid's limit)
     const int64_t cost = ((cols * n + slots - 1) / slots) * (r + 8);
     if (!best || cost < best) {
       best = cost;
