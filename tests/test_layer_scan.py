@@ -376,3 +376,33 @@ def test_helper_refusals():
         L.scan_bwd(u, u, A, bc, bc, u, states=torch.zeros(3))
     with pytest.raises(ValueError, match="shared by all tokens"):
         L.scan_fwd(u, u, A, bc[:, :1].expand(-1, 5, -1), bc)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F, BF])
+def test_growing_states(dtype):
+    """Rates of both signs, decays up to e^2 a token: values and gradients against autograd in 64
+    bits.  12 tokens, some 8 roundings of 2^-24 each and the decays' 2^-22, none of which cancels
+    more than the sums do: 12 (8 2^-24 + 2^-22) = 9e-6, and 2^-8 for what leaves in 16 bits."""
+    B, T, D, N = 2, 12, 24, 8
+    gen = torch.Generator().manual_seed(3)
+    u, dy = (torch.randn(B, T, D, generator=gen).to(dtype) for _ in range(2))
+    dt = (1 + torch.rand(B, T, D, generator=gen)).to(dtype)
+    Bm, Cm = (torch.randn(B, T, N, generator=gen).to(dtype) for _ in range(2))
+    A = 2 * torch.rand(D, N, generator=gen) - 1
+    leaves = [t.double().requires_grad_() for t in (u, dt, A, Bm, Cm)]
+    u64, dt64, A64, B64, C64 = leaves
+    h, ys = torch.zeros(B, D, N, dtype=torch.float64), []
+    for t in range(T):
+        h = torch.exp(dt64[:, t, :, None] * A64) * h + (dt64 * u64)[:, t, :, None] * B64[:, t, None]
+        ys.append((h * C64[:, t, None]).sum(-1))
+    y64 = torch.stack(ys, 1)
+    (y64 * dy.double()).sum().backward()
+    a = [t.cuda() for t in (u, dt, A, Bm, Cm)]
+    y, _ = L.scan_fwd(*a, softplus=False)
+    g = L.scan_bwd(*a, dy.cuda(), softplus=False)
+    got = [y, g["du"], g["ddt"], g["dA"], g["dB"], g["dC"]]
+    for name, x, ref in zip(("y", "du", "ddt", "dA", "dB", "dC"), got,
+                            [y64.detach()] + [t.grad for t in leaves]):
+        err = float((x.double().cpu() - ref).norm() / ref.norm())
+        assert err <= (9e-6 if x.dtype == F else 9e-6 + 2 ** -8), (name, err)
