@@ -217,3 +217,37 @@ def test_captured_norms_and_convolutions_replay(D):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_rows_beyond_32_bit_offsets():
+    """The second sequence stands more than 2^32 elements behind the first: the results are those of
+    contiguous inputs, bit for bit."""
+    T, D, N = 70, 48, 8
+    gen = torch.Generator().manual_seed(5)
+    gap = (1 << 32) + 64
+    buf = torch.empty(gap + 8 * T * D, dtype=torch.bfloat16, device="cuda")
+    far = []
+
+    def place(*shape):
+        x = torch.randn(2, T, *shape, generator=gen).bfloat16().cuda()
+        width = x[0, 0].numel()
+        v = buf[len(far) * T * D:].as_strided((2, T) + shape, (gap, width) + x.stride()[2:])
+        v.copy_(x)
+        far.append(v)
+        return x, v
+
+    (x, xv), (dt, dtv), (z, zv), (Bm, Bv), (Cm, Cv) = place(D), place(D), place(D), place(N), place(N)
+    f = lambda *s: torch.randn(*s, generator=gen).cuda()
+    w, b, A = f(D, 4), f(D), -torch.rand(D, N, generator=gen).cuda()
+    dy = f(2, T, D).bfloat16()
+
+    def call(x, dt, z, Bm, Cm):
+        y, _ = L.conv_fwd(x, w, b)
+        c = L.conv_bwd(x, w, dy, b)
+        out, n = L.block_norm_fwd(x, w=b, z=z, r=dt, w2=b)
+        g = L.block_norm_bwd(x, w=b, z=z, w2=b, out=out, dn=dy, want_dr=True)
+        s, hT = L.scan_fwd(x, dt, A, Bm, Cm, z=z, want_hT=True)
+        sg = L.scan_bwd(x, dt, A, Bm, Cm, dy, z=z)
+        return [y, out, n, s, hT] + [t for d in (c, g, sg) for t in d.values() if t is not None]
+
+    assert all(torch.equal(p, q) for p, q in zip(call(x, dt, z, Bm, Cm), call(xv, dtv, zv, Bv, Cv)))
