@@ -62,41 +62,16 @@ struct ScanParams {
   void* dC;
 };
 
-__device__ __forceinline__ f2 ex2v(f2 x) { return pk(ex2(lo(x)), ex2(hi(x))); }
-
-// 2^x to 8e-8 (3e-8 on average): x = n + f with |f| <= 1/2, 2^f = 1 + f q(f) (q of
-// degree 5, fitted to the smallest largest error, 2e-9), times 2^n.  2^128 and
-// more is infinite, what is below 2^-126 zero; NaN stays NaN.
-__device__ __forceinline__ f2 ex2_fine(f2 x) {
-  auto clamp = [](float v) {
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-127.f));
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(128.f));
-    return v;
-  };
-  constexpr float kRound = 12582912.f;  // 3 * 2^22: a sum with it is rounded to a whole number
-  x = pk(clamp(lo(x)), clamp(hi(x)));
-  const f2 t = add2(x, pk(kRound, kRound)), n = add2(t, pk(-kRound, -kRound));
-  const f2 f = fma2(n, pk(-1.f, -1.f), x);
-  auto c = [](float v) { return pk(v, v); };
-  f2 q = fma2(f, c(1.53533624e-4f), c(1.33988750e-3f));
-  q = fma2(f, q, c(9.61843692e-3f));
-  q = fma2(f, q, c(5.55033237e-2f));
-  q = fma2(f, q, c(2.40226477e-1f));
-  q = fma2(f, q, c(6.93147182e-1f));
-  q = fma2(f, q, c(1.f));
-  auto scale = [](float v) { return __uint_as_float((__float_as_uint(v) << 23) + 0x3f800000u); };
-  return mul2(q, pk(scale(lo(t)), scale(hi(t))));
-}
-
-// The decays of the backward walk.  Their errors add up over a state's memory:
-// with the special-function unit's (1e-7 each) the gradient of A is off by 1.2e-6
-// after some 500 tokens and that of h0 by 1.3e-6, with these by 6e-7 and 3e-7, as
-// little as the rest of the 32-bit arithmetic.  (3 x 511 x 1000 x 8: 54 -> 65 us.)
-// 16-bit inputs and gradients are rounded by 2e-3, and take the faster ones.
-template <typename IO>
-__device__ __forceinline__ f2 decay(f2 x) {
-  if constexpr (sizeof(IO) == 4) return ex2_fine(x);
-  else return ex2v(x);
+// 2^(A2 d), the decay.  Its errors add up over a state's memory, so their mean
+// counts: the special-function unit's results just below 1 are 3e-8 too small on
+// average (measured over the arguments; as if cut off, not rounded), which 2^-24.5
+// added to the argument makes up for (3 x 511 x 1000 x 8: the gradient of A is off
+// by 1.2e-6 without, by 7.5e-7 with it; a polynomial gave 6e-7 and took half as long
+// again).
+__device__ __forceinline__ f2 decay(f2 A2, f2 d) {
+  constexpr float kCut = 4.2e-8f;
+  const f2 x = fma2(A2, d, pk(kCut, kCut));
+  return pk(ex2(lo(x)), ex2(hi(x)));
 }
 
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative

@@ -113,8 +113,8 @@ __device__ __forceinline__ void walk_tile(bool want_y, const ulonglong2 h0, cons
         const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&q[(i + j) * DS]);
         f2 B0, B1;
         load_bc(bf + (i + j) * NP, B0, B1);
-        a[j][0] = ex2v(mul2(A2[0], d.x));
-        a[j][1] = ex2v(mul2(A2[1], d.x));
+        a[j][0] = decay(A2[0], d.x);
+        a[j][1] = decay(A2[1], d.x);
         x[j][0] = mul2(d.y, B0);
         x[j][1] = mul2(d.y, B1);
       }
@@ -190,8 +190,8 @@ __device__ __forceinline__ void walk_tile(bool want_y, const ulonglong2 h0, cons
       const f2 dB0 = mul2(gr[0], du2), dB1 = mul2(gr[1], du2);
       const f2 dC0 = mul2(h[m + 1][0], e2), dC1 = mul2(h[m + 1][1], e2);
       const f2 sB = fma2(gr[1], o.B1, mul2(gr[0], o.B0));
-      gr[0] = mul2(gr[0], decay<IO>(mul2(A2[0], d2)));
-      gr[1] = mul2(gr[1], decay<IO>(mul2(A2[1], d2)));
+      gr[0] = mul2(gr[0], decay(A2[0], d2));
+      gr[1] = mul2(gr[1], decay(A2[1], d2));
       const f2 gp0 = mul2(gr[0], h[m][0]), gp1 = mul2(gr[1], h[m][1]);
       const f2 sA = fma2(gp1, A2[1], mul2(gp0, A2[0]));
       dA[0] = fma2(gp0, d2, dA[0]);
@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
       load_state(p.segE + s * sstep + sidx, p.N, on0, on1, x);
       const float* sd = p.segD + ((size_t)s * p.B + b) * p.D + c;
       const f2 d = pk(on0 ? sd[0] : 0.f, on1 ? sd[1] : 0.f);
-      gr[0] = fma2(decay<IO>(mul2(A2[0], d)), gr[0], x[0]);
-      gr[1] = fma2(decay<IO>(mul2(A2[1], d)), gr[1], x[1]);
+      gr[0] = fma2(decay(A2[0], d), gr[0], x[0]);
+      gr[1] = fma2(decay(A2[1], d), gr[1], x[1]);
     }
   }
   __syncthreads();
@@ -508,8 +508,8 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
         const f2 d = *reinterpret_cast<const f2*>(&q[i * G::DS]), e = *reinterpret_cast<const f2*>(&qe[i * G::DS]);
         f2 C0, C1;
         load_bc(cf + i * NP, C0, C1);
-        gr[0] = mul2(fma2(e, C0, gr[0]), decay<IO>(mul2(A2[0], d)));
-        gr[1] = mul2(fma2(e, C1, gr[1]), decay<IO>(mul2(A2[1], d)));
+        gr[0] = mul2(fma2(e, C0, gr[0]), decay(A2[0], d));
+        gr[1] = mul2(fma2(e, C1, gr[1]), decay(A2[1], d));
         sumd = add2(sumd, d);
       }
     } else {

@@ -77,8 +77,8 @@ __device__ __forceinline__ void scan_tile(const float2* __restrict__ dd, const I
     f2 B0, B1;
     load_bc(bf + i * NP, B0, B1);
     const f2 d2 = pk(d.x, d.x), du2 = pk(d.y, d.y);
-    a[0] = ex2v(mul2(A2[0], d2));
-    a[1] = ex2v(mul2(A2[1], d2));
+    a[0] = decay(A2[0], d2);
+    a[1] = decay(A2[1], d2);
     x[0] = mul2(du2, B0);
     x[1] = mul2(du2, B1);
     if (END) sumd += d.x;
@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(32 * (W + WE), W + WE > 8 ? 1 : 2) scan_fwd_ke
       for (int s = 0; s < seg; ++s) {
         const float4 x = *reinterpret_cast<const float4*>(p.segE + s * sstep + sidx);
         const float d = p.segD[((size_t)s * p.B + b) * p.D + c];
-        h[0] = fma2(ex2v(mul2(A2[0], pk(d, d))), h[0], pk(x.x, x.y));
-        h[1] = fma2(ex2v(mul2(A2[1], pk(d, d))), h[1], pk(x.z, x.w));
+        h[0] = fma2(decay(A2[0], pk(d, d)), h[0], pk(x.x, x.y));
+        h[1] = fma2(decay(A2[1], pk(d, d)), h[1], pk(x.z, x.w));
       }
     }
   }
