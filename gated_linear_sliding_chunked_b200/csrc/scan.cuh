@@ -68,8 +68,8 @@ struct ScanParams {
 // added to the argument makes up for (3 x 511 x 1000 x 8: the gradient of A is off
 // by 1.2e-6 without, by 7.5e-7 with it; a polynomial gave 6e-7 and took half as long
 // again).
+constexpr float kCut = 4.2e-8f;
 __device__ __forceinline__ f2 decay(f2 A2, f2 d) {
-  constexpr float kCut = 4.2e-8f;
   const f2 x = fma2(A2, d, pk(kCut, kCut));
   return pk(ex2(lo(x)), ex2(hi(x)));
 }

@@ -412,10 +412,10 @@ __global__ void __launch_bounds__(kStepThreads, 3) scan_step_kernel(ScanParams p
     for (int q = 0; q < Q; ++q) {
       float4 x = in.h[q];
       const Pack<IO, 4>&Bq = in.B[q], &Cq = in.C[q];
-      x.x = fmaf(ex2(d2 * A[q].x), x.x, du * Bq.get(0));
-      x.y = fmaf(ex2(d2 * A[q].y), x.y, du * Bq.get(1));
-      x.z = fmaf(ex2(d2 * A[q].z), x.z, du * Bq.get(2));
-      x.w = fmaf(ex2(d2 * A[q].w), x.w, du * Bq.get(3));
+      x.x = fmaf(ex2(fmaf(d2, A[q].x, kCut)), x.x, du * Bq.get(0));
+      x.y = fmaf(ex2(fmaf(d2, A[q].y, kCut)), x.y, du * Bq.get(1));
+      x.z = fmaf(ex2(fmaf(d2, A[q].z, kCut)), x.z, du * Bq.get(2));
+      x.w = fmaf(ex2(fmaf(d2, A[q].w, kCut)), x.w, du * Bq.get(3));
       if (on) reinterpret_cast<float4*>(state + ((size_t)b * p.D + c) * p.N + n0)[q] = x;
       y += x.x * Cq.get(0) + x.y * Cq.get(1) + x.z * Cq.get(2) + x.w * Cq.get(3);
     }
