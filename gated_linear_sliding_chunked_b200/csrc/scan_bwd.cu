@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
       load_state(p.segE + s * sstep + sidx, p.N, on0, on1, x);
       const float* sd = p.segD + ((size_t)s * p.B + b) * p.D + c;
       const f2 d = pk(on0 ? sd[0] : 0.f, on1 ? sd[1] : 0.f);
-      gr[0] = fma2(decay(A2[0], d), gr[0], x[0]);
-      gr[1] = fma2(decay(A2[1], d), gr[1], x[1]);
+      gr[0] = carry(A2[0], d, gr[0], x[0]);
+      gr[1] = carry(A2[1], d, gr[1], x[1]);
     }
   }
   __syncthreads();

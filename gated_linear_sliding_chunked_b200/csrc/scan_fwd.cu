@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(32 * (W + WE), W + WE > 8 ? 1 : 2) scan_fwd_ke
       for (int s = 0; s < seg; ++s) {
         const float4 x = *reinterpret_cast<const float4*>(p.segE + s * sstep + sidx);
         const float d = p.segD[((size_t)s * p.B + b) * p.D + c];
-        h[0] = fma2(decay(A2[0], pk(d, d)), h[0], pk(x.x, x.y));
-        h[1] = fma2(decay(A2[1], pk(d, d)), h[1], pk(x.z, x.w));
+        h[0] = carry(A2[0], pk(d, d), h[0], pk(x.x, x.y));
+        h[1] = carry(A2[1], pk(d, d), h[1], pk(x.z, x.w));
       }
     }
   }

@@ -1,0 +1,57 @@
+"""Layer operators where a value overflows, a length ends or a call meets another device: against the
+definitions in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import gated_linear_sliding_chunked_b200 as L
+from layer_ref import np64, scan
+
+
+def _growing(T, dt, u_on, dy_on, h0=None, dhT=None):
+    """Inputs of one sequence (8 channels, 4 states, rates of 1: one block, cut into segments of 64
+    tokens) with u and dy zero outside the given tokens, the reference and the kernel's results."""
+    D, N = 8, 4
+    g = torch.Generator().manual_seed(T)
+    pos = lambda *s: torch.rand(*s, generator=g) + 0.5
+    only = lambda x, on: x * torch.zeros(T, 1).index_fill(0, torch.tensor(on), 1.0)
+    c = dict(u=only(pos(1, T, D), u_on), dt=dt.expand(1, D, T).transpose(1, 2).contiguous(),
+             A=torch.ones(D, N), Bm=pos(1, T, 1, N), Cm=pos(1, T, 1, N))
+    dy = only(pos(1, T, D), dy_on)
+    more = {k: torch.full((1, D, N), v) for k, v in (("h0", h0), ("dhT", dhT)) if v is not None}
+    ref = scan(**{k: np64(v) for k, v in {**c, **more, "dy": dy}.items()}, softplus=False)
+    a = [v.cuda() for v in c.values()]
+    m = {k: v.cuda() for k, v in more.items()}
+    y, hT = L.scan_fwd(*a, softplus=False, h0=m.get("h0"), want_hT=True)
+    got = dict(L.scan_bwd(*a, dy.cuda(), softplus=False, **m, want_dh0=True), y=y, hT=hT)
+    return {k: (np64(got[k]), v) for k, v in ref.items()}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", ["late input", "early gradient", "small state", "small gradient"])
+def test_states_that_grow_over_segments(case):
+    """Rates of 1 and steps of 1.5: over a segment of 64 tokens a state grows by 2^138, more than a
+    float holds, and what enters it is nothing (left padding) or small: the results are finite.
+
+    Steps are multiples of 1/2, so their sums are exact.  A segment's factor is off by the rounding
+    of the rate (2^-24) and of the exponent (2^-17 of 138), 2.9e-6 x 2 + 5.3e-6; a token's by 2^-22
+    and the sums behind it by some 8 2^-24, over 20 tokens 1.5e-5: 3e-5 holds all."""
+    if case == "late input":  # 3 empty segments, then 12 tokens
+        r = _growing(204, torch.tensor(1.5).expand(204), list(range(192, 204)), [203])
+        names = ("y", "hT", "dC")  # (the gradients before the input are beyond a float)
+    elif case == "early gradient":  # the gradient of 12 tokens, nothing behind them
+        r = _growing(256, torch.tensor(1.5).expand(256), [255], list(range(12)))
+        names = ("y", "hT", "du", "dB", "dh0", "dA", "dC")
+    elif case == "small state":  # 2^-100 before 70 tokens of 2^2.16
+        r = _growing(70, torch.tensor(1.5).expand(70), [69], [69], h0=2.0 ** -100)
+        names = ("y", "hT", "dC")
+    else:  # 2^-100 behind a segment of 2^138
+        dt = torch.full((128,), 1.5)
+        dt[:64] = 0.0
+        r = _growing(128, dt, [0], [0], dhT=2.0 ** -100)
+        names = ("y", "du", "dh0", "dB")
+    for n in names:
+        got, ref = r[n]
+        assert np.isfinite(ref).all() and np.abs(ref).max() < 3e38, (case, n, "not a test")
+        assert np.isfinite(got).all(), (case, n)
+        assert np.linalg.norm(got - ref) <= 3e-5 * np.linalg.norm(ref) + 1e-30, (case, n)
