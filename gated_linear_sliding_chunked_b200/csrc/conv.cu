@@ -259,11 +259,12 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) 
           a.fma(w[K - 1], x, bias);
 #pragma unroll
           for (int j = 0; j < K - 1; ++j) a.fma(w[j], xw[j], a);
-          // (dy is zero behind the end, and with it dp)
           dp.set([&](int e) {
             const float v = a.get(e), sg = sigmoid(v), vs = v * sg;
             return dyv[i].get(e) * fmaf(-vs, sg, sg + vs);
           });
+          // (dy is zero behind the end, act'(p) need not be finite there)
+          if (EDGE && s >= slive) dp.fill(0.f);
         } else {
           dp.set([&](int e) { return dyv[i].get(e); });
         }

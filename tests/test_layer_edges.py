@@ -55,3 +55,23 @@ def test_states_that_grow_over_segments(case):
         assert np.isfinite(ref).all() and np.abs(ref).max() < 3e38, (case, n, "not a test")
         assert np.isfinite(got).all(), (case, n)
         assert np.linalg.norm(got - ref) <= 3e-5 * np.linalg.norm(ref) + 1e-30, (case, n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D,T,n", [(torch.bfloat16, 64, 21, 9), (torch.bfloat16, 13, 40, 33),
+                                         (torch.float32, 36, 300, 256), (torch.float32, 5, 9, 1)])
+def test_convolution_behind_an_overflow(dtype, D, T, n):
+    """The last token of a padded sequence is infinite: its own gradients are not finite, those of
+    the tokens behind the end are zeros all the same, and those before the taps' reach are what they
+    are without it."""
+    K = 4
+    g = torch.Generator().manual_seed(T)
+    x, dy = (torch.randn(2, T, D, generator=g).to(dtype).cuda() for _ in range(2))
+    w, b = torch.randn(D, K, generator=g).cuda(), torch.randn(D, generator=g).cuda()
+    lens = torch.tensor([T, n]).cuda()
+    want = L.conv_bwd(x, w, dy, b, lens=lens)["dx"]
+    x[1, n - 1] = float("inf")
+    got = L.conv_bwd(x, w, dy, b, lens=lens)["dx"]
+    assert not got[1, n:].any()  # (NaN counts as true)
+    assert torch.equal(got[0], want[0])
+    assert torch.equal(got[1, :max(0, n - K)], want[1, :max(0, n - K)])
