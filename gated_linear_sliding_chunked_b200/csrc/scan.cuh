@@ -63,12 +63,16 @@ struct ScanParams {
 };
 
 // 2^(A2 d), the decay.  Its errors add up over a state's memory, so their mean
-// counts: the special-function unit's results just below 1 are 3e-8 too small on
-// average (measured over the arguments; as if cut off, not rounded), which 2^-24.5
-// added to the argument makes up for (3 x 511 x 1000 x 8: the gradient of A is off
-// by 1.2e-6 without, by 7.5e-7 with it; a polynomial gave 6e-7 and took half as long
-// again).
-constexpr float kCut = 4.2e-8f;
+// counts.  The special-function unit's results just below 1 are too small on
+// average (measured over the arguments of each binade): by 1.6e-8 to 2.7e-8 for
+// exponents of 2^-8 to 1, by 5e-9 to 8e-9 for smaller ones, whose states remember
+// longest.  2^-26 in the exponent leaves at most 1.6e-8 of the former and 5e-9 of
+// the latter.  (Twice and three times as much centres the fast decays, and takes
+// the slow ones off by 1e-8 and 2.4e-8: the gradient of A after 8192 tokens with
+// rates of 1 and steps of 0.001 is off by 3.1e-6 with 2^-26, 3.9e-6 with nothing,
+// 1.5e-5 with 4.2e-8; torch's products of 32-bit exps by 2.3e-5.  A polynomial took
+// half as long again.)
+constexpr float kCut = 0x1p-26f;
 __device__ __forceinline__ f2 decay(f2 A2, f2 d) {
   const f2 x = fma2(A2, d, pk(kCut, kCut));
   return pk(ex2(lo(x)), ex2(hi(x)));
