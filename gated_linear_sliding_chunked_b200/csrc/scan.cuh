@@ -80,21 +80,12 @@ __device__ __forceinline__ f2 decay(f2 A2, f2 d) {
 
 // 2^(A2 d) h + e: a state h carried over a segment whose steps add up to d, with
 // what the segment adds to it.  Where rates grow, the factor alone can be more
-// than a float holds while its product with h (none, or a small one) is not: it
-// is then applied in parts.
-__device__ __forceinline__ float grown(float x, float h) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i)  // (2^378 takes the smallest float beyond the largest)
-    if (x > 126.f) {
-      h *= 0x1p126f;
-      x -= 126.f;
-    }
-  return h * ex2(fminf(x, 126.f));
-}
+// than a float holds while its product with h (none, or a small one) is not, so
+// that h is multiplied by the factor's root twice.
 __device__ __forceinline__ f2 carry(f2 A2, f2 d, f2 h, f2 e) {
   const f2 x = fma2(A2, d, pk(kCut, kCut));
-  if (fmaxf(lo(x), hi(x)) <= 126.f) return fma2(pk(ex2(lo(x)), ex2(hi(x))), h, e);
-  return add2(pk(grown(lo(x), lo(h)), grown(hi(x), hi(h))), e);
+  const f2 r = pk(ex2(fminf(0.5f * lo(x), 127.99f)), ex2(fminf(0.5f * hi(x), 127.99f)));
+  return fma2(mul2(h, r), r, e);
 }
 
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), and its derivative

@@ -72,3 +72,18 @@ def test_decays_have_no_mean_error(run, B):
     assert abs(sum(means.values())) / len(means) <= 2.0 ** -27
     for k, m in means.items():
         assert abs(m) <= (2.0 ** -27 if k <= -9 else 3 * 2.0 ** -27), (k, m)
+
+
+def test_parameter_gradients_over_many_tokens():
+    """16384 equal terms a channel, each a little above 1, so that one 32-bit sum over a thread's 1024
+    of them rounds down every time (1.5e-5 of the result).  Summed over 16 tiles of tokens at a time
+    the longest way through the sums has 16 + 64 + 16 + 1 roundings of 2^-24: 5.8e-6."""
+    T, D, N = 16384, 800, 64  # 100 blocks: sequences are not cut
+    c = 1 + 0.49 * 2.0 ** -14
+    u = torch.full((1, T, D), c, device="cuda")
+    bc = torch.zeros(1, T, N, device="cuda")
+    A, Ds = -torch.ones(D, N, device="cuda"), torch.ones(D, device="cuda")
+    dy = torch.ones(1, T, D, device="cuda")
+    got = L.scan_bwd(u, torch.full_like(u, 0.1), A, bc, bc, dy, softplus=False, Dskip=Ds)["dDskip"]
+    want = T * float(u[0, 0, 0].double())
+    assert float((got.double() - want).abs().max()) <= 97 * 2.0 ** -24 * want
