@@ -40,6 +40,7 @@ struct Geo {
   static constexpr int U = L < 8 ? L / 2 : 4;  // tokens whose lane sums are formed together
   static constexpr int YS = row_of(CH, L == 4 ? 16 : L == 8 ? 8 : 4);
   static constexpr int DS = CH / 2 + 1;     // row of a [tokens][channel pairs] tile of 4 words
+  static constexpr int EV = kCk * CH / NE > 8 ? 8 : kCk * CH / NE > 1 ? kCk * CH / NE : 2;  // channels of an elementwise thread
 };
 
 // 2 elements of B or C as the scan warps read them from shared memory, each
@@ -77,6 +78,12 @@ __device__ __forceinline__ void store_state(float* p, int N, bool on0, bool on1,
 }
 
 constexpr int TB = kCk;  // tokens of a tile
+// The parameter gradients are summed over this many tiles at a time: thousands
+// of tokens added to one 32-bit sum would cost it bits.  (At 2 x 8192 tokens the
+// gradients of Dskip and dt_bias are off by 1.6e-7 and 4.1e-7, with one sum a
+// thread by 4.1e-7 and 6.4e-7, for 0.7 % of the time; equal terms by 2^-24 for
+// every token that a thread adds up.)
+constexpr int kSum = 16;
 
 template <typename IO, int L, int W>
 struct alignas(16) Smem {
@@ -88,6 +95,7 @@ struct alignas(16) Smem {
   float gB[2][TB * G::YS], gA[2][TB * G::YS], yc[2][TB * G::YS];
   float red[2][W][TB][2 * NP];  // dB, dC over a warp's channels
   ulonglong2 ck[2][G::NS];  // the state before the tile, as the scan threads hold it
+  float sum[2][G::EV][G::NE];  // dDskip, ddt_bias of an elementwise thread's channels
 };
 
 // The scan warps' walk over one tile, forward and back.  Sums over lanes take
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
   using G = Geo<L, W>;
   constexpr int CH = G::CH, NP = G::NP, YS = G::YS;
   constexpr int NS = G::NS, NE = G::NE;
-  constexpr int EV = TB * CH / NE > 1 ? (TB * CH / NE < 8 ? TB * CH / NE : 8) : 2;  // channels of an elementwise thread
+  constexpr int EV = G::EV;
   constexpr int ROWT = CH / EV;                                 // threads of a token
   constexpr int PASS = (TB * ROWT + NE - 1) / NE;               // tokens of a thread
   constexpr int BV = TB * NP / 4, BN = (BV + NE - 1) / NE;   // 4-element vectors of B and of C, a thread's
@@ -259,13 +267,21 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
     Next nx[PASS];
     Pack<IO, 4> nb[BN], ncv[BN];
     Tok tok[2][PASS];
-    float Ds[EV], bias[EV], sD[EV], sT[EV];
+    float Ds[EV], bias[EV], sD[EV], sT[EV];  // (sums of up to kSum tiles, added to sm.sum)
 #pragma unroll
     for (int e = 0; e < EV; ++e) {
       Ds[e] = p.Dskip && e < nc ? p.Dskip[c + e] : 0.f;
       bias[e] = p.dtb && e < nc ? p.dtb[c + e] : 0.f;
-      sD[e] = sT[e] = 0.f;
+      sD[e] = sT[e] = sm.sum[0][e][et] = sm.sum[1][e][et] = 0.f;
     }
+    auto flush = [&] {  // (a thread's own words)
+#pragma unroll
+      for (int e = 0; e < EV; ++e) {
+        sm.sum[0][e][et] += sD[e];
+        sm.sum[1][e][et] += sT[e];
+        sD[e] = sT[e] = 0.f;
+      }
+    };
     // Pointers to this thread's elements: of the next tile to load, and of the
     // next tile of outputs, from the last tile down.
     const int tl = t0 + (ntile - 1) * TB;
@@ -441,12 +457,15 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
     for (int k = 0; k < ntile; k += 2) {
       step(k, tok[1]);
       if (k + 1 < ntile) step(k + 1, tok[0]);
+      if constexpr (!END)
+        if (k % kSum == kSum - 2) flush();
     }
     if constexpr (!END) {
       if (ntile > 0) {
         if (ntile & 1) finish(ntile - 1, tok[0]);
         else finish(ntile - 1, tok[1]);
       }
+      flush();
       // sums of e u and ddt over the block's token rows, in order
       float* s1 = &sm.red[0][0][0][0];
       float* s2 = &sm.gB[0][0];
@@ -454,8 +473,8 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
       asm volatile("bar.sync 1, %0;" ::"n"(NE) : "memory");
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
-        s1[i0 * CH + cl + e] = sD[e];
-        s2[i0 * CH + cl + e] = sT[e];
+        s1[i0 * CH + cl + e] = sm.sum[0][e][et];
+        s2[i0 * CH + cl + e] = sm.sum[1][e][et];
       }
       asm volatile("bar.sync 1, %0;" ::"n"(NE) : "memory");
       for (int x = et; x < CH; x += NE)
@@ -515,9 +534,7 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
     } else {
       walk_tile<IO, L, W>(p.dz != nullptr, sm.ck[w][tid], q, qe, bf, cf, sm.gB[w] + cl, sm.gA[w] + cl, sm.yc[w] + cl,
                        &sm.red[w][warp][0][0] + n0, A2, gr, dAt, lane, l);
-      // dA over 16 tiles at a time: thousands of tokens added to one sum would
-      // cost it bits
-      if (k % 16 == 15) {
+      if (k % kSum == kSum - 1) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           dA[x] = add2(dA[x], dAt[x]);
