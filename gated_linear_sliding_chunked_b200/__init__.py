@@ -707,6 +707,8 @@ def _on(dev, stream):
     if stream is not None:
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=dev)
+        elif stream.device != dev:
+            raise ValueError(f"a stream of {stream.device} cannot take tensors on {dev}")
         return torch.cuda.stream(stream)
     return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 

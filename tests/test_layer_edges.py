@@ -75,3 +75,16 @@ def test_convolution_behind_an_overflow(dtype, D, T, n):
     assert not got[1, n:].any()  # (NaN counts as true)
     assert torch.equal(got[0], want[0])
     assert torch.equal(got[1, :max(0, n - K)], want[1, :max(0, n - K)])
+
+
+class _Stream:  # of a device that no machine need have
+    cuda_stream = 0
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+def test_stream_of_another_device_is_refused():
+    """Work on a stream goes to that stream's device, which need not reach the tensors' memory."""
+    with pytest.raises(ValueError, match="cuda:1"):
+        L._on(torch.device("cuda", 0), _Stream(1))
