@@ -88,3 +88,20 @@ def test_stream_of_another_device_is_refused():
     """Work on a stream goes to that stream's device, which need not reach the tensors' memory."""
     with pytest.raises(ValueError, match="cuda:1"):
         L._on(torch.device("cuda", 0), _Stream(1))
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """The library's sizes are C ints: a larger one must not arrive there cut off."""
+    big = 2 ** 32 + 5
+    e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device="meta")
+    x, x1, w = e(1, big, 1), e(1, big), e(1, 4)
+    calls = [lambda: L.conv_fwd(x, w), lambda: L.conv_bwd(x, w, x), lambda: L.conv_fwd(e(1, 1, big), e(big, 4)),
+             lambda: L.conv_step(e(1, 3, big), x1, e(big, 4)),
+             lambda: L.scan_fwd(x, x, e(1, 4), e(1, big, 4), e(1, big, 4)),
+             lambda: L.scan_bwd(x, x, e(1, 4), e(1, big, 4), e(1, big, 4), x),
+             lambda: L.scan_step(e(big, 1, 4), e(big, 1), e(big, 1), e(1, 4), e(big, 4), e(big, 4)),
+             lambda: L.block_norm_fwd(x, w=e(1)), lambda: L.block_norm_bwd(x, w=e(1), dout=x),
+             lambda: L.block_norm_fwd(e(1, 2 ** 16, 1, 2 ** 16), w=e(2 ** 32))]
+    for call in calls:
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
