@@ -36,9 +36,10 @@ EXPORTS = ("lz_gla_fwd", "lz_gla_bwd", "lz_swa_meta_fwd", "lz_hybrid_fwd", "lz_s
            "lz_hybrid_fwd_mse", "lz_selftest_bounded_wait", "lz_cp_segment_decay", "lz_cp_fold",
            "lz_cp_rows", "lz_tcgen05_all", "lz_qkg_projection", "lz_fused_gate_logits",
            "lz_conv_fwd", "lz_conv_bwd", "lz_conv_step", "lz_scan_fwd", "lz_scan_bwd",
-           "lz_scan_step", "lz_block_norm_fwd", "lz_block_norm_bwd", "lz_layer_workspace_bytes")
+           "lz_scan_bwd_saved", "lz_scan_step", "lz_block_norm_fwd", "lz_block_norm_bwd", "lz_layer_workspace_bytes")
 
-LZ_WS_CONV_BWD, LZ_WS_SCAN_FWD, LZ_WS_SCAN_BWD, LZ_WS_SCAN_STATES, LZ_WS_NORM_BWD = range(16, 21)
+(LZ_WS_CONV_BWD, LZ_WS_SCAN_FWD, LZ_WS_SCAN_BWD, LZ_WS_SCAN_STATES, LZ_WS_NORM_BWD,
+ LZ_WS_SCAN_BWD_SAVED) = range(16, 22)
 
 # size of the static scratch array behind lz_swa_meta_bwd_noalloc
 LZ_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -128,6 +129,7 @@ def load(path: str = LIB_PATH):
     lib.lz_conv_step.argtypes = [CD] + [_P] * 5 + [_P]
     lib.lz_scan_fwd.argtypes = [SD] + [_P] * 13 + [_P, sz, _P]
     lib.lz_scan_bwd.argtypes = [SD] + [_P] * 22 + [_P, sz, _P]
+    lib.lz_scan_bwd_saved.argtypes = lib.lz_scan_bwd.argtypes
     lib.lz_scan_step.argtypes = [SD] + [_P] * 10 + [_P]
     lib.lz_block_norm_fwd.argtypes = [ND] + [_P] * 8 + [_P]
     lib.lz_block_norm_bwd.argtypes = [ND] + [_P] * 14 + [_P, sz, _P]
@@ -622,6 +624,16 @@ def lz_scan_bwd(dims, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT, st
                               _ptr(dh0), _ptr(ws), ws_bytes, _stream(stream)))
 
 
+def lz_scan_bwd_saved(dims, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT, states, du,
+                      ddt, dA, dB, dC, dDskip, ddt_bias, dz, dh0, ws, ws_bytes, stream=None):
+    _check(load().lz_scan_bwd_saved(ctypes.byref(dims), _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm),
+                                    _ptr(Cm), _ptr(Dskip), _ptr(z), _ptr(dt_bias), _ptr(h0),
+                                    _ptr(lens), _ptr(dy), _ptr(dhT), _ptr(states), _ptr(du),
+                                    _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dDskip),
+                                    _ptr(ddt_bias), _ptr(dz), _ptr(dh0), _ptr(ws), ws_bytes,
+                                    _stream(stream)))
+
+
 def lz_scan_step(dims, state, u, dt, A, Bm, Cm, Dskip, z, dt_bias, y, stream=None):
     _check(load().lz_scan_step(ctypes.byref(dims), _ptr(state), _ptr(u), _ptr(dt), _ptr(A),
                                _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z), _ptr(dt_bias), _ptr(y),
@@ -842,7 +854,8 @@ def scan_bwd(u, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, dt_bias=None, softplus
              lens=None, dhT=None, states=None, want_dh0=False, stream=None):
     """Gradients of scan_fwd: a dict of du, ddt, dA, dB, dC, dDskip, ddt_bias and
     dz (None for what was not given) and dh0 (None unless wanted).  states: the
-    forward's (optional; saves a walk over the sequence)."""
+    forward's (optional; saves a walk over the sequence and scratch of their
+    size)."""
     fn, dev = "scan_bwd", u.device
     d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus)
     B, T, D = u.shape
@@ -861,10 +874,12 @@ def scan_bwd(u, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, dt_bias=None, softplus
         dD = torch.empty(D, **f32) if Dskip is not None else None
         db = torch.empty(D, **f32) if dt_bias is not None else None
         dh0 = torch.empty(B, D, N, **f32) if want_dh0 else None
-        n = lz_layer_workspace_bytes(d, LZ_WS_SCAN_BWD)
+        call, which = (lz_scan_bwd, LZ_WS_SCAN_BWD) if states is None else \
+            (lz_scan_bwd_saved, LZ_WS_SCAN_BWD_SAVED)
+        n = lz_layer_workspace_bytes(d, which)
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        lz_scan_bwd(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT, states, du, ddt,
-                    dA, dB, dC, dD, db, dz, dh0, ws, n, _stream_on(dev, stream))
+        call(d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT, states, du, ddt, dA, dB,
+             dC, dD, db, dz, dh0, ws, n, _stream_on(dev, stream))
     return {"du": du, "ddt": ddt, "dA": dA, "dB": dB, "dC": dC, "dDskip": dD, "ddt_bias": db,
             "dz": dz, "dh0": dh0}
 

@@ -60,6 +60,7 @@ extern "C" size_t lz_layer_workspace_bytes(const void* d, int which) {
     case LZ_WS_CONV_BWD: return lz::conv_bwd_ws((const lz_conv_dims*)d);
     case LZ_WS_SCAN_FWD:
     case LZ_WS_SCAN_BWD:
+    case LZ_WS_SCAN_BWD_SAVED:
     case LZ_WS_SCAN_STATES: return lz::scan_ws((const lz_scan_dims*)d, which);
     case LZ_WS_NORM_BWD: return lz::norm_bwd_ws((const lz_norm_dims*)d);
     default: return 0;

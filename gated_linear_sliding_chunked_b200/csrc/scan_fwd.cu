@@ -529,7 +529,8 @@ size_t state_bytes(const lz_scan_dims* d) {
 struct Ws {
   size_t segE, segD, part, bc, states, total;
 };
-Ws ws_of(const lz_scan_dims* d, bool bwd) {
+enum { WS_FWD, WS_BWD, WS_BWD_SAVED };  // (saved: the caller has the forward's states)
+Ws ws_of(const lz_scan_dims* d, int kind) {
   int W, nct, seg, nseg;
   plan(d, &W, &nct, &seg, &nseg);
   const size_t bd = (size_t)d->B * d->D;
@@ -538,10 +539,10 @@ Ws ws_of(const lz_scan_dims* d, bool bwd) {
   auto take = [&](size_t bytes) { const size_t at = o; o += ws_round(bytes); return at; };
   w.segE = take(nseg > 1 ? nseg * bd * d->N * sizeof(float) : 0);
   w.segD = take(nseg > 1 ? nseg * bd * sizeof(float) : 0);
-  if (bwd) {
+  if (kind != WS_FWD) {
     w.part = take((size_t)d->B * nseg * scan::part_ld(d->D, d->N) * sizeof(float));
     w.bc = take((size_t)nct * d->B * d->T * d->G * 2 * d->N * sizeof(float));
-    w.states = take(state_bytes(d));  // used when the caller gives none
+    w.states = take(kind == WS_BWD ? state_bytes(d) : 0);  // used when the caller gives none
   }
   w.total = o;
   return w;
@@ -573,7 +574,7 @@ ScanParams params_of(const lz_scan_dims* d, const void* u, const void* dt, const
 size_t scan_ws(const lz_scan_dims* d, int which) {
   if (check_scan("lz_layer_workspace_bytes", d) != LZ_OK) return 0;
   if (which == LZ_WS_SCAN_STATES) return state_bytes(d);
-  return ws_of(d, which == LZ_WS_SCAN_BWD).total;
+  return ws_of(d, which == LZ_WS_SCAN_FWD ? WS_FWD : which == LZ_WS_SCAN_BWD ? WS_BWD : WS_BWD_SAVED).total;
 }
 
 }  // namespace lz
@@ -590,7 +591,7 @@ extern "C" lz_status lz_scan_fwd(const lz_scan_dims* d, const void* u, const voi
   if (d->B == 0 || d->D == 0 || (d->T == 0 && !hT)) return layer_done(cudaSuccess, fn);
   const unsigned es = (unsigned)esize(d->io);
   const bool data = d->T > 0;
-  const Ws w = ws_of(d, false);
+  const Ws w = ws_of(d, WS_FWD);
   st = check_ptrs(fn, {{u, "u", data, es}, {dt, "dt", data, es}, {A, "A", true, 16}, {Bm, "Bm", data, es},
                        {Cm, "Cm", data, es}, {Dskip, "Dskip", false, 16}, {z, "z", false, es},
                        {dt_bias, "dt_bias", false, 16}, {h0, "h0", false, 16}, {lens, "lens", false, 8},
@@ -607,23 +608,23 @@ extern "C" lz_status lz_scan_fwd(const lz_scan_dims* d, const void* u, const voi
   return layer_done(launch_scan_fwd(p, d->io == LZ_BF16, (cudaStream_t)stream), fn);
 }
 
-extern "C" lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const void* dt, const float* A,
-                                 const void* Bm, const void* Cm, const float* Dskip, const void* z,
-                                 const float* dt_bias, const float* h0, const int64_t* lens, const void* dy,
-                                 const float* dhT, const float* states, void* du, void* ddt, float* dA, void* dB,
-                                 void* dC, float* dDskip, float* ddt_bias, void* dz, float* dh0, void* ws,
-                                 size_t ws_bytes, lz_stream stream) {
-  const char* fn = "lz_scan_bwd";
+static lz_status scan_bwd(const char* fn, int kind, const lz_scan_dims* d, const void* u, const void* dt,
+                          const float* A, const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                          const float* dt_bias, const float* h0, const int64_t* lens, const void* dy,
+                          const float* dhT, const float* states, void* du, void* ddt, float* dA, void* dB, void* dC,
+                          float* dDskip, float* ddt_bias, void* dz, float* dh0, void* ws, size_t ws_bytes,
+                          lz_stream stream) {
   lz_status st = check_scan(fn, d);
   if (st != LZ_OK) return st;
   if (d->D == 0) return layer_done(cudaSuccess, fn);
   const unsigned es = (unsigned)esize(d->io);
   const bool data = d->T > 0 && d->B > 0;
-  const Ws w = ws_of(d, true);
+  const Ws w = ws_of(d, kind);
   st = check_ptrs(fn, {{u, "u", data, es}, {dt, "dt", data, es}, {A, "A", true, 16}, {Bm, "Bm", data, es},
                        {Cm, "Cm", data, es}, {Dskip, "Dskip", false, 16}, {z, "z", data && dz, es},
                        {dt_bias, "dt_bias", false, 16}, {h0, "h0", false, 16}, {lens, "lens", false, 8},
-                       {dy, "dy", data, 16}, {dhT, "dhT", false, 16}, {states, "states", false, 16},
+                       {dy, "dy", data, 16}, {dhT, "dhT", false, 16},
+                       {states, "states", data && kind == WS_BWD_SAVED, 16},
                        {du, "du", data, 16}, {ddt, "ddt", data, 16}, {dA, "dA", true, 16}, {dB, "dB", data, 16},
                        {dC, "dC", data, 16}, {dDskip, "dDskip", false, 16}, {ddt_bias, "ddt_bias", false, 16},
                        {dz, "dz", false, 16}, {dh0, "dh0", false, 16}, {ws, "workspace", w.total > 0, 256}});
@@ -654,6 +655,26 @@ extern "C" lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const voi
                          (size_t)d->D, ddt_bias, (size_t)d->D},
                         s);
   return layer_done(e, fn);
+}
+
+extern "C" lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const void* dt, const float* A,
+                                 const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                 const float* dt_bias, const float* h0, const int64_t* lens, const void* dy,
+                                 const float* dhT, const float* states, void* du, void* ddt, float* dA, void* dB,
+                                 void* dC, float* dDskip, float* ddt_bias, void* dz, float* dh0, void* ws,
+                                 size_t ws_bytes, lz_stream stream) {
+  return scan_bwd("lz_scan_bwd", WS_BWD, d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT, states, du, ddt,
+                  dA, dB, dC, dDskip, ddt_bias, dz, dh0, ws, ws_bytes, stream);
+}
+
+extern "C" lz_status lz_scan_bwd_saved(const lz_scan_dims* d, const void* u, const void* dt, const float* A,
+                                       const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                                       const float* dt_bias, const float* h0, const int64_t* lens, const void* dy,
+                                       const float* dhT, const float* states, void* du, void* ddt, float* dA,
+                                       void* dB, void* dC, float* dDskip, float* ddt_bias, void* dz, float* dh0,
+                                       void* ws, size_t ws_bytes, lz_stream stream) {
+  return scan_bwd("lz_scan_bwd_saved", WS_BWD_SAVED, d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, lens, dy, dhT,
+                  states, du, ddt, dA, dB, dC, dDskip, ddt_bias, dz, dh0, ws, ws_bytes, stream);
 }
 
 extern "C" lz_status lz_scan_step(const lz_scan_dims* d, float* state, const void* u, const void* dt,

@@ -409,6 +409,20 @@ lz_status lz_scan_bwd(const lz_scan_dims* d, const void* u, const void* dt,
                       float* ddt_bias, void* dz, float* dh0, void* ws,
                       size_t ws_bytes, lz_stream stream);
 
+/* lz_scan_bwd with the forward's states, which must be given: its scratch,
+ * LZ_WS_SCAN_BWD_SAVED, has no room for states of its own (LZ_WS_SCAN_STATES
+ * bytes less, rounded). */
+lz_status lz_scan_bwd_saved(const lz_scan_dims* d, const void* u,
+                            const void* dt, const float* A, const void* Bm,
+                            const void* Cm, const float* Dskip, const void* z,
+                            const float* dt_bias, const float* h0,
+                            const int64_t* lens, const void* dy,
+                            const float* dhT, const float* states, void* du,
+                            void* ddt, float* dA, void* dB, void* dC,
+                            float* dDskip, float* ddt_bias, void* dz,
+                            float* dh0, void* ws, size_t ws_bytes,
+                            lz_stream stream);
+
 /* One generation step of B sequences: state [B,D,N] in place; u, dt, z [B,D],
  * Bm, Cm [B,G,N] (sequence to sequence bs elements when ld > 0); y [B,D].  T
  * is not used. */
@@ -457,7 +471,7 @@ lz_status lz_block_norm_bwd(const lz_norm_dims* d, const void* o,
  * dims struct that the entry point takes.  0 is possible, and returned for
  * dims that the entry point refuses. */
 enum { LZ_WS_CONV_BWD = 16, LZ_WS_SCAN_FWD = 17, LZ_WS_SCAN_BWD = 18,
-       LZ_WS_SCAN_STATES = 19, LZ_WS_NORM_BWD = 20 };
+       LZ_WS_SCAN_STATES = 19, LZ_WS_NORM_BWD = 20, LZ_WS_SCAN_BWD_SAVED = 21 };
 size_t lz_layer_workspace_bytes(const void* d, int which);
 
 /* ---- Context parallelism: one sequence over R ranks ----------------------

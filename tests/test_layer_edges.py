@@ -105,3 +105,41 @@ def test_sizes_beyond_32_bits_are_refused():
     for call in calls:
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def _scan_bwd_args():
+    d = L.LzScanDims(2, 4096, 64, 1, 16, L.LZ_BF16, 1)
+    return d, [0x7F0000000000 + 4096 * i for i in range(23)]  # never dereferenced
+
+
+def test_scratch_with_the_forwards_states():
+    """The backward that is given the states asks for no room for them, and refuses to go without."""
+    d, p = _scan_bwd_args()
+    whole, saved, states = (L.lz_layer_workspace_bytes(d, w) for w in
+                            (L.LZ_WS_SCAN_BWD, L.LZ_WS_SCAN_BWD_SAVED, L.LZ_WS_SCAN_STATES))
+    assert states == 2 * 256 * 64 * 16 * 4 and saved == whole - states > 0
+    f = L.load().lz_scan_bwd_saved
+    with pytest.raises(L.LzError, match="too small"):
+        L._check(f(d, *p, saved - 1, 0))
+    with pytest.raises(L.LzError, match="states"):
+        L._check(f(d, *p[:12], None, *p[13:], saved, 0))
+
+
+@pytest.mark.gpu
+def test_backward_with_states_takes_no_room_for_them():
+    B, T, D, N = 1, 4096, 512, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    u, dt, dy = (torch.randn(B, T, D, generator=g, device="cuda") for _ in range(3))
+    bc, A = torch.randn(B, T, N, generator=g, device="cuda"), -torch.ones(D, N, device="cuda")
+    st = L.scan_fwd(u, dt, A, bc, bc, want_states=True)[2]
+
+    def peak(states):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        at = torch.cuda.memory_allocated()
+        out = L.scan_bwd(u, dt, A, bc, bc, dy, states=states)
+        return torch.cuda.max_memory_allocated() - at, out
+
+    (own, a), (given, b) = peak(None), peak(st)
+    assert given <= own - 4 * st.numel() + (1 << 20)
+    assert all(torch.equal(a[k], b[k]) for k in a if a[k] is not None)
