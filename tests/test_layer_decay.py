@@ -68,7 +68,6 @@ def test_decays_have_no_mean_error(run, B):
     for k in BINADES:
         T, A, dt, x = _problem(k, B)
         means[k] = _mean(run(T, A, dt, x), x, T)
-    print({k: f"{m:.2e}" for k, m in means.items()})
     assert abs(sum(means.values())) / len(means) <= 2.0 ** -27
     for k, m in means.items():
         assert abs(m) <= (2.0 ** -27 if k <= -9 else 3 * 2.0 ** -27), (k, m)
