@@ -143,3 +143,50 @@ def test_backward_with_states_takes_no_room_for_them():
     (own, a), (given, b) = peak(None), peak(st)
     assert given <= own - 4 * st.numel() + (1 << 20)
     assert all(torch.equal(a[k], b[k]) for k in a if a[k] is not None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,B,D,N,G", [(torch.bfloat16, 3, 64, 16, 1), (torch.float32, 2, 20, 8, 2),
+                                           (torch.bfloat16, 5, 13, 4, 1)])
+def test_captured_generation_steps(dtype, B, D, N, G):
+    """One token through norm, convolution, scan step and gated norm, captured into a CUDA graph and
+    replayed token by token on states that move in place: the bits of the eager calls."""
+    g = torch.Generator().manual_seed(D)
+    r = lambda *s: torch.randn(*s, generator=g).cuda()
+    T, K = 6, 4
+    w, b, wc, A, w2 = r(D), r(D), r(D, K), -torch.rand(D, N, generator=g).cuda(), r(D)
+    xs, zs, bcs = r(T, B, 1, D).to(dtype), r(T, B, D).to(dtype), r(T, B, 2, G, N).to(dtype)
+    hist0, state0 = r(B, K - 1, D).to(dtype), r(B, D, N)
+    x, z, bc, hist, state = (torch.empty_like(v) for v in (xs[0], zs[0], bcs[0], hist0, state0))
+
+    def token():
+        n, _ = L.block_norm_fwd(x, w=w)
+        c = L.conv_step(hist, n[:, 0], wc, b)
+        y = L.scan_step(state, c, n[:, 0], A, bc[:, 0], bc[:, 1], Dskip=b, z=z, dt_bias=b)
+        return L.block_norm_fwd(y[:, None], w=w, z=z[:, None], r=x, w2=w2)
+
+    def run(step):
+        hist.copy_(hist0)
+        state.copy_(state0)
+        out = []
+        for t in range(T):
+            for dst, src in ((x, xs[t]), (z, zs[t]), (bc, bcs[t])):
+                dst.copy_(src)
+            out += [v.clone() for v in step()] + [hist.clone(), state.clone()]
+        return out
+
+    want = run(token)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        token()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = token()
+
+    def replay():
+        graph.replay()
+        return got
+
+    assert all(torch.equal(p, q) for p, q in zip(run(replay), want))
