@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 512 ? (VW == 1 ? 768 : 512) / MA
     auto has = [&](int k) { return there(row, k); };
     auto one = [&](int i, int k, const IO* q) {
       if constexpr (RING) {
-        if (has(k)) cp_async<16>(slot(st, i, k), q);
+        if (has(k)) cp_async16(slot(st, i, k), q);
       } else {
         in.v[i][k].load_if(q, has(k));
       }

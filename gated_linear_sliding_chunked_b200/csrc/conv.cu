@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvParams p) {
 
 template <typename IO, int K, int VW>
 __global__ void __launch_bounds__(NT) conv_step_kernel(ConvParams p, void* hist) {
+  static_assert(VW == 1 || VW * sizeof(IO) == 16, "the history is read an element or 16 bytes at a time");
   const int c = (blockIdx.x * NT + threadIdx.x) * VW;
   if (c >= p.D) return;
   float w[K * VW], bias[VW];
@@ -224,9 +225,9 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(ConvBwdParams q) 
     // s walks the tokens whose dp is formed; dx of token s - (K-1) is then
     // complete.  RT tokens at a time, the next ones' loads in flight.
     const int send = t1 + K - 1, slive = min(send, L);
-    // [t0 + RT, sin): whole chunks of this run's own tokens, all live, whose dx
-    // rows get nothing from the final history
-    const int sin = min(t1, q.dxT ? L : slive);
+    // [t0 + RT, sin): whole chunks of this run's own tokens, all live (s < L keeps
+    // t below L - (K-1), so that their dx rows get nothing from the final history)
+    const int sin = min(t1, L);
     const IO* px = (const IO*)p.px + p.x.at(b, t0) + c;
     const IO* pdy = (const IO*)q.dy + ((size_t)b * p.T + t0) * p.D + c;
     IO* pdx = (IO*)q.dx + ((int64_t)b * p.T + t0 - (K - 1)) * p.D + c;  // (used from token t0 on)

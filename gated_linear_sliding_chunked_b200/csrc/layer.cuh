@@ -46,7 +46,8 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// VW consecutive elements as floats (one 16- or 8-byte access, or one element)
+// VW consecutive elements as floats (one access: vectors of 4, or of 8 16-bit
+// elements to store)
 template <int VW>
 __device__ __forceinline__ void load_vec(const float* p, float* x) {
   if constexpr (VW == 4) {
@@ -58,15 +59,8 @@ __device__ __forceinline__ void load_vec(const float* p, float* x) {
 }
 template <int VW>
 __device__ __forceinline__ void load_vec(const bf16* p, float* x) {
-  if constexpr (VW == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(q[e] << 16);
-      x[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
-    }
-  } else if constexpr (VW == 4) {
+  static_assert(VW == 4 || VW == 1, "vectors of 4 or single elements");
+  if constexpr (VW == 4) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
     x[0] = __uint_as_float(u.x << 16);
     x[1] = __uint_as_float(u.x & 0xffff0000u);
@@ -113,14 +107,10 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// 16 or 8 bytes to shared memory without waiting
-template <int BYTES>
-__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+// 16 bytes to shared memory without waiting
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -218,13 +208,9 @@ struct Raw {
     else zero();
   }
   __device__ __forceinline__ void load_shared(const void* p) {
-    if constexpr (W == 4) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p);
-      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else if constexpr (W == 2) {
-      const uint2 x = *reinterpret_cast<const uint2*>(p);
-      w[0] = x.x; w[1] = x.y;
-    }
+    static_assert(W == 4, "16 bytes");
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
   }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);

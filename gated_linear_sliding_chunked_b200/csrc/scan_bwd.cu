@@ -621,11 +621,7 @@ cudaError_t go_any(const ScanParams& p, cudaStream_t s) {
 }  // namespace
 }  // namespace scan
 
-cudaError_t launch_scan_bwd(const scan::ScanParams& p0, bool bf, cudaStream_t s) {
-  scan::ScanParams p = p0;
-  // gradients are contiguous: vectors of 4 need whole rows of them
-  const size_t es = bf ? 2 : 4;
-  p.vec = p.vec && rows_vec(p.dy, Rows{p.D, 0}, (int)(16 / es), es);
+cudaError_t launch_scan_bwd(const scan::ScanParams& p, bool bf, cudaStream_t s) {
   return bf ? scan::go_any<bf16>(p, s) : scan::go_any<float>(p, s);
 }
 
