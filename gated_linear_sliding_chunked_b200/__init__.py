@@ -658,9 +658,13 @@ def _need(ok, fn, what):
         raise ValueError(f"{fn}: {what}")
 
 
+_INT = 1 << 31
+
+
 def _sizes(fn, *sizes):
-    """Sizes that the library takes as C ints."""
-    if max(sizes) >= 1 << 31:
+    """Sizes that the library takes as C ints; called for tensors of as many
+    elements (single-token calls are a few microseconds)."""
+    if max(sizes) >= _INT:
         raise ValueError(f"{fn}: sizes must be below 2^31, got {sizes}")
 
 
@@ -748,7 +752,8 @@ def conv_fwd(x, w, bias=None, x0=None, *, silu=True, lens=None, want_xT=False, s
     fn, dev = "conv_fwd", x.device
     _need(x.dim() == 3 and w.dim() == 2, fn, "x must be [B, T, D] and w [D, K]")
     (B, T, D), K = x.shape, w.shape[1]
-    _sizes(fn, B, T, D, K)
+    if x.numel() >= _INT or w.numel() >= _INT:
+        _sizes(fn, B, T, D, K)
     d = LzConvDims(B, T, D, K, io_of(x.dtype), int(bool(silu)),
                    _rows(fn, "x", x, x.shape, x.dtype, dev))
     _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
@@ -767,7 +772,8 @@ def conv_bwd(x, w, dy, bias=None, x0=None, dxT=None, *, silu=True, lens=None, wa
     fn, dev = "conv_bwd", x.device
     _need(x.dim() == 3 and w.dim() == 2, fn, "x must be [B, T, D] and w [D, K]")
     (B, T, D), K = x.shape, w.shape[1]
-    _sizes(fn, B, T, D, K)
+    if x.numel() >= _INT or w.numel() >= _INT:
+        _sizes(fn, B, T, D, K)
     d = LzConvDims(B, T, D, K, io_of(x.dtype), int(bool(silu)),
                    _rows(fn, "x", x, x.shape, x.dtype, dev))
     _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
@@ -791,7 +797,8 @@ def conv_step(hist, x, w, bias=None, *, silu=True, y=None, stream=None):
     fn, dev = "conv_step", x.device
     _need(x.dim() == 2 and w.dim() == 2, fn, "x must be [B, D] and w [D, K]")
     (B, D), K = x.shape, w.shape[1]
-    _sizes(fn, B, D, K)
+    if x.numel() >= _INT or w.numel() >= _INT:
+        _sizes(fn, B, D, K)
     d = LzConvDims(B, 1, D, K, io_of(x.dtype), int(bool(silu)),
                    _rows(fn, "x", x, (B, D), x.dtype, dev, 1))
     _whole(fn, dev, ("w", w, (D, K), torch.float32), ("bias", bias, (D,), torch.float32),
@@ -812,7 +819,8 @@ def _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, lead=2):
     _need(len(bs) in (lead + 1, lead + 2), fn, "Bm must be [.., N] or [.., G, N]")
     dev, dtype, D, N = u.device, u.dtype, us[-1], A.shape[1]
     G = bs[lead] if len(bs) == lead + 2 else 1
-    _sizes(fn, *us, G, N)
+    if u.numel() >= _INT or A.numel() >= _INT or Bm.numel() >= _INT:
+        _sizes(fn, *us, G, N)
     bc = us[:lead] + ((G, N) if len(bs) == lead + 2 else (N,))
     _whole(fn, dev, ("A", A, (D, N), torch.float32), ("Dskip", Dskip, (D,), torch.float32),
            ("dt_bias", dt_bias, (D,), torch.float32))
@@ -908,7 +916,8 @@ def _norm_args(fn, o, z, r, groups, eps):
     else:
         B, T, D = o.shape
     dev, dtype = o.device, o.dtype
-    _sizes(fn, B, T, D, groups)
+    if o.numel() >= _INT or groups >= _INT:
+        _sizes(fn, B, T, D, groups)
     if heads:
         _whole(fn, dev, ("o", o, o.shape, dtype))
     ro = _CONT if heads else _rows(fn, "o", o, o.shape, dtype, dev)

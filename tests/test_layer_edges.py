@@ -100,7 +100,7 @@ def test_sizes_beyond_32_bits_are_refused():
              lambda: L.scan_fwd(x, x, e(1, 4), e(1, big, 4), e(1, big, 4)),
              lambda: L.scan_bwd(x, x, e(1, 4), e(1, big, 4), e(1, big, 4), x),
              lambda: L.scan_step(e(big, 1, 4), e(big, 1), e(big, 1), e(1, 4), e(big, 4), e(big, 4)),
-             lambda: L.block_norm_fwd(x, w=e(1)), lambda: L.block_norm_bwd(x, w=e(1), dout=x),
+             lambda: L.block_norm_fwd(e(1, 1, 8), w=e(8), groups=2 ** 32 + 1), lambda: L.block_norm_fwd(x, w=e(1)), lambda: L.block_norm_bwd(x, w=e(1), dout=x),
              lambda: L.block_norm_fwd(e(1, 2 ** 16, 1, 2 ** 16), w=e(2 ** 32))]
     for call in calls:
         with pytest.raises(ValueError, match="2\\^31"):
