@@ -587,6 +587,11 @@ def qkg_projection(x, Wq=None, Wk=None, Wg=None, *, heads, gate_scale=1.0, strea
 
 
 # ---- layer operators: short convolution, selective scan, block norms --------
+# What a helper's docstring does not call strided must be contiguous and start on
+# a 16-byte boundary: a fresh tensor does, one of several slices of a batch need
+# not (`dy[1:2]` of an odd-sized batch: clone it), and is refused.  With `stream`,
+# a call behaves as under torch.cuda.stream(stream): its outputs belong to that
+# stream, which another one waits for, and records, before it uses them.
 def lz_layer_workspace_bytes(dims, which: int) -> int:
     return int(load().lz_layer_workspace_bytes(ctypes.byref(dims), which))
 
@@ -745,10 +750,11 @@ def _stream_on(dev, stream):
 
 def conv_fwd(x, w, bias=None, x0=None, *, silu=True, lens=None, want_xT=False, stream=None):
     """Short causal convolution (see lz_conv_fwd): x [B, T, D] (rows may be
-    strided), w [D, K] and bias [D] fp32, x0 [B, K-1, D] the history in front,
-    lens an int64 tensor [B] of the sequences' lengths in a right-padded batch.
-    Returns (y, xT); xT (None unless wanted) is the history after the last
-    token, which conv_step or the next conv_fwd continues."""
+    strided; everything else is contiguous and starts on a 16-byte boundary), w
+    [D, K] and bias [D] fp32, x0 [B, K-1, D] the history in front, lens an int64
+    tensor [B] of the sequences' lengths in a right-padded batch.  Returns (y,
+    xT); xT (None unless wanted) is the history after the last token, which
+    conv_step or the next conv_fwd continues."""
     fn, dev = "conv_fwd", x.device
     _need(x.dim() == 3 and w.dim() == 2, fn, "x must be [B, T, D] and w [D, K]")
     (B, T, D), K = x.shape, w.shape[1]
@@ -835,10 +841,11 @@ def _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus, lead=2):
 def scan_fwd(u, dt, A, Bm, Cm, *, Dskip=None, z=None, dt_bias=None, softplus=True, h0=None,
              lens=None, want_hT=False, want_states=False, stream=None):
     """Selective state space scan (see lz_scan_fwd): u, dt, z [B, T, D], A [D, N]
-    fp32 (negative), Bm, Cm [B, T, N] or [B, T, G, N] (rows may be strided),
-    Dskip, dt_bias [D] fp32, h0 [B, D, N] fp32, lens an int64 tensor [B] of the
-    sequences' lengths in a right-padded batch.  Returns (y, hT), or (y, hT,
-    states) with want_states; `states` is for scan_bwd."""
+    fp32 (negative), Bm, Cm [B, T, N] or [B, T, G, N] (rows of u, dt, z, Bm, Cm
+    may be strided; everything else is contiguous and starts on a 16-byte
+    boundary), Dskip, dt_bias [D] fp32, h0 [B, D, N] fp32, lens an int64 tensor
+    [B] of the sequences' lengths in a right-padded batch.  Returns (y, hT), or
+    (y, hT, states) with want_states; `states` is for scan_bwd."""
     fn, dev = "scan_fwd", u.device
     d = _scan_args(fn, u, dt, A, Bm, Cm, Dskip, z, dt_bias, softplus)
     B, T, D = u.shape
@@ -932,7 +939,8 @@ def block_norm_fwd(o, *, w=None, z=None, s=None, r=None, w2=None, groups=1, eps=
     of `groups` runs of features of o times w (o itself without w), n =
     rmsnorm(out) * w2.  o [B, T, D] (rows may be strided, as z's and r's), or
     the attention's [B, H, T, d], normed a head and laid out as rows.  w, s, w2
-    [D] fp32.  Returns (out, n); n is None without w2."""
+    [D] fp32; what is not strided starts on a 16-byte boundary.  Returns (out,
+    n); n is None without w2."""
     fn, dev = "block_norm_fwd", o.device
     d = _norm_args(fn, o, z, r, groups, eps)
     par = (d.D,)

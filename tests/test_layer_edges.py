@@ -190,3 +190,20 @@ def test_captured_generation_steps(dtype, B, D, N, G):
         return got
 
     assert all(torch.equal(p, q) for p, q in zip(run(replay), want))
+
+
+@pytest.mark.gpu
+def test_slices_off_a_16_byte_boundary_are_refused():
+    """One sequence of an odd-sized batch is contiguous and still not where vectors can be stored or
+    loaded: the library refuses it; as a strided input it is read."""
+    T, D, N = 3, 5, 4
+    x, w, o = torch.zeros(2, T, D, device="cuda"), torch.zeros(D, 2, device="cuda"), torch.ones(D, device="cuda")
+    bc, A = torch.zeros(1, T, N, device="cuda"), -torch.ones(D, N, device="cuda")
+    for call in (lambda v: L.conv_bwd(x[:1], w, v), lambda v: L.scan_bwd(x[:1], x[:1], A, bc, bc, v),
+                 lambda v: L.block_norm_bwd(x[:1], w=o, dout=v)):
+        with pytest.raises(L.LzError, match="16-byte aligned"):
+            call(x[1:])
+        call(x[1:].clone())
+    L.conv_fwd(x[1:], w)
+    L.scan_fwd(x[1:], x[1:], A, bc, bc)
+    L.block_norm_fwd(x[1:], w=o)
