@@ -81,7 +81,7 @@ constexpr int TB = kCk;  // tokens of a tile
 // The parameter gradients are summed over this many tiles at a time: thousands
 // of tokens added to one 32-bit sum would cost it bits.  (At 2 x 8192 tokens the
 // gradients of Dskip and dt_bias are off by 1.6e-7 and 4.1e-7, with one sum a
-// thread by 4.1e-7 and 6.4e-7, for 0.7 % of the time; equal terms by 2^-24 for
+// thread by 4.1e-7 and 6.4e-7, for 0.7 % of the time (8 states: 1.7 %); equal terms by 2^-24 for
 // every token that a thread adds up.)
 constexpr int kSum = 16;
 
@@ -268,11 +268,13 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
     Pack<IO, 4> nb[BN], ncv[BN];
     Tok tok[2][PASS];
     float Ds[EV], bias[EV], sD[EV], sT[EV];  // (sums of up to kSum tiles, added to sm.sum)
+    const bool many = !END && ntile >= kSum;
 #pragma unroll
     for (int e = 0; e < EV; ++e) {
       Ds[e] = p.Dskip && e < nc ? p.Dskip[c + e] : 0.f;
       bias[e] = p.dtb && e < nc ? p.dtb[c + e] : 0.f;
-      sD[e] = sT[e] = sm.sum[0][e][et] = sm.sum[1][e][et] = 0.f;
+      sD[e] = sT[e] = 0.f;
+      if (many) sm.sum[0][e][et] = sm.sum[1][e][et] = 0.f;
     }
     auto flush = [&] {  // (a thread's own words)
 #pragma unroll
@@ -458,14 +460,20 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
       step(k, tok[1]);
       if (k + 1 < ntile) step(k + 1, tok[0]);
       if constexpr (!END)
-        if (k % kSum == kSum - 2) flush();
+        if (many && k % kSum == kSum - 2) flush();
     }
     if constexpr (!END) {
       if (ntile > 0) {
         if (ntile & 1) finish(ntile - 1, tok[0]);
         else finish(ntile - 1, tok[1]);
       }
-      flush();
+      if (many) {
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+          sD[e] += sm.sum[0][e][et];
+          sT[e] += sm.sum[1][e][et];
+        }
+      }
       // sums of e u and ddt over the block's token rows, in order
       float* s1 = &sm.red[0][0][0][0];
       float* s2 = &sm.gB[0][0];
@@ -473,8 +481,8 @@ __global__ void __launch_bounds__(64 * W, L >= 8 && W == 4 ? 2 : 1) scan_bwd_ker
       asm volatile("bar.sync 1, %0;" ::"n"(NE) : "memory");
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
-        s1[i0 * CH + cl + e] = sm.sum[0][e][et];
-        s2[i0 * CH + cl + e] = sm.sum[1][e][et];
+        s1[i0 * CH + cl + e] = sD[e];
+        s2[i0 * CH + cl + e] = sT[e];
       }
       asm volatile("bar.sync 1, %0;" ::"n"(NE) : "memory");
       for (int x = et; x < CH; x += NE)
