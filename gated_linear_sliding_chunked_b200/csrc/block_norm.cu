@@ -12,7 +12,10 @@
 // At 2 x 8192 rows of 4096 (bf16): forward by 32 heads with a gate 76 to 80 us
 // (77 % of the copy bandwidth), backward of everything 246 to 254 us (66 %: two
 // sums over a row, with a barrier each, between its loads and its stores); rows
-// of 1024: backward 68 us (60 %).
+// of 1024: backward 68 us (60 %).  Rows too long for the backward's ring (above 5120
+// 32-bit features, 8192 16-bit ones, or 4096 where vectors are single elements) run
+// on blocks of up to 1024 threads, whose 64 registers spill: 4096 x 8192 in 32 bits
+// 484 us against a floor of 164, 4096 x 16384 in 16 bits 661 us.
 #include "layer.cuh"
 
 namespace lz {

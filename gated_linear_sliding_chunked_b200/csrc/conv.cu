@@ -7,8 +7,8 @@
 // inputs in registers, so that a token is read once and only the K-1 tokens
 // before a run are read twice (they come out of L2).  At 2 x 8192 tokens, 4096
 // channels, 4 taps (bf16) the backward takes 98 us: 62 % of the copy
-// bandwidth; its 24 instructions an element and few resident warps (163
-// registers) hold it there.  The forward takes 59 us (69 %).
+// bandwidth; its 26 instructions an element (counted) and few resident warps
+// (166 registers) hold it there.  The forward takes 59 us (69 %).
 #include <type_traits>
 
 #include "layer.cuh"

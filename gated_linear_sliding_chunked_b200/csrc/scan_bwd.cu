@@ -16,10 +16,11 @@
 // kernel, in a fixed order.
 //
 // Per (token, 4 states of a channel) about 123 instructions, 99 of them the
-// scan warps': bound by the issue slots.  At 2 x 8192 tokens, 4096 channels, 16
-// states (bf16, gated) 1545 us, 56 % of the issue slots on average (a seventh
-// of the schedulers have one scan warp, the others two); its bytes would take
-// 184 us.
+// scan warps', and 14 warps of 128 registers an SM to issue them.  At 2 x 8192
+// tokens, 4096 channels, 16 states (bf16, gated) 1556 to 1574 us, 56 % of the
+// issue slots on average (a seventh of the schedulers have one scan warp, the
+// others two); what its warps wait for most is the barrier after every tile (1.6
+// cycles an instruction).  Its bytes would take 184 us, its exps 480 us.
 #include "scan.cuh"
 
 namespace lz {
@@ -81,8 +82,8 @@ constexpr int TB = kCk;  // tokens of a tile
 // The parameter gradients are summed over this many tiles at a time: thousands
 // of tokens added to one 32-bit sum would cost it bits.  (At 2 x 8192 tokens the
 // gradients of Dskip and dt_bias are off by 1.6e-7 and 4.1e-7, with one sum a
-// thread by 4.1e-7 and 6.4e-7, for 0.7 % of the time (8 states: 1.7 %); equal terms by 2^-24 for
-// every token that a thread adds up.)
+// thread by 4.1e-7 and 6.4e-7, for 0.7 % of the time, 1.7 % with 8 states; equal
+// terms by 2^-24 for every token that a thread adds up.)
 constexpr int kSum = 16;
 
 template <typename IO, int L, int W>

@@ -1,10 +1,11 @@
 // Selective state space scan, forward and single tokens.
 //
 // Per (token, channel, state): one exp (16 a cycle and SM) and some 10 more
-// instructions with everything counted, against 8 bytes a (token, channel):
-// bound by the special-function unit and the issue slots.  At 2 x 8192 tokens,
-// 4096 channels, 16 states (bf16, gated) 515 to 537 us: 54 to 56 % of the
-// special-function rate, 61 % of the issue slots; its bytes would take 82 us.
+// instructions with everything counted, against 8 bytes a (token, channel): its
+// floor is the special-function unit's.  At 2 x 8192 tokens, 4096 channels, 16
+// states (bf16, gated) 506 to 537 us: 54 to 57 % of the special-function rate, 62 %
+// of the issue slots, neither of them full; its warps wait at the barrier after
+// every tile as long as for an issue slot.  Its bytes would take 82 us.
 #include "scan.cuh"
 
 namespace lz {
